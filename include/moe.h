@@ -78,6 +78,7 @@ extern "C" {
 #define MOE_OP_COMBINE 4
 #define MOE_OP_ROUTE_BACKWARD 5
 #define MOE_OP_EXPERT_FFN_BACKWARD 6
+#define MOE_OP_LAYER_NORM_BACKWARD 7  /* uses the shape's T (rows) and d */
 
 /* tokens per row of the block histogram written by moe_route */
 #define MOE_ROUTE_BLOCK 64
@@ -432,6 +433,16 @@ int moe_route_backward(const moe_shape* shape, const void* x, int x_dtype, const
                        size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * moe_route_backward_add - moe_route_backward with other gradients of the
+ * logits at hand (moe_balance_loss_backward's): dlogits [T, E] holds them at
+ * entry, the gate path's are added, and dx and dw_gate take the sum.
+ */
+int moe_route_backward_add(const moe_shape* shape, const void* x, int x_dtype, const float* w_gate,
+                           const float* logit_offset, const float* logits, const int32_t* topk_idx,
+                           const float* d_topk_w, float* dlogits, float* dx, float* dw_gate, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/*
  * moe_route_hash - hash router (mastering-deepseek-v4 "MoE + Expert-Parallel
  * Overlap (Exp08)", Implemented: a hash router emulates the early layers; a
  * token's experts follow from its token id).  Replaces moe_route; dispatch,
@@ -476,6 +487,144 @@ int moe_route_hash(const moe_shape* shape, const int32_t* token_ids, uint64_t se
  */
 int moe_bias_update(int64_t n_rows, int32_t E, const int32_t* counts, float gamma, float* bias,
                     int32_t* load, moe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------- training step
+ * What a training step needs around the layer: the norm in front of it, a
+ * balance loss on the router with its gradient, and the optimizer.
+ */
+
+/*
+ * moe_balance_loss - the router's balance loss and the per-expert counts, for
+ * n_seq sequences packed along the tokens.  With p[t,e] = a[t,e] / sum_e
+ * a[t,e], a = sqrt(softplus(logits + logit_offset)) (0 for a row whose
+ * affinities all vanish), and for sequence s its T_s counted tokens:
+ *     counts[s,e] = slots (t, j) of counted tokens with topk_idx[t,j] = e
+ *     f[s,e] = E counts[s,e] / (k T_s),   prob[s,e] = sum_t p[t,e] / T_s
+ *     loss = alpha / n_seq * sum_s sum_e f[s,e] prob[s,e]
+ *     dprob[s,e] = alpha f[s,e] / (n_seq T_s)  = d loss / d p[t,e] for t in s
+ * A sequence without a counted token adds 0 (its rows are 0).
+ *   shape        uses T, E, k (k <= E; E <= 1024, k <= 16)
+ *   logits       [T, E] fp32 as moe_route wrote them; logit_offset [E] or NULL
+ *   topk_idx     [T, k] int32; an index outside [0, E) is not counted
+ *   seq_offsets  [n_seq + 1] int32, non-decreasing: sequence s holds tokens
+ *                [seq_offsets[s], seq_offsets[s+1]); tokens outside all of them
+ *                are not counted.  NULL with n_seq = 1: all T tokens.
+ *                n_seq <= MOE_MAX_SEQUENCES
+ *   token_mask   [T] bytes, 0: the token is not counted (its logits and
+ *                indices may hold anything), or NULL
+ *   counts [n_seq, E] int32, prob, dprob [n_seq, E] fp32, loss [1] fp32: out,
+ *                written for every sequence, also with T = 0
+ *   ws           moe_balance_loss_workspace_size(shape, n_seq) bytes; nothing
+ *                in it needs to start at zero
+ * The sums run in a fixed order (deterministic), in fp32.
+ */
+#define MOE_MAX_SEQUENCES 65535
+size_t moe_balance_loss_workspace_size(const moe_shape* shape, int32_t n_seq);
+int moe_balance_loss(const moe_shape* shape, const float* logits, const float* logit_offset,
+                     const int32_t* topk_idx, const int32_t* seq_offsets, int32_t n_seq,
+                     const uint8_t* token_mask, float alpha, int32_t* counts, float* prob, float* dprob,
+                     float* loss, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_balance_loss_backward - the loss's gradient for the logits, the counts
+ * held fixed (they are piecewise constant):
+ *     dlogits[t,e] = d_extra[t,e] + grad_loss * (dprob[s,e] - sum_j dprob[s,j] p[t,j])
+ *                    / (sum_j a[t,j]) * sig(l) / (2 a[t,e])
+ * and d_extra alone for tokens that are not counted.  shape, logits,
+ * logit_offset, seq_offsets, n_seq, token_mask as moe_balance_loss's.
+ *   dprob      [n_seq, E] fp32 from moe_balance_loss
+ *   grad_loss  [1] fp32 device, or NULL: 1
+ *   d_extra    [T, E] fp32 or NULL: 0 (may be dlogits: the gradient is added)
+ *   dlogits    [T, E] fp32 out
+ */
+int moe_balance_loss_backward(const moe_shape* shape, const float* logits, const float* logit_offset,
+                              const int32_t* seq_offsets, int32_t n_seq, const uint8_t* token_mask,
+                              const float* dprob, const float* grad_loss, const float* d_extra, float* dlogits,
+                              moe_stream_t stream);
+
+/*
+ * moe_layer_norm - layer norm over rows of d, with the residual add in front:
+ *     s = x + residual (rounded to x_dtype; s = x without),  mu = sum(s) / d,
+ *     rstd = 1 / sqrt(sum((s - mu)^2) / d + eps),   y = (s - mu) rstd weight + bias
+ *   x, residual  [rows, d] in x_dtype (MOE_BF16 or MOE_F32); residual may be NULL
+ *   weight, bias [d] fp32; bias may be NULL
+ *   sum          [rows, d] in x_dtype out: s (with a residual, else NULL); may
+ *                be x or residual
+ *   y            [rows, d] in y_dtype (MOE_BF16 or MOE_F32) out
+ *   mean, rstd   [rows] fp32 out, both or neither (NULL)
+ * 1 <= d <= 32768, any element alignment; eps >= 0.  Statistics in fp32.
+ * rows = 0 is a no-op.
+ */
+int moe_layer_norm(int64_t rows, int32_t d, const void* x, const void* residual, int x_dtype,
+                   const float* weight, const float* bias, float eps, void* sum, void* y, int y_dtype,
+                   float* mean, float* rstd, moe_stream_t stream);
+
+/*
+ * moe_layer_norm_backward - with x the rows that were normalised (moe_layer_norm's
+ * sum, or its x), xh = (x - mean) rstd and q = dy weight:
+ *     dx = rstd (q - mean_d(q) - xh mean_d(q xh)) + d_sum
+ *     dweight = sum_rows dy xh,   dbias = sum_rows dy
+ *   dy       [rows, d] in dy_dtype;  x [rows, d] in x_dtype
+ *   d_sum    [rows, d] in x_dtype or NULL: the gradient that reaches the sum
+ *            past the norm; dx is then the gradient of both x and residual
+ *   dx       [rows, d] in dx_dtype out; may be dy or d_sum where the types agree
+ *   dweight, dbias [d] fp32 out (dbias may be NULL); zeros with rows = 0
+ *   ws       moe_workspace_size(MOE_OP_LAYER_NORM_BACKWARD, shape, 0) bytes
+ *            with the shape's T = rows: the parts of dweight and dbias
+ * Each type MOE_BF16 or MOE_F32; d as moe_layer_norm.  All sums in fp32 and in
+ * a fixed order (deterministic).
+ */
+int moe_layer_norm_backward(int64_t rows, int32_t d, const void* dy, int dy_dtype, const void* x, int x_dtype,
+                            const float* weight, const float* mean, const float* rstd, const void* d_sum,
+                            void* dx, int dx_dtype, float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/*
+ * moe_adamw_step - one AdamW step over many tensors, in place.  For each
+ * element, in fp32 with every operation rounded on its own:
+ *     g' = grad * grad_scale
+ *     m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) (g' g')
+ *     w = w (1 - lr weight_decay) - lr / (1 - beta1^step) * (m / (sqrt(v) / sqrt(1 - beta2^step) + eps))
+ * (the factors of lr, beta and step are formed in fp64 and rounded once).
+ *   tensors     host array, read during the call; tensors must not overlap.
+ *     n           elements (0: skipped); pointers need only element alignment
+ *     param       in param_dtype (MOE_F32 or MOE_BF16)
+ *     grad        in grad_dtype (MOE_F32 or MOE_BF16)
+ *     master      NULL: w is param.  With a bf16 param: the fp32 weights w;
+ *                 param is written as their rounded copy
+ *     state_dtype MOE_F32: m, v fp32.  MOE_E4M3: m and r = sqrt(v) as e4m3
+ *                 codes, element i's value code[i] * scale[i / MOE_FP8_TILE]
+ *                 with m_scale, v_scale [ceil(n / MOE_FP8_TILE)] fp32.  A
+ *                 tile's scale is the smallest power of two (at least 2^-100;
+ *                 1 for a tile of zeros) with amax <= 448 scale; codes are
+ *                 rounded to nearest even; a non-finite moment gets the NaN
+ *                 code and does not count for the scale.  All-zero codes with
+ *                 any finite scales are a fresh state.
+ *   params      host: lr >= 0, 0 <= beta < 1, eps > 0, step >= 1 (this step's
+ *               number, counted from 1).  They are passed by value: a
+ *               captured graph repeats the step it was captured with.
+ *   grad_scale  [1] fp32 device (a loss scale's inverse, a clipping factor), or
+ *               NULL: 1
+ */
+typedef struct moe_adamw_tensor {
+  int64_t n;
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  double weight_decay;
+  int32_t param_dtype, grad_dtype, state_dtype, reserved;
+} moe_adamw_tensor;
+typedef struct moe_adamw_params {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+} moe_adamw_params;
+int moe_adamw_step(int32_t n_tensors, const moe_adamw_tensor* tensors, const moe_adamw_params* params,
+                   const float* grad_scale, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -15,6 +15,10 @@ library is missing, or a tensor is not on the GPU, calls raise.
     combine_backward / expert_ffn_backward / dispatch_backward / route_backward
                                              the layer's backward, stage by stage
     MoELayer                                 weights + buffers, forward(x) = the four calls
+    layer_norm(x, weight, bias, residual)    -> y, sum, mean, rstd; layer_norm_backward -> dx, dw, db
+    balance_loss(shape, logits, idx, alpha)  -> loss, counts, prob, dprob; balance_loss_backward -> dlogits
+    AdamW                                    many tensors, 32-bit or 8-bit states; step() = one call
+    MoEBlock                                 norm + MoELayer + balance loss + AdamW: a training step
 """
 from __future__ import annotations
 
@@ -26,14 +30,16 @@ import torch
 from . import _lib
 from ._lib import (MOE_BF16, MOE_BWD_AU_SAVED, MOE_E4M3, MOE_F32, MOE_FFN_ALL, MOE_FFN_DOWN,  # noqa: F401
                    MOE_FFN_UP, MOE_FP8_TILE, MOE_OP_COMBINE, MOE_OP_DISPATCH, MOE_OP_EXPERT_FFN,
-                   MOE_OP_EXPERT_FFN_BACKWARD, MOE_OP_ROUTE, MOE_OP_ROUTE_BACKWARD, MOE_ROUTE_BLOCK,
+                   MOE_OP_EXPERT_FFN_BACKWARD, MOE_OP_LAYER_NORM_BACKWARD, MOE_OP_ROUTE,
+                   MOE_OP_ROUTE_BACKWARD, MOE_ROUTE_BLOCK,
                    MOE_ROUTE_LOGITS_IN, MoeError, MoeFfnExtra, MoeShape)
 
 __all__ = ["shape", "workspace_bytes", "workspace", "route", "route_hash", "dispatch", "dispatch_noalloc",
            "combine_backward",
            "expert_ffn_train",
            "expert_ffn_backward", "dispatch_backward", "route_backward", "expert_ffn", "combine",
-           "quantize_blocks_e4m3", "quantize_rows_e4m3", "bias_update", "MoELayer", "MoeError", "lib"]
+           "quantize_blocks_e4m3", "quantize_rows_e4m3", "bias_update", "MoELayer", "MoeError", "lib",
+           "layer_norm", "layer_norm_backward", "balance_loss", "balance_loss_backward", "AdamW", "MoEBlock"]
 
 
 def lib():
@@ -438,8 +444,12 @@ def dispatch_backward(sh: MoeShape, dest, d_xp, d_extra=None, dx=None, accumulat
 
 
 def route_backward(sh: MoeShape, x, w_gate, logits, idx, d_w, dx, logit_offset=None, dlogits=None,
-                   dw_gate=None, ws=None):
-    """Gate path: dlogits [T, E] (written), dx += dlogits W_g^T, dw_gate = x^T dlogits."""
+                   dw_gate=None, ws=None, add_dlogits: bool = False):
+    """Gate path: dlogits [T, E] (written), dx += dlogits W_g^T, dw_gate = x^T dlogits.
+    add_dlogits: dlogits holds other gradients of the logits (balance_loss_backward's)
+    and the gate's are added to them."""
+    if add_dlogits and dlogits is None:
+        raise ValueError("add_dlogits needs dlogits")
     T, E, d = sh.T, sh.E, sh.d
     dev = x.device
     if dlogits is None:
@@ -460,10 +470,10 @@ def route_backward(sh: MoeShape, x, w_gate, logits, idx, d_w, dx, logit_offset=N
     wsb = workspace_bytes(MOE_OP_ROUTE_BACKWARD, sh, _dt(x))
     if ws is None and wsb > 0:
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
-    st = lib().moe_route_backward(ctypes.byref(sh), _ptr(x), _dt(x), _ptr(w_gate), _ptr(logit_offset), _ptr(logits),
-                                  _ptr(idx), _ptr(d_w), _ptr(dlogits), _ptr(dx), _ptr(dw_gate), _ptr(ws),
-                                  _ws_len(ws), _stream())
-    _lib.check("moe_route_backward", st)
+    fn = lib().moe_route_backward_add if add_dlogits else lib().moe_route_backward
+    st = fn(ctypes.byref(sh), _ptr(x), _dt(x), _ptr(w_gate), _ptr(logit_offset), _ptr(logits), _ptr(idx), _ptr(d_w),
+            _ptr(dlogits), _ptr(dx), _ptr(dw_gate), _ptr(ws), _ws_len(ws), _stream())
+    _lib.check("moe_route_backward_add" if add_dlogits else "moe_route_backward", st)
     return dlogits, dw_gate
 
 
@@ -488,3 +498,5 @@ def bias_update(counts: torch.Tensor, bias: torch.Tensor, gamma: float,
 
 
 from .layer import MoELayer  # noqa: E402
+from .training import (AdamW, MoEBlock, balance_loss, balance_loss_backward, layer_norm,  # noqa: E402
+                       layer_norm_backward)

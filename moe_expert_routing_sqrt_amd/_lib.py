@@ -25,6 +25,8 @@ MOE_ROUTE_BLOCK = 64
 MOE_FP8_TILE = 128
 MOE_OP_ROUTE, MOE_OP_DISPATCH, MOE_OP_EXPERT_FFN, MOE_OP_COMBINE = 1, 2, 3, 4
 MOE_OP_ROUTE_BACKWARD, MOE_OP_EXPERT_FFN_BACKWARD = 5, 6
+MOE_OP_LAYER_NORM_BACKWARD = 7
+MOE_MAX_SEQUENCES = 65535
 
 
 class MoeShape(ctypes.Structure):
@@ -39,6 +41,20 @@ class MoeFfnExtra(ctypes.Structure):
                 ("w13", ctypes.c_void_p), ("w13_scale", ctypes.c_void_p), ("w2", ctypes.c_void_p),
                 ("w2_scale", ctypes.c_void_p), ("h", ctypes.c_void_p), ("h_scale", ctypes.c_void_p),
                 ("y", ctypes.c_void_p)]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    """moe_adamw_tensor: one tensor of an AdamW step, with its state."""
+    _fields_ = [("n", ctypes.c_int64), ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("weight_decay", ctypes.c_double),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class MoeAdamwParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -77,6 +93,16 @@ SIGNATURES = {
     "moe_dispatch_backward": (_INT, [ctypes.POINTER(MoeShape), _P, _P, _INT, _P, _P, _INT, _P]),
     "moe_route_backward": (_INT, [ctypes.POINTER(MoeShape), _P, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                   ctypes.c_size_t, _P]),
+    "moe_route_backward_add": (_INT, [ctypes.POINTER(MoeShape), _P, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                      _SZ, _P]),
+    "moe_balance_loss_workspace_size": (_SZ, [ctypes.POINTER(MoeShape), _I32]),
+    "moe_balance_loss": (_INT, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _I32, _P, _F32, _P, _P, _P, _P, _P, _SZ,
+                                _P]),
+    "moe_balance_loss_backward": (_INT, [ctypes.POINTER(MoeShape), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P]),
+    "moe_layer_norm": (_INT, [_I64, _I32, _P, _P, _INT, _P, _P, _F32, _P, _P, _INT, _P, _P, _P]),
+    "moe_layer_norm_backward": (_INT, [_I64, _I32, _P, _INT, _P, _INT, _P, _P, _P, _P, _P, _INT, _P, _P, _P, _SZ,
+                                       _P]),
+    "moe_adamw_step": (_INT, [_I32, ctypes.POINTER(MoeAdamwTensor), ctypes.POINTER(MoeAdamwParams), _P, _P]),
 }
 
 _lib = None

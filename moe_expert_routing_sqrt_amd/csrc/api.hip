@@ -514,10 +514,10 @@ int moe_dispatch_backward(const moe_shape* shape, const int32_t* dest, const voi
                                    MOE_F32, accumulate, as_stream(stream)));
 }
 
-int moe_route_backward(const moe_shape* shape, const void* x, int x_dtype, const float* w_gate,
-                       const float* logit_offset, const float* logits, const int32_t* topk_idx,
-                       const float* d_topk_w, float* dlogits, float* dx, float* dw_gate, void* ws,
-                       size_t ws_bytes, moe_stream_t stream) {
+static int route_backward(const moe_shape* shape, const void* x, int x_dtype, const float* w_gate,
+                          const float* logit_offset, const float* logits, const int32_t* topk_idx,
+                          const float* d_topk_w, float* dlogits, float* dx, float* dw_gate, void* ws,
+                          size_t ws_bytes, moe_stream_t stream, bool add_dlogits) {
   if (shape == nullptr || shape->T < 0 || shape->E < 1 || shape->k < 1 || shape->k > shape->E || shape->d < 1)
     return MOE_ERR_INVALID_ARG;
   if (x_dtype != MOE_F32 && x_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
@@ -530,7 +530,23 @@ int moe_route_backward(const moe_shape* shape, const void* x, int x_dtype, const
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned256(ws))) return MOE_ERR_WORKSPACE;
   return hip_status(launch_gate_bwd(shape->T, shape->d, shape->E, shape->k, x, x_dtype, w_gate, logits,
                                     logit_offset, topk_idx, d_topk_w, dlogits, dx, dw_gate,
-                                    static_cast<float*>(ws), as_stream(stream)));
+                                    static_cast<float*>(ws), as_stream(stream), add_dlogits));
+}
+
+int moe_route_backward(const moe_shape* shape, const void* x, int x_dtype, const float* w_gate,
+                       const float* logit_offset, const float* logits, const int32_t* topk_idx,
+                       const float* d_topk_w, float* dlogits, float* dx, float* dw_gate, void* ws,
+                       size_t ws_bytes, moe_stream_t stream) {
+  return route_backward(shape, x, x_dtype, w_gate, logit_offset, logits, topk_idx, d_topk_w, dlogits, dx, dw_gate,
+                        ws, ws_bytes, stream, false);
+}
+
+int moe_route_backward_add(const moe_shape* shape, const void* x, int x_dtype, const float* w_gate,
+                           const float* logit_offset, const float* logits, const int32_t* topk_idx,
+                           const float* d_topk_w, float* dlogits, float* dx, float* dw_gate, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  return route_backward(shape, x, x_dtype, w_gate, logit_offset, logits, topk_idx, d_topk_w, dlogits, dx, dw_gate,
+                        ws, ws_bytes, stream, true);
 }
 
 int moe_route_hash(const moe_shape* shape, const int32_t* token_ids, uint64_t seed,
@@ -554,6 +570,109 @@ int moe_bias_update(int64_t n_rows, int32_t E, const int32_t* counts, float gamm
   return hip_status(launch_bias_update(n_rows, E, counts, gamma, bias, load, as_stream(stream)));
 }
 
+static bool is_float(int t) { return t == MOE_F32 || t == MOE_BF16; }
+
+// T, E and k of a balance loss, and its sequences
+static int balance_check(const moe_shape* s, int32_t n_seq, const int32_t* seq_offsets) {
+  if (s == nullptr || s->T < 0 || s->E < 1 || s->k < 1 || s->k > s->E || n_seq < 1) return MOE_ERR_INVALID_ARG;
+  if (seq_offsets == nullptr && n_seq != 1) return MOE_ERR_INVALID_ARG;
+  if (s->E > kMaxExperts || s->k > 16 || n_seq > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
+  if (s->T > (int64_t)INT32_MAX / s->k) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_balance_loss_workspace_size(const moe_shape* shape, int32_t n_seq) {
+  if (balance_check(shape, n_seq, reinterpret_cast<const int32_t*>(1)) != MOE_OK) return 0;
+  return balance_loss_workspace_bytes(shape->T, shape->E, n_seq);
+}
+
+int moe_balance_loss(const moe_shape* shape, const float* logits, const float* logit_offset,
+                     const int32_t* topk_idx, const int32_t* seq_offsets, int32_t n_seq,
+                     const uint8_t* token_mask, float alpha, int32_t* counts, float* prob, float* dprob,
+                     float* loss, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const int st = balance_check(shape, n_seq, seq_offsets);
+  if (st != MOE_OK) return st;
+  if (!std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
+  if (shape->T > 0 && (logits == nullptr || topk_idx == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (counts == nullptr || prob == nullptr || dprob == nullptr || loss == nullptr) return MOE_ERR_INVALID_ARG;
+  if (ws == nullptr || ws_bytes < balance_loss_workspace_bytes(shape->T, shape->E, n_seq) || !aligned256(ws))
+    return MOE_ERR_WORKSPACE;
+  return hip_status(launch_balance_loss(shape->T, shape->E, shape->k, logits, logit_offset, topk_idx, seq_offsets,
+                                        n_seq, token_mask, alpha, counts, prob, dprob, loss, ws,
+                                        as_stream(stream)));
+}
+
+int moe_balance_loss_backward(const moe_shape* shape, const float* logits, const float* logit_offset,
+                              const int32_t* seq_offsets, int32_t n_seq, const uint8_t* token_mask,
+                              const float* dprob, const float* grad_loss, const float* d_extra, float* dlogits,
+                              moe_stream_t stream) {
+  const int st = balance_check(shape, n_seq, seq_offsets);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  if (logits == nullptr || dprob == nullptr || dlogits == nullptr) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_balance_loss_bwd(shape->T, shape->E, logits, logit_offset, seq_offsets, n_seq, token_mask,
+                                            dprob, grad_loss, d_extra, dlogits, as_stream(stream)));
+}
+
+static int norm_check(int64_t rows, int32_t d) {
+  if (rows < 0 || d < 1) return MOE_ERR_INVALID_ARG;
+  if (d > kMaxNormWidth || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int moe_layer_norm(int64_t rows, int32_t d, const void* x, const void* residual, int x_dtype,
+                   const float* weight, const float* bias, float eps, void* sum, void* y, int y_dtype,
+                   float* mean, float* rstd, moe_stream_t stream) {
+  if (!is_float(x_dtype) || !is_float(y_dtype) || !(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  const int st = norm_check(rows, d);
+  if (st != MOE_OK) return st;
+  if ((residual == nullptr) != (sum == nullptr) || (mean == nullptr) != (rstd == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || weight == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_layer_norm(rows, d, x, residual, x_dtype, weight, bias, eps, sum, y, y_dtype, mean, rstd,
+                                      as_stream(stream)));
+}
+
+int moe_layer_norm_backward(int64_t rows, int32_t d, const void* dy, int dy_dtype, const void* x, int x_dtype,
+                            const float* weight, const float* mean, const float* rstd, const void* d_sum,
+                            void* dx, int dx_dtype, float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                            moe_stream_t stream) {
+  if (!is_float(dy_dtype) || !is_float(x_dtype) || !is_float(dx_dtype)) return MOE_ERR_INVALID_ARG;
+  const int st = norm_check(rows, d);
+  if (st != MOE_OK) return st;
+  if (dweight == nullptr) return MOE_ERR_INVALID_ARG;
+  if (rows > 0) {
+    if (dy == nullptr || x == nullptr || weight == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr)
+      return MOE_ERR_INVALID_ARG;
+    if (ws == nullptr || ws_bytes < layer_norm_bwd_workspace_bytes(rows, d) || !aligned256(ws))
+      return MOE_ERR_WORKSPACE;
+  }
+  return hip_status(launch_layer_norm_bwd(rows, d, dy, dy_dtype, x, x_dtype, weight, mean, rstd, d_sum, dx, dx_dtype,
+                                          dweight, dbias, static_cast<float*>(ws), as_stream(stream)));
+}
+
+int moe_adamw_step(int32_t n_tensors, const moe_adamw_tensor* tensors, const moe_adamw_params* params,
+                   const float* grad_scale, moe_stream_t stream) {
+  if (n_tensors < 0 || params == nullptr || (n_tensors > 0 && tensors == nullptr)) return MOE_ERR_INVALID_ARG;
+  const moe_adamw_params& h = *params;
+  if (!std::isfinite(h.lr) || h.lr < 0.0 || !(h.beta1 >= 0.0 && h.beta1 < 1.0) ||
+      !(h.beta2 >= 0.0 && h.beta2 < 1.0) || !std::isfinite(h.eps) || !(static_cast<float>(h.eps) > 0.0f) ||
+      h.step < 1)
+    return MOE_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || !is_float(t.param_dtype) || !is_float(t.grad_dtype) || !std::isfinite(t.weight_decay))
+      return MOE_ERR_INVALID_ARG;
+    if (t.state_dtype != MOE_F32 && t.state_dtype != MOE_E4M3) return MOE_ERR_INVALID_ARG;
+    if (t.master != nullptr && t.param_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (t.param == nullptr || t.grad == nullptr || t.m == nullptr || t.v == nullptr) return MOE_ERR_INVALID_ARG;
+    if (t.state_dtype == MOE_E4M3 && (t.m_scale == nullptr || t.v_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (t.n > (int64_t{1} << 40)) return MOE_ERR_UNSUPPORTED;
+  }
+  return hip_status(launch_adamw(n_tensors, tensors, h, grad_scale, as_stream(stream)));
+}
+
 size_t moe_workspace_size(int op, const moe_shape* shape, int dtype) {
   switch (op) {
     case MOE_OP_ROUTE:
@@ -571,6 +690,9 @@ size_t moe_workspace_size(int op, const moe_shape* shape, int dtype) {
       return gate_bwd_workspace_bytes(shape->T, shape->d, shape->E);
     case MOE_OP_EXPERT_FFN_BACKWARD:
       return kTicketSetBytes;
+    case MOE_OP_LAYER_NORM_BACKWARD:
+      if (shape == nullptr || norm_check(shape->T, shape->d) != MOE_OK) return 0;
+      return layer_norm_bwd_workspace_bytes(shape->T, shape->d);
     default:
       return 0;
   }

@@ -138,10 +138,11 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(const int32_t* rows_dev
 
 // ---------------------------------------------------------------- gate backward
 // One wave per token: lanes j < k derive dl_j from the token's logits and slot
-// gradients; every lane then writes its share of the dense dL row once.
+// gradients; every lane then writes its share of the dense dL row once (add:
+// onto what the row holds).
 __global__ __launch_bounds__(256) void gate_bwd_kernel(int64_t T, int E, int k, const float* logits,
                                                        const float* offset, const int32_t* idx,
-                                                       const float* d_w, float* dL) {
+                                                       const float* d_w, float* dL, bool add) {
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(int64_t T, int E, int k, 
 #pragma unroll
     for (int j = 0; j < kMaxK; ++j)
       if (j < k && ej[j] == c) v = dj[j];
-    dL[t * E + c] = v;
+    dL[t * E + c] = add ? dL[t * E + c] + v : v;
   }
 }
 
@@ -417,9 +418,9 @@ size_t gate_bwd_workspace_bytes(int64_t T, int d, int E) {
 
 hipError_t launch_gate_bwd(int64_t T, int d, int E, int k, const void* x, int x_dtype, const float* w_gate,
                            const float* logits, const float* offset, const int32_t* idx, const float* d_w,
-                           float* dL, float* dx, float* dw_gate, float* ws, hipStream_t s) {
+                           float* dL, float* dx, float* dw_gate, float* ws, hipStream_t s, bool add_dl) {
   hipLaunchKernelGGL(gate_bwd_kernel, dim3(static_cast<unsigned>((T + 3) / 4)), dim3(256), 0, s, T, E, k,
-                     logits, offset, idx, d_w, dL);
+                     logits, offset, idx, d_w, dL, add_dl);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (gate_bwd_mfma(d, E, x_dtype)) {

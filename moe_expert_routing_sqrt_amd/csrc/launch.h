@@ -124,10 +124,34 @@ int gate_bwd_splits(int64_t T);
 size_t gate_bwd_workspace_bytes(int64_t T, int d, int E);
 hipError_t launch_gate_bwd(int64_t T, int d, int E, int k, const void* x, int x_dtype, const float* w_gate,
                            const float* logits, const float* offset, const int32_t* idx, const float* d_w,
-                           float* dL, float* dx, float* dw_gate, float* ws, hipStream_t s);
+                           float* dL, float* dx, float* dw_gate, float* ws, hipStream_t s, bool add_dl = false);
 
 // load balancing
 hipError_t launch_bias_update(int64_t n_rows, int E, const int32_t* counts, float gamma, float* bias,
                               int32_t* load, hipStream_t s);
+
+// balance loss (balance_loss.hip); seq: n_seq + 1 offsets or nullptr (one
+// sequence); mask, offset, grad, extra: nullptr for none
+size_t balance_loss_workspace_bytes(int64_t T, int E, int n_seq);
+hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, const float* offset, const int32_t* idx,
+                               const int32_t* seq, int n_seq, const uint8_t* mask, float alpha, int32_t* counts,
+                               float* prob, float* dprob, float* loss, void* ws, hipStream_t s);
+hipError_t launch_balance_loss_bwd(int64_t T, int E, const float* logits, const float* offset, const int32_t* seq,
+                                   int n_seq, const uint8_t* mask, const float* dprob, const float* grad,
+                                   const float* extra, float* dl, hipStream_t s);
+
+// layer norm (norm.hip); r / ds: the residual and its gradient or nullptr
+constexpr int kMaxNormWidth = 32768;
+hipError_t launch_layer_norm(int64_t rows, int d, const void* x, const void* r, int x_dtype, const float* w,
+                             const float* b, float eps, void* sum, void* y, int y_dtype, float* mean, float* rstd,
+                             hipStream_t s);
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int d);
+hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dtype, const void* x, int x_dtype,
+                                 const float* w, const float* mean, const float* rstd, const void* ds, void* dx,
+                                 int dx_dtype, float* dw, float* db, float* ws, hipStream_t s);
+
+// optimizer (adamw.hip); t: host array
+hipError_t launch_adamw(int n_tensors, const moe_adamw_tensor* t, const moe_adamw_params& h, const float* grad_scale,
+                        hipStream_t s);
 
 }  // namespace moe

@@ -206,13 +206,15 @@ class MoELayer:
         return self.out
 
     def backward(self, x: torch.Tensor, grad_out: torch.Tensor,
-                 marks: Optional[Sequence[torch.cuda.Event]] = None) -> dict:
+                 marks: Optional[Sequence[torch.cuda.Event]] = None, add_dlogits: bool = False) -> dict:
         """Gradients of the last forward(x) for grad_out = d loss / d out (bf16
         [T, d]): dx [T, d] fp32, dw_gate [d, E] fp32, dw13 / dw2 of the routed
         experts and dsh_w13 / dsh_w2 of the shared expert (fp32).  The expert
         selection of the forward is held fixed; the routing bias gets no
         gradient.  `marks`: optional 5 events around the four stages
-        (combine, routed experts, shared expert, dispatch + gate)."""
+        (combine, routed experts, shared expert, dispatch + gate).
+        add_dlogits: the layer's dlogits buffer holds other gradients of the
+        router's logits (a balance loss's), which dx and dw_gate then include."""
         if self.dtype != MOE_BF16 or self.local or self.router != "topk":
             raise ValueError("backward covers the bf16 top-k layer with all experts local")
         if grad_out.dtype != torch.bfloat16:
@@ -240,7 +242,7 @@ class MoELayer:
         dispatch_backward(sh, b["dest"], r["d_xp"], d_extra=sx, dx=w["dx"])
         route_backward(sh, x, self.w_gate, self.logits, self.idx, w["d_w"], w["dx"],
                        logit_offset=self.logit_offset, dlogits=w["dlogits"], dw_gate=w["dw_gate"],
-                       ws=w["gate_ws"])
+                       ws=w["gate_ws"], add_dlogits=add_dlogits)
         mark(4)
         out = {"dx": w["dx"], "dw_gate": w["dw_gate"], "dw13": r["dw13"], "dw2": r["dw2"],
                "d_topk_w": w["d_w"]}

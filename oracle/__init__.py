@@ -25,6 +25,9 @@ Stages (pages cited by title and section):
   balance   - per-expert bias update from the batch's expert load
               (auxiliary-loss-free balancing; mastering-deepseek-v4, Implemented
               and Measured)
+  norm      - layer norm with the residual add, and its backward
+  balance_loss - the router's balance loss, counts and gradient
+  adamw     - the optimizer step with fp32 or 8-bit states
 
 Parity pinned by tests/test_oracle_*.py; see each module's header for the pins
 and for the functions whose parity the pages leave unpinned.
