@@ -150,9 +150,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a) {
     Raw8<TG> rg;
     Raw8<float> rw;
     Raw8<TP> rp;
-    load8(rg, static_cast<const TG*>(it.g) + i, n);
-    if constexpr (MASTER) load8(rw, it.w + i, n);
-    else load8(rp, static_cast<const TP*>(it.p) + i, n);
+    const Piece q{0, n > 0 ? 0 : 8, n};
+    load8(rg, static_cast<const TG*>(it.g) + i, q);
+    if constexpr (MASTER) load8(rw, it.w + i, q);
+    else load8(rp, static_cast<const TP*>(it.p) + i, q);
     float g[8], w[8], m[8], v[8], r[8];
     if constexpr (BITS8) {
       Codes cm, cv;
@@ -165,8 +166,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a) {
       for (int j = 0; j < 8; ++j) v[j] = v[j] * v[j];
     } else {
       Raw8<float> rm, rv;
-      load8(rm, static_cast<const float*>(it.m) + i, n);
-      load8(rv, static_cast<const float*>(it.v) + i, n);
+      load8(rm, static_cast<const float*>(it.m) + i, q);
+      load8(rv, static_cast<const float*>(it.v) + i, q);
       to_f32(rm, m);
       to_f32(rv, v);
     }
@@ -193,18 +194,18 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a) {
     } else {
       Raw8<float> o;
       from_f32(o, m);
-      store8(static_cast<float*>(it.m) + i, o, n);
+      store8(static_cast<float*>(it.m) + i, o, q);
       from_f32(o, v);
-      store8(static_cast<float*>(it.v) + i, o, n);
+      store8(static_cast<float*>(it.v) + i, o, q);
     }
     if constexpr (MASTER) {
       Raw8<float> o;
       from_f32(o, w);
-      store8(it.w + i, o, n);
+      store8(it.w + i, o, q);
     }
     Raw8<TP> o;
     from_f32(o, w);
-    store8(static_cast<TP*>(it.p) + i, o, n);
+    store8(static_cast<TP*>(it.p) + i, o, q);
   }
 }
 

@@ -13,6 +13,8 @@
 // lives in the registers of wpr waves (8 N elements a lane), so the mean and
 // then the centred squares are summed from registers; two sums instead of one
 // of squares keep the variance exact when the mean is large.
+#include <algorithm>
+
 #include "launch.h"
 #include "stream8.h"
 
@@ -36,86 +38,113 @@ struct NormArgs {
   float* rstd;
 };
 
-// sum over the wpr waves of a row, the same tree on every call
+// Sum over the waves of a row, the same tree on every call.  s_red: 16 slots,
+// zero where there is no wave; every lane reads the slot of its place in its
+// 16-lane DPP row, so one LDS read and four DPP adds end it.
 __device__ __forceinline__ float row_sum(float v, float* s_red, int wpr) {
   v = wave_sum(v);
   if (wpr == 1) return v;
-  const int wave = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) s_red[wave] = v;
+  if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
   __syncthreads();
-  float t = s_red[0];
-  for (int i = 1; i < wpr; ++i) t += s_red[i];
-  return t;
+  return row16_sum(s_red[threadIdx.x & 15]);
 }
 
+// A work-group walks rows gridDim.x * rpb apart and issues the next row's loads
+// before it reduces this one's.  Its columns' weights stay in registers up to
+// N = 2; wider rows read them again from cache.
 template <typename TX, typename TY, bool RES, int N>
 __global__ __launch_bounds__(kMaxWaves* kWave) void norm_fwd_kernel(const NormArgs p) {
+  constexpr bool kKeep = N <= 2;
   __shared__ float s_red[2][kMaxWaves];
+  if (threadIdx.x < 2 * kMaxWaves) s_red[threadIdx.x / kMaxWaves][threadIdx.x % kMaxWaves] = 0.0f;
+  __syncthreads();
   const int slot = p.wpr == 1 ? threadIdx.x >> 6 : 0;
   const int rt = p.wpr == 1 ? threadIdx.x & 63 : threadIdx.x;  // thread within the row
-  const int64_t row = (int64_t)blockIdx.x * p.rpb + slot;
-  if (row >= p.rows) return;  // whole waves, and only where no barrier follows (rpb > 1 has wpr = 1)
-  const int stride = p.wpr * kWave;
-  const int64_t base = row * p.d;
-  const TX* x = static_cast<const TX*>(p.x) + base;
+  const int64_t step = (int64_t)gridDim.x * p.rpb;
+  int64_t row = (int64_t)blockIdx.x * p.rpb + slot;
+  if (row >= p.rows) return;  // whole waves, and no barrier follows where rpb > 1 (then wpr = 1)
+  const TX* const x = static_cast<const TX*>(p.x);
+  const TX* const r = static_cast<const TX*>(p.r);
+  Piece q[N];
   Raw8<TX> rx[N], rr[RES ? N : 1];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int c = (i * stride + rt) * 8;
-    load8(rx[i], x + c, p.d - c);
-    if constexpr (RES) load8(rr[i], static_cast<const TX*>(p.r) + base + c, p.d - c);
+    q[i] = piece_of(i * p.wpr * kWave + rt, p.d);
+    load8(rx[i], x + row * p.d, q[i]);
+    if constexpr (RES) load8(rr[i], r + row * p.d, q[i]);
   }
-  float f[N][8];
-  float acc = 0.0f;
+  float w[N][8], b[N][8];
+  auto weights = [&](int i) __attribute__((always_inline)) {
+    Raw8<float> t;
+    load8<false>(t, p.w, q[i]);
+    to_f32(t, w[i]);
+    if (p.b != nullptr) {
+      load8<false>(t, p.b, q[i]);
+      to_f32(t, b[i]);
+    } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    to_f32(rx[i], f[i]);
-    if constexpr (RES) {
-      float g[8];
-      to_f32(rr[i], g);
+      for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
+    }
+  };
+  if constexpr (kKeep) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] += g[j];
-      const int c = (i * stride + rt) * 8;
-      Raw8<TX> s;
-      from_f32(s, f[i]);
-      store8(static_cast<TX*>(p.sum) + base + c, s, p.d - c);
-      to_f32(s, f[i]);
+    for (int i = 0; i < N; ++i) weights(i);
+  }
+  const float inv_d = 1.0f / static_cast<float>(p.d);
+  for (; row < p.rows; row += step) {
+    const int64_t base = row * p.d;
+    float f[N][8];
+    float acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      to_f32(rx[i], f[i]);
+      if constexpr (RES) {
+        float g[8];
+        to_f32(rr[i], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] += g[j];
+        Raw8<TX> s;
+        from_f32(s, f[i]);
+        store8(static_cast<TX*>(p.sum) + base, s, q[i]);
+        to_f32(s, f[i]);
+      }
+      mask8(f[i], q[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc += f[i][j];
+    }
+    if (row + step < p.rows) {
+      const int64_t next = base + step * p.d;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        load8(rx[i], x + next, q[i]);
+        if constexpr (RES) load8(rr[i], r + next, q[i]);
+      }
+    }
+    const float mean = row_sum(acc, s_red[0], p.wpr) * inv_d;
+    acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] -= mean;
+      mask8(f[i], q[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc = __builtin_fmaf(f[i][j], f[i][j], acc);
+    }
+    const float var = row_sum(acc, s_red[1], p.wpr) * inv_d;
+    const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
+    if (rt == 0 && p.mean != nullptr) {
+      p.mean[row] = mean;
+      p.rstd[row] = rstd;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc += f[i][j];
-  }
-  const float mean = row_sum(acc, s_red[0], p.wpr) / static_cast<float>(p.d);
-  acc = 0.0f;
+    for (int i = 0; i < N; ++i) {
+      if constexpr (!kKeep) weights(i);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int left = p.d - (i * stride + rt) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[i][j] = j < left ? f[i][j] - mean : 0.0f;
-      acc = __builtin_fmaf(f[i][j], f[i][j], acc);
+      for (int j = 0; j < 8; ++j) f[i][j] = __builtin_fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
+      Raw8<TY> o;
+      from_f32(o, f[i]);
+      store8(static_cast<TY*>(p.y) + base, o, q[i]);
     }
-  }
-  const float var = row_sum(acc, s_red[1], p.wpr) / static_cast<float>(p.d);
-  const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
-  if (rt == 0 && p.mean != nullptr) {
-    p.mean[row] = mean;
-    p.rstd[row] = rstd;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int c = (i * stride + rt) * 8;
-    if (c >= p.d) continue;
-    float w[8], b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = c + j < p.d;
-      w[j] = in ? p.w[c + j] : 0.0f;
-      b[j] = in && p.b != nullptr ? p.b[c + j] : 0.0f;
-      f[i][j] = __builtin_fmaf(f[i][j] * rstd, w[j], b[j]);
-    }
-    Raw8<TY> o;
-    from_f32(o, f[i]);
-    store8(static_cast<TY*>(p.y) + base + c, o, p.d - c);
   }
 }
 
@@ -133,53 +162,87 @@ struct NormBwdArgs {
   float* part;  // [gridDim.x][2][d]: dw, db of this work-group's rows
 };
 
-// A work-group takes every gridDim.x-th row and keeps its columns' dw and db
-// in registers; their sums leave once at the end.
-template <typename TD, typename TX, typename TO, bool DS, int N>
+// A work-group takes every gridDim.x-th row and keeps its columns' dw and db in
+// registers; their sums leave once at the end.  With one piece a lane the
+// weights stay there too, and the next row's loads are issued before this one
+// is reduced; wider rows have no registers for either (beyond d = 16384 they
+// spill).  MULTI (rows of one wave): each of the work-group's
+// waves takes rows of its own, and their sums are joined in LDS, so that the
+// parts stay one per work-group.
+constexpr int kMultiRows = 8;
+template <typename TD, typename TX, typename TO, bool DS, int N, bool MULTI>
 __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBwdArgs p) {
   __shared__ float s_red[2][2][kMaxWaves];
-  const int tid = threadIdx.x, wave = tid >> 6, waves = blockDim.x >> 6;
-  float w[N][8], dw[N][8], db[N][8];
+  __shared__ float s_part[MULTI ? kMultiRows : 1][MULTI ? 8 * kWave : 1];
+  const int wave = threadIdx.x >> 6, waves = MULTI ? 1 : blockDim.x >> 6;
+  const int tid = MULTI ? threadIdx.x & 63 : threadIdx.x;  // thread within the row
+  const int width = waves * kWave;
+  if (!MULTI && tid < 4 * kMaxWaves) (&s_red[0][0][0])[tid] = 0.0f;
+  __syncthreads();
+  const TD* const dy = static_cast<const TD*>(p.dy);
+  const TX* const x = static_cast<const TX*>(p.x);
+  const TX* const ds = static_cast<const TX*>(p.ds);
+  const int64_t step = (int64_t)gridDim.x * (MULTI ? kMultiRows : 1);
+  int64_t row = MULTI ? (int64_t)blockIdx.x * kMultiRows + wave : blockIdx.x;
+  Piece q[N];
+  Raw8<TD> rd[N];
+  Raw8<TX> rx[N], rs[DS ? N : 1];
+  float mean = 0.0f, rstd = 0.0f;
+  auto load = [&](int64_t r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      load8(rd[i], dy + r * p.d, q[i]);
+      load8(rx[i], x + r * p.d, q[i]);
+      if constexpr (DS) load8(rs[i], ds + r * p.d, q[i]);
+    }
+    mean = p.mean[r];
+    rstd = p.rstd[r];
+  };
+#pragma unroll
+  for (int i = 0; i < N; ++i) q[i] = piece_of(i * width + tid, p.d);
+  constexpr bool kAhead = N == 1;
+  float w[1][8], dw[N][8], db[N][8];
+  auto weights = [&](int i, float (&f)[8]) __attribute__((always_inline)) {
+    Raw8<float> t;
+    load8<false>(t, p.w, q[i]);
+    to_f32(t, f);
+  };
+  if constexpr (kAhead) {
+    if (row < p.rows) load(row);
+    weights(0, w[0]);
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int c = (i * blockDim.x + tid) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[i][j] = c + j < p.d ? p.w[c + j] : 0.0f;
-      dw[i][j] = db[i][j] = 0.0f;
-    }
+    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
   }
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  int buf = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, buf ^= 1) {
+  for (int buf = 0; row < p.rows; row += step, buf ^= 1) {
     const int64_t base = row * p.d;
-    Raw8<TD> rd[N];
-    Raw8<TX> rx[N], rs[DS ? N : 1];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * blockDim.x + tid) * 8;
-      load8(rd[i], static_cast<const TD*>(p.dy) + base + c, p.d - c);
-      load8(rx[i], static_cast<const TX*>(p.x) + base + c, p.d - c);
-      if constexpr (DS) load8(rs[i], static_cast<const TX*>(p.ds) + base + c, p.d - c);
-    }
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float xh[N][8], q[N][8];
+    float xh[N][8], g[N][8], res[DS ? N : 1][8];
     float c1 = 0.0f, c2 = 0.0f;
+    if constexpr (!kAhead) load(row);
+    const float rs1 = rstd;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float dy[8];
-      to_f32(rd[i], dy);
+      if constexpr (!kAhead) weights(i, w[0]);
+      float (&wi)[8] = w[0];
+      to_f32(rd[i], g[i]);
       to_f32(rx[i], xh[i]);
-      const int left = p.d - (i * static_cast<int>(blockDim.x) + tid) * 8;
+      if constexpr (DS) to_f32(rs[i], res[i]);
+      mask8(g[i], q[i]);  // dy = 0 where the piece owns nothing: no term of any sum
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[i][j] = j < left ? (xh[i][j] - mean) * rstd : 0.0f;
-        q[i][j] = dy[j] * w[i][j];
-        dw[i][j] = __builtin_fmaf(dy[j], xh[i][j], dw[i][j]);
-        db[i][j] += dy[j];
-        c1 += q[i][j];
-        c2 = __builtin_fmaf(q[i][j], xh[i][j], c2);
+        xh[i][j] = (xh[i][j] - mean) * rs1;
+        dw[i][j] = __builtin_fmaf(g[i][j], xh[i][j], dw[i][j]);
+        db[i][j] += g[i][j];
+        g[i][j] *= wi[j];
+        c1 += g[i][j];
+        c2 = __builtin_fmaf(g[i][j], xh[i][j], c2);
       }
+    }
+    if constexpr (kAhead) {
+      if (row + step < p.rows) load(row + step);
     }
     c1 = wave_sum(c1);
     c2 = wave_sum(c2);
@@ -189,60 +252,80 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
         s_red[buf][1][wave] = c2;
       }
       __syncthreads();  // the other buffer is free again once all waves are here
-      c1 = s_red[buf][0][0];
-      c2 = s_red[buf][1][0];
-      for (int i = 1; i < waves; ++i) {
-        c1 += s_red[buf][0][i];
-        c2 += s_red[buf][1][i];
-      }
+      c1 = row16_sum(s_red[buf][0][tid & 15]);
+      c2 = row16_sum(s_red[buf][1][tid & 15]);
     }
     c1 *= inv_d;
     c2 *= inv_d;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = (i * blockDim.x + tid) * 8;
-      if (c >= p.d) continue;
-      float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = rstd * (q[i][j] - c1 - xh[i][j] * c2);
-      if constexpr (DS) {
-        float g[8];
-        to_f32(rs[i], g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += g[j];
+      for (int j = 0; j < 8; ++j) {
+        g[i][j] = rs1 * (g[i][j] - c1 - xh[i][j] * c2);
+        if constexpr (DS) g[i][j] += res[i][j];
       }
-      Raw8<TO> ro;
-      from_f32(ro, o);
-      store8(static_cast<TO*>(p.dx) + base + c, ro, p.d - c);
+      Raw8<TO> o;
+      from_f32(o, g[i]);
+      store8(static_cast<TO*>(p.dx) + base, o, q[i]);
     }
   }
   float* part = p.part + (int64_t)blockIdx.x * 2 * p.d;
+  if constexpr (MULTI) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Raw8<float> r;
+      from_f32(r, h == 0 ? dw[0] : db[0]);
+      store8(s_part[wave], r, q[0]);
+      __syncthreads();
+      for (int c = threadIdx.x; c < p.d; c += kMultiRows * kWave) {
+        float v = s_part[0][c];
+#pragma unroll
+        for (int k = 1; k < kMultiRows; ++k) v += s_part[k][c];
+        part[h * p.d + c] = v;
+      }
+      __syncthreads();
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int c = (i * blockDim.x + tid) * 8;
-    if (c >= p.d) continue;
     Raw8<float> r;
     from_f32(r, dw[i]);
-    store8(part + c, r, p.d - c);
+    store8(part, r, q[i]);
     from_f32(r, db[i]);
-    store8(part + p.d + c, r, p.d - c);
+    store8(part + p.d, r, q[i]);
   }
 }
 
-// dw and db as the sums of the work-groups' parts, each column by 4 lanes that
-// take every fourth part in order, then (l0 + l1) + (l2 + l3)
-__global__ __launch_bounds__(256) void norm_param_grad_kernel(const float* part, int parts, int d, float* dw,
-                                                              float* db) {
-  __shared__ float s_sum[4][kWave];
-  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+// dw and db as the sums of the work-groups' parts: 64 columns a work-group, each
+// of its 16 waves adds every 16th part in order (8 loads in flight), then the
+// waves in order.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(kSumWaves* kWave) void norm_param_grad_kernel(const float* part, int parts, int d,
+                                                                          float* dw, float* db) {
+  __shared__ float s_sum[kSumWaves][kWave];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * kWave + lane;  // column of [dw | db]
   float v = 0.0f;
-  if (c < 2 * d)
-    for (int g = q; g < parts; g += 4) v += part[(int64_t)g * 2 * d + c];
-  s_sum[q][lane] = v;
+  if (c < 2 * d) {
+    const int64_t pitch = 2 * (int64_t)d;
+    const float* at = part + c;
+    int g = wave;
+    for (; g + 7 * kSumWaves < parts; g += 8 * kSumWaves) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = at[(g + i * kSumWaves) * pitch];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += t[i];
+    }
+    for (; g < parts; g += kSumWaves) v += at[g * pitch];
+  }
+  s_sum[wave][lane] = v;
   __syncthreads();
-  if (q == 0 && c < 2 * d) {
-    v = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+  if (wave == 0 && c < 2 * d) {
+    v = s_sum[0][lane];
+#pragma unroll
+    for (int i = 1; i < kSumWaves; ++i) v += s_sum[i][lane];
     if (c < d) dw[c] = v;
     else if (db != nullptr) db[c - d] = v;
   }
@@ -253,36 +336,44 @@ hipError_t fwd_n(const NormArgs& a, int n, dim3 grid, dim3 block, hipStream_t s)
   switch (n) {
     case 1: hipLaunchKernelGGL((norm_fwd_kernel<TX, TY, RES, 1>), grid, block, 0, s, a); break;
     case 2: hipLaunchKernelGGL((norm_fwd_kernel<TX, TY, RES, 2>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((norm_fwd_kernel<TX, TY, RES, 4>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((norm_fwd_kernel<TX, TY, RES, 8>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((norm_fwd_kernel<TX, TY, RES, 4>), grid, block, 0, s, a); break;
   }
   return hipGetLastError();
 }
 
+// launch shape of the backward: pieces of 8 a lane holds, waves of a row, rows
+// at once in a work-group, work-groups (= parts of the parameter gradients)
+struct BwdShape {
+  int n, waves, rpb;
+  int64_t groups;
+};
+// One piece a lane while a row then fits 16 waves (d <= 8192): two need over
+// 128 registers (16384 x 7168: 206 us against 400).  One work-group per CU
+// keeps the parts few (256: 206 + 5 us, 512: 223 + 9); narrow rows take two, to
+// have enough loads in flight.
+BwdShape bwd_shape(int64_t rows, int d) {
+  const int pieces = (d + 7) / 8;
+  int n = 1;
+  while (pieces > n * kWave * kMaxWaves) n *= 2;
+  const int waves = (pieces + n * kWave - 1) / (n * kWave);
+  const int rpb = waves == 1 ? kMultiRows : 1;
+  const int64_t need = (rows + rpb - 1) / rpb, fill = 256 * (waves < 4 ? 2 : 1);
+  return {n, waves, rpb, need < fill ? need : fill};
+}
+
 template <typename TD, typename TX, typename TO, bool DS>
-hipError_t bwd_n(const NormBwdArgs& a, int n, dim3 grid, dim3 block, hipStream_t s) {
-  switch (n) {
-    case 1: hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 2>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 4>), grid, block, 0, s, a); break;
-  }
+hipError_t bwd_n(const NormBwdArgs& a, const BwdShape& b, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(b.groups)), block(b.waves * b.rpb * kWave);
+  if (b.rpb > 1) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, true>), grid, block, 0, s, a);
+  else if (b.n == 1) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, false>), grid, block, 0, s, a);
+  else if (b.n == 2) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 2, false>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 4, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
 template <typename TD, typename TX, typename TO>
-hipError_t bwd_ds(const NormBwdArgs& a, int n, dim3 grid, dim3 block, hipStream_t s) {
-  return a.ds != nullptr ? bwd_n<TD, TX, TO, true>(a, n, grid, block, s)
-                         : bwd_n<TD, TX, TO, false>(a, n, grid, block, s);
-}
-
-// pieces of 8 a lane holds, and the waves that then cover a row
-struct Split {
-  int n, waves;
-};
-Split row_split(int d, int n) {
-  const int pieces = (d + 7) / 8;
-  while (pieces > n * kWave * kMaxWaves) n *= 2;
-  return {n, (pieces + n * kWave - 1) / (n * kWave)};
+hipError_t bwd_ds(const NormBwdArgs& a, const BwdShape& b, hipStream_t s) {
+  return a.ds != nullptr ? bwd_n<TD, TX, TO, true>(a, b, s) : bwd_n<TD, TX, TO, false>(a, b, s);
 }
 
 }  // namespace
@@ -290,59 +381,65 @@ Split row_split(int d, int n) {
 hipError_t launch_layer_norm(int64_t rows, int d, const void* x, const void* r, int x_dtype, const float* w,
                              const float* b, float eps, void* sum, void* y, int y_dtype, float* mean, float* rstd,
                              hipStream_t s) {
-  const Split sp = row_split(d, d <= 512 ? 1 : 2);
-  const int rpb = sp.waves == 1 ? 4 : 1;
-  const NormArgs a{rows, d, sp.waves, rpb, x, r, w, b, eps, sum, y, mean, rstd};
-  const dim3 grid(static_cast<unsigned>((rows + rpb - 1) / rpb)), block(sp.waves * rpb * kWave);
+  // two pieces a lane, one for narrow rows (4096 x 2048 bf16: 13.1 us against
+  // 13.4; fp32 16384 x 7168: 303 against 296)
+  const int pieces = (d + 7) / 8;
+  int n = d <= 2048 ? 1 : 2;
+  while (pieces > n * kWave * kMaxWaves) n *= 2;
+  const int waves = (pieces + n * kWave - 1) / (n * kWave), rpb = waves == 1 ? 4 : 1;
+  // Work-groups: all at once while the chip holds them; else about 24 KB of
+  // loads per CU in flight (more only lengthens the queues: 16384 x 7168 bf16
+  // 164 us with 256 work-groups, 180 with 512), in passes of equal length.
+  const int64_t need = (rows + rpb - 1) / rpb;
+  int64_t groups = need;
+  if (need * waves * rpb > 256 * 16) {
+    const int64_t bytes = (int64_t)rpb * d * (x_dtype == MOE_BF16 ? 2 : 4) * (r != nullptr ? 2 : 1);
+    const int64_t most = 256 * std::max<int64_t>(1, (24576 + bytes / 2) / bytes);
+    const int64_t passes = (need + most - 1) / most;
+    groups = (need + passes - 1) / passes;
+  }
+  const NormArgs a{rows, d, waves, rpb, x, r, w, b, eps, sum, y, mean, rstd};
+  const dim3 grid(static_cast<unsigned>(groups)), block(waves * rpb * kWave);
   const bool xb = x_dtype == MOE_BF16, yb = y_dtype == MOE_BF16;
   if (r != nullptr) {
-    if (xb) return yb ? fwd_n<uint16_t, uint16_t, true>(a, sp.n, grid, block, s)
-                      : fwd_n<uint16_t, float, true>(a, sp.n, grid, block, s);
-    return yb ? fwd_n<float, uint16_t, true>(a, sp.n, grid, block, s)
-              : fwd_n<float, float, true>(a, sp.n, grid, block, s);
+    if (xb) return yb ? fwd_n<uint16_t, uint16_t, true>(a, n, grid, block, s)
+                      : fwd_n<uint16_t, float, true>(a, n, grid, block, s);
+    return yb ? fwd_n<float, uint16_t, true>(a, n, grid, block, s)
+              : fwd_n<float, float, true>(a, n, grid, block, s);
   }
-  if (xb) return yb ? fwd_n<uint16_t, uint16_t, false>(a, sp.n, grid, block, s)
-                    : fwd_n<uint16_t, float, false>(a, sp.n, grid, block, s);
-  return yb ? fwd_n<float, uint16_t, false>(a, sp.n, grid, block, s)
-            : fwd_n<float, float, false>(a, sp.n, grid, block, s);
-}
-
-// work-groups of the backward (= parts of the parameter gradients)
-static int64_t norm_bwd_groups(int64_t rows, int d) {
-  const Split sp = row_split(d, d <= 512 ? 1 : 2);
-  const int64_t fill = 256 * (sp.waves >= 8 ? 2 : 16 / sp.waves);
-  return rows < fill ? rows : fill;
+  if (xb) return yb ? fwd_n<uint16_t, uint16_t, false>(a, n, grid, block, s)
+                    : fwd_n<uint16_t, float, false>(a, n, grid, block, s);
+  return yb ? fwd_n<float, uint16_t, false>(a, n, grid, block, s)
+            : fwd_n<float, float, false>(a, n, grid, block, s);
 }
 
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int d) {
-  return static_cast<size_t>(norm_bwd_groups(rows, d)) * 2 * d * sizeof(float);
+  return static_cast<size_t>(bwd_shape(rows, d).groups) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dtype, const void* x, int x_dtype,
                                  const float* w, const float* mean, const float* rstd, const void* ds, void* dx,
                                  int dx_dtype, float* dw, float* db, float* ws, hipStream_t s) {
-  const int64_t groups = norm_bwd_groups(rows, d);
-  if (groups > 0) {
-    const Split sp = row_split(d, d <= 512 ? 1 : 2);
+  const BwdShape b = bwd_shape(rows, d);
+  if (b.groups > 0) {
     const NormBwdArgs a{rows, d, dy, x, w, mean, rstd, ds, dx, ws};
-    const dim3 grid(static_cast<unsigned>(groups)), block(sp.waves * kWave);
     const int key = (dy_dtype == MOE_BF16) | (x_dtype == MOE_BF16) << 1 | (dx_dtype == MOE_BF16) << 2;
     hipError_t e = hipSuccess;
     using B = uint16_t;
     switch (key) {
-      case 0: e = bwd_ds<float, float, float>(a, sp.n, grid, block, s); break;
-      case 1: e = bwd_ds<B, float, float>(a, sp.n, grid, block, s); break;
-      case 2: e = bwd_ds<float, B, float>(a, sp.n, grid, block, s); break;
-      case 3: e = bwd_ds<B, B, float>(a, sp.n, grid, block, s); break;
-      case 4: e = bwd_ds<float, float, B>(a, sp.n, grid, block, s); break;
-      case 5: e = bwd_ds<B, float, B>(a, sp.n, grid, block, s); break;
-      case 6: e = bwd_ds<float, B, B>(a, sp.n, grid, block, s); break;
-      default: e = bwd_ds<B, B, B>(a, sp.n, grid, block, s); break;
+      case 0: e = bwd_ds<float, float, float>(a, b, s); break;
+      case 1: e = bwd_ds<B, float, float>(a, b, s); break;
+      case 2: e = bwd_ds<float, B, float>(a, b, s); break;
+      case 3: e = bwd_ds<B, B, float>(a, b, s); break;
+      case 4: e = bwd_ds<float, float, B>(a, b, s); break;
+      case 5: e = bwd_ds<B, float, B>(a, b, s); break;
+      case 6: e = bwd_ds<float, B, B>(a, b, s); break;
+      default: e = bwd_ds<B, B, B>(a, b, s); break;
     }
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(norm_param_grad_kernel, dim3((2 * d + kWave - 1) / kWave), dim3(256), 0, s, ws,
-                     static_cast<int>(groups), d, dw, db);
+  hipLaunchKernelGGL(norm_param_grad_kernel, dim3((2 * d + kWave - 1) / kWave), dim3(kSumWaves * kWave), 0, s, ws,
+                     static_cast<int>(b.groups), d, dw, db);
   return hipGetLastError();
 }
 

@@ -24,26 +24,53 @@ struct Raw8<float> {
   u32x4 a, b;
 };
 
-// n: how many of the 8 exist (the others read as 0 and are not touched)
-__device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* p, int n) {
-  if (n >= 8) {
+// A lane's piece of a row of d elements: the 8 columns [c, c + 8), of which it
+// owns [lo, hi).  A row's last piece is moved back to end with the row, so that
+// it is loaded whole too and owns only what the piece before it does not reach;
+// rows shorter than 8 have one partial piece.  lo = 8: no piece.
+struct Piece {
+  int c, lo, hi;
+};
+__device__ __forceinline__ Piece piece_of(int i, int d) {
+  const int c = i * 8;
+  if (d < 8) return {0, i == 0 ? 0 : 8, d};
+  const int back = max(0, c + 8 - d);
+  return {c - back, min(back, 8), 8};
+}
+__device__ __forceinline__ bool owns(const Piece& q, int j) { return j >= q.lo && j < q.hi; }
+
+// loads the piece (zeros where there is none, or past hi)
+__device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* p, const Piece& q) {
+  r.a = u32x4{0, 0, 0, 0};
+  if (q.lo >= 8) return;
+  p += q.c;
+  if (q.hi == 8) {
     r.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
   } else {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-      if (i < n) w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+      if (i < q.hi) w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
     r.a = u32x4{w[0], w[1], w[2], w[3]};
   }
 }
-__device__ __forceinline__ void load8(Raw8<float>& r, const float* p, int n) {
-  if (n >= 8) {
-    r.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p));
-    r.b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p + 4));
+template <bool STREAM = true>
+__device__ __forceinline__ void load8(Raw8<float>& r, const float* p, const Piece& q) {
+  r.a = r.b = u32x4{0, 0, 0, 0};
+  if (q.lo >= 8) return;
+  p += q.c;
+  if (q.hi == 8) {
+    if constexpr (STREAM) {
+      r.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p));
+      r.b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p + 4));
+    } else {  // what many work-groups read
+      r.a = *reinterpret_cast<const u32x4_a4*>(p);
+      r.b = *reinterpret_cast<const u32x4_a4*>(p + 4);
+    }
   } else {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+    for (int i = 0; i < 8; ++i) w[i] = i < q.hi ? __float_as_uint(p[i]) : 0u;
     r.a = u32x4{w[0], w[1], w[2], w[3]};
     r.b = u32x4{w[4], w[5], w[6], w[7]};
   }
@@ -76,24 +103,33 @@ __device__ __forceinline__ void from_f32(Raw8<float>& r, const float (&f)[8]) {
   }
 }
 
-__device__ __forceinline__ void store8(uint16_t* p, const Raw8<uint16_t>& r, int n) {
-  if (n >= 8) {
+// stores the elements the piece owns
+__device__ __forceinline__ void store8(uint16_t* p, const Raw8<uint16_t>& r, const Piece& q) {
+  p += q.c;
+  if (q.lo == 0 && q.hi == 8) {
     *reinterpret_cast<u32x4_a2*>(p) = r.a;
   } else {
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = static_cast<uint16_t>(r.a[i / 2] >> (16 * (i & 1)));
+    for (int i = 0; i < 8; ++i)
+      if (owns(q, i)) p[i] = static_cast<uint16_t>(r.a[i / 2] >> (16 * (i & 1)));
   }
 }
-__device__ __forceinline__ void store8(float* p, const Raw8<float>& r, int n) {
-  if (n >= 8) {
+__device__ __forceinline__ void store8(float* p, const Raw8<float>& r, const Piece& q) {
+  p += q.c;
+  if (q.lo == 0 && q.hi == 8) {
     *reinterpret_cast<u32x4_a4*>(p) = r.a;
     *reinterpret_cast<u32x4_a4*>(p + 4) = r.b;
   } else {
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = __uint_as_float(i < 4 ? r.a[i & 3] : r.b[i & 3]);
+    for (int i = 0; i < 8; ++i)
+      if (owns(q, i)) p[i] = __uint_as_float(i < 4 ? r.a[i & 3] : r.b[i & 3]);
   }
+}
+// zeros the elements the piece does not own
+__device__ __forceinline__ void mask8(float (&f)[8], const Piece& q) {
+  if (q.lo == 0 && q.hi == 8) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = owns(q, j) ? f[j] : 0.0f;
 }
 
 // Sum over the 64 lanes in every lane, by the same tree on every call: DPP
@@ -103,11 +139,14 @@ template <int CTRL>
 __device__ __forceinline__ float dpp_f32(float v) {
   return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xF, 0xF, false));
 }
+__device__ __forceinline__ float row16_sum(float v) {  // over 16 lanes
+  v += dpp_f32<0xB1>(v);          // quad_perm [1,0,3,2]
+  v += dpp_f32<0x4E>(v);          // quad_perm [2,3,0,1]
+  v += dpp_f32<0x141>(v);         // row_half_mirror
+  return v + dpp_f32<0x140>(v);   // row_mirror
+}
 __device__ __forceinline__ float wave_sum(float v) {
-  v += dpp_f32<0xB1>(v);   // quad_perm [1,0,3,2]
-  v += dpp_f32<0x4E>(v);   // quad_perm [2,3,0,1]
-  v += dpp_f32<0x141>(v);  // row_half_mirror
-  v += dpp_f32<0x140>(v);  // row_mirror
+  v = row16_sum(v);
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
   const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
