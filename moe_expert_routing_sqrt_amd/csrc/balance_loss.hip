@@ -16,6 +16,8 @@
 // no cancellation, and no underflow before e^(l/2) itself.  Two
 // transcendental instructions and 16 others an element.
 // A row whose affinities all vanish has no probabilities: it adds 0.
+#include <type_traits>
+
 #include "launch.h"
 #include "stream8.h"
 
@@ -25,6 +27,7 @@ namespace {
 constexpr int kTile = 64;  // tokens of a forward work-group: one per lane
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kSumGroups = 64;  // sequences summed at once (each costs one atomic at the end)
 
 struct Affinity {
   float a;   // sqrt(softplus(l))
@@ -68,27 +71,59 @@ __device__ __forceinline__ int sequence_of(int64_t t, int64_t T, const int32_t* 
   return lo;
 }
 
-// A row of E logits in a wave: aligned groups of `lpt` lanes (a power of two)
-// hold one token each, a lane 4 consecutive experts of every 256.
+// A row of E values in a wave: aligned groups of `lpt` lanes (a power of two)
+// hold one token each, a lane 4 consecutive columns of every 256.  FULL: E is
+// 4 lpt NR, every lane's columns exist.  Otherwise the last lane's columns are
+// moved back to end with the row and lanes past it read those too, so that
+// every load is a whole one and no branch stands between a load and the next
+// (E < 4: single elements, the last one repeated); `lo` counts the columns at
+// a lane's start that are not its own (4: none are).
+template <int NR, bool FULL>
 struct RowMap {
-  int E, lpt, log_lpt;
-};
-template <int NR>
-__device__ __forceinline__ void load_row(const float* row, const RowMap& m, int sub, bool in, float fill,
-                                         float (&l)[NR][4]) {
+  int E, lpt, sub, which;
+  int col[NR], lo[NR];
+  __device__ __forceinline__ RowMap(int E_, int log_lpt) : E(E_), lpt(1 << log_lpt) {
+    const int lane = threadIdx.x & 63;
+    sub = lane & (lpt - 1);
+    which = lane >> log_lpt;
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int e = r * 256 + sub * 4;
-    if (in && e + 4 <= m.E) {
-      const u32x4 v = *reinterpret_cast<const u32x4_a4*>(row + e);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) l[r][i] = __uint_as_float(v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) l[r][i] = in && e + i < m.E ? row[e + i] : fill;
+    for (int r = 0; r < NR; ++r) {
+      const int c = r * 256 + sub * 4;
+      col[r] = FULL ? c : max(0, min(c, E - 4));
+      lo[r] = FULL ? 0 : min(4, c - col[r]);
     }
   }
-}
+  __device__ __forceinline__ bool owns(int r, int j) const {
+    return FULL || (j >= lo[r] && col[r] + j < E);
+  }
+  __device__ __forceinline__ void load(const float* row, float (&l)[NR][4]) const {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (FULL || E >= 4) {
+        const u32x4 v = *reinterpret_cast<const u32x4_a4*>(row + col[r]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[r][i] = __uint_as_float(v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[r][i] = row[min(i, E - 1)];
+      }
+    }
+  }
+  // the columns a lane owns
+  __device__ __forceinline__ void store(float* row, const float (&v)[NR][4]) const {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (FULL || (lo[r] == 0 && E >= 4)) {
+        *reinterpret_cast<u32x4_a4*>(row + col[r]) = u32x4{__float_as_uint(v[r][0]), __float_as_uint(v[r][1]),
+                                                           __float_as_uint(v[r][2]), __float_as_uint(v[r][3])};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (owns(r, i)) row[col[r] + i] = v[r][i];
+      }
+    }
+  }
+};
 
 // sum over the aligned group of lpt lanes
 __device__ __forceinline__ float group_sum(float v, int lpt) {
@@ -104,8 +139,7 @@ __device__ __forceinline__ float group_sum(float v, int lpt) {
 // ---------------------------------------------------------------- forward
 struct LossArgs {
   int64_t T;
-  RowMap m;
-  int k, n_seq;
+  int E, log_lpt, k, n_seq;
   const float* logits;
   const float* offset;
   const int32_t* idx;
@@ -117,27 +151,58 @@ struct LossArgs {
   int* ticket;    // of the sums that follow: reset here
 };
 
-// One work-group per tile of 64 tokens, lane i of every wave knowing token i's
-// sequence, so that a sequence's tokens in the tile are a ballot.  For each
-// sequence s with tokens in tile b it writes the sums of p, the slot counts and
-// the token count to row b + s: along the tokens b and s only grow, so no two
-// pairs share a row.
-template <int NR>
+// One work-group per tile of 64 tokens: their probabilities are formed once, in
+// registers.  Lane i of every wave knows token i's sequence, so that a
+// sequence's tokens in the tile are a ballot.  For each sequence s with tokens
+// in tile b the sums of p, the slot counts and the token count go to row b + s:
+// along the tokens b and s only grow, so no two pairs share a row.
+template <int NR, bool FULL>
 __global__ __launch_bounds__(kThreads) void balance_part_kernel(const LossArgs p) {
-  constexpr int U = NR == 4 ? 2 : 4;  // tokens of a lane group with their loads in flight
+  constexpr int U = kTile / kWaves;  // tokens of a lane group (at one token a wave)
   __shared__ int s_cnt[NR * 256];
-  __shared__ float s_sum[kWaves][NR * 256];
+  __shared__ __align__(16) float s_sum[kWaves][NR * 256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t t0 = (int64_t)blockIdx.x * kTile;
   const int ntok = static_cast<int>(min((int64_t)kTile, p.T - t0));
-  const int E = p.m.E, lpt = p.m.lpt, tpw = kWave / lpt, sub = lane & (lpt - 1), which = lane >> p.m.log_lpt;
-  if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
-  // a slot of the tile per thread: 64 k <= 1024
-  const int my_tok = tid / p.k;
+  const int E = p.E;
+  const RowMap<NR, FULL> m(E, p.log_lpt);
+  const int tpw = kWave / m.lpt;
+  // every load of the tile before the first wait; a token that does not count
+  // may hold anything, also NaN: its row is read but never selected
+  float pr[U][NR][4], off[NR][4] = {};
+  if (ntok > 0) {
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      const int i = (v * kWaves + wave) * tpw + m.which;
+      m.load(p.logits + (t0 + min(i, ntok - 1)) * E, pr[v]);
+    }
+    if (p.offset != nullptr) m.load(p.offset, off);
+  }
+  const int my_tok = tid / p.k;  // a slot of the tile per thread: 64 k <= 1024
   const int my_e = my_tok < ntok ? p.idx[t0 * p.k + tid] : -1;
-  const int seq = sequence_of(t0 + lane, p.T, p.seq, p.n_seq);
   const bool on = lane < ntok && (p.mask == nullptr || p.mask[t0 + lane] != 0);
+  const int seq = sequence_of(t0 + lane, p.T, p.seq, p.n_seq);
+  if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
   for (int e = tid; e < E; e += kThreads) s_cnt[e] = 0;
+#pragma unroll
+  for (int v = 0; v < U; ++v) {
+    if ((v * kWaves + wave) * tpw >= ntok) break;  // uniform over the wave
+    float total = 0.0f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = affinity<false>(pr[v][r][j] + off[r][j]).a;
+        pr[v][r][j] = m.owns(r, j) ? a : 0.0f;
+        total += pr[v][r][j];
+      }
+    total = group_sum(total, m.lpt);
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pr[v][r][j] *= inv;
+  }
   __syncthreads();
   for (uint64_t left = __ballot(seq >= 0); left != 0;) {  // one sequence at a time, the same in every wave
     const int s = __builtin_amdgcn_readlane(seq, __builtin_ctzll(left));
@@ -145,47 +210,23 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(const LossArgs p
     const uint64_t counted = run & __ballot(on);
     left &= ~run;
     float sum[NR][4] = {};
-    for (int i0 = 0; i0 < kTile; i0 += U * kWaves * tpw) {
-      float l[U][NR][4];
-      bool in[U];
 #pragma unroll
-      for (int v = 0; v < U; ++v) {
-        const int i = i0 + (v * kWaves + wave) * tpw + which;
-        in[v] = i < kTile && ((counted >> (i & 63)) & 1) != 0;
-        // a token that does not count may hold anything, also NaN: it is not read
-        load_row<NR>(p.logits + (t0 + i) * E, p.m, sub, in[v], 0.0f, l[v]);
-      }
+    for (int v = 0; v < U; ++v) {
+      const int i = (v * kWaves + wave) * tpw + m.which;
+      const bool in = i < kTile && ((counted >> (i & 63)) & 1) != 0;
 #pragma unroll
-      for (int v = 0; v < U; ++v) {
-        if (!__any(in[v])) continue;
-        float total = 0.0f;
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = r * 256 + sub * 4 + j;
-            if (p.offset != nullptr && e < E) l[v][r][j] += p.offset[e];
-            l[v][r][j] = in[v] && e < E ? affinity<false>(l[v][r][j]).a : 0.0f;
-            total += l[v][r][j];
-          }
-        total = group_sum(total, lpt);
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum[r][j] = __builtin_fmaf(l[v][r][j], inv, sum[r][j]);
-      }
+        for (int j = 0; j < 4; ++j) sum[r][j] += in ? pr[v][r][j] : 0.0f;
     }
     if (my_e >= 0 && my_e < E && ((counted >> my_tok) & 1) != 0) atomicAdd(&s_cnt[my_e], 1);
     // the lane groups of a wave, then the waves in order
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float v = sum[r][j];
-        for (int o = lpt; o < kWave; o <<= 1) v += __shfl_xor(v, o, kWave);
-        if (which == 0) s_sum[wave][r * 256 + sub * 4 + j] = v;
-      }
+      for (int j = 0; j < 4; ++j)
+        for (int o = m.lpt; o < kWave; o <<= 1) sum[r][j] += __shfl_xor(sum[r][j], o, kWave);
+    if (m.which == 0) m.store(s_sum[wave], sum);
     __syncthreads();
     const int64_t row = (int64_t)blockIdx.x + s;
     for (int e = tid; e < E; e += kThreads) {
@@ -197,7 +238,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(const LossArgs p
       s_cnt[e] = 0;
     }
     if (tid == 0) p.ptok[row] = __builtin_popcountll(counted);
-    __syncthreads();
+    if (left != 0) __syncthreads();
   }
 }
 
@@ -212,89 +253,91 @@ struct SumArgs {
   int32_t* counts;
   float* prob;
   float* dprob;
-  float* part;  // [n_seq * column slices]: sum of f P
+  float* part;  // one per work-group: its sum of f P
   int* ticket;
   float* loss;
 };
 
-// One work-group per sequence and slice of W = 2^log_w experts: thread (q, c)
-// adds every (1024/W)-th part of column c, the parts of a column are then
-// joined pairwise.  The last work-group to finish adds the slices' sums of f P,
-// in their order, into the loss.
+// Work-group (x, y): slice y of W = 2^log_w experts, for sequences x, x +
+// gridDim.x, ...  Thread (q, c) adds every (threads/W)-th part of column c; the
+// parts of a column are then joined in order of q.  The last work-group to
+// finish adds everyone's sums of f P, in their order, into the loss.
 __global__ __launch_bounds__(kThreads) void balance_sum_kernel(const SumArgs p) {
   __shared__ float s_v[kThreads];
   __shared__ int s_c[kThreads];
-  __shared__ int s_t[kThreads];
+  __shared__ int s_t[kWaves];
   __shared__ bool s_last;
-  const int s = blockIdx.x, tid = threadIdx.x;
-  const int W = 1 << p.log_w, lanes = kThreads >> p.log_w;
+  const int tid = threadIdx.x;
+  const int W = 1 << p.log_w, lanes = static_cast<int>(blockDim.x) >> p.log_w;
   const int e = blockIdx.y * W + (tid & (W - 1)), q = tid >> p.log_w;
-  const int64_t lo = p.seq == nullptr ? 0 : max((int64_t)p.seq[s], (int64_t)0);
-  const int64_t hi = p.seq == nullptr ? p.T : min((int64_t)p.seq[s + 1], p.T);
-  const int64_t r0 = lo / kTile + s, r1 = lo < hi ? (hi - 1) / kTile + 1 + s : r0;  // its rows of parts
-  float v = 0.0f;
-  int c = 0, t = 0;
-  for (int64_t r = r0 + tid; r < r1; r += kThreads) t += p.ptok[r];
-  if (e < p.E) {
-    int64_t r = r0 + q;
-    for (; r + 3 * lanes < r1; r += 4 * lanes) {
-      float a[4];
-      int b[4];
+  float loss = 0.0f;  // of thread c < W
+  for (int s = blockIdx.x; s < p.n_seq; s += gridDim.x) {
+    const int64_t lo = p.seq == nullptr ? 0 : max((int64_t)p.seq[s], (int64_t)0);
+    const int64_t hi = p.seq == nullptr ? p.T : min((int64_t)p.seq[s + 1], p.T);
+    const int64_t r0 = lo / kTile + s, r1 = lo < hi ? (hi - 1) / kTile + 1 + s : r0;  // its rows of parts
+    float v = 0.0f;
+    int c = 0, t = 0;
+    for (int64_t r = r0 + tid; r < r1; r += blockDim.x) t += p.ptok[r];
+    if (e < p.E) {
+      int64_t r = r0 + q;
+      for (; r + 3 * lanes < r1; r += 4 * lanes) {
+        float a[4];
+        int b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = p.psum[(r + i * lanes) * p.E + e];
-        b[i] = p.pcnt[(r + i * lanes) * p.E + e];
-      }
+        for (int i = 0; i < 4; ++i) {
+          a[i] = p.psum[(r + i * lanes) * p.E + e];
+          b[i] = p.pcnt[(r + i * lanes) * p.E + e];
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v += a[i];
-        c += b[i];
+        for (int i = 0; i < 4; ++i) {
+          v += a[i];
+          c += b[i];
+        }
+      }
+      for (; r < r1; r += lanes) {
+        v += p.psum[r * p.E + e];
+        c += p.pcnt[r * p.E + e];
       }
     }
-    for (; r < r1; r += lanes) {
-      v += p.psum[r * p.E + e];
-      c += p.pcnt[r * p.E + e];
-    }
-  }
-  s_v[tid] = v;
-  s_c[tid] = c;
-  s_t[tid] = t;
-  __syncthreads();
-  for (int o = kThreads / 2; o >= 1; o >>= 1) {
-    if (tid < o) {
-      s_t[tid] += s_t[tid + o];
-      if (o >= W) {
-        s_v[tid] += s_v[tid + o];
-        s_c[tid] += s_c[tid + o];
-      }
-    }
+    for (int o = 32; o >= 1; o >>= 1) t += __shfl_xor(t, o, kWave);
+    s_v[tid] = v;
+    s_c[tid] = c;
+    if ((tid & 63) == 0) s_t[tid >> 6] = t;
     __syncthreads();
-  }
-  if (tid < kWave) {
-    const float per = s_t[0] > 0 ? 1.0f / static_cast<float>(s_t[0]) : 0.0f;
-    float part = 0.0f;
-    if (tid < W && e < p.E) {
-      const float f = static_cast<float>(s_c[tid]) * (static_cast<float>(p.E) / static_cast<float>(p.k)) * per;
-      const float P = s_v[tid] * per;
-      const int64_t at = (int64_t)s * p.E + e;
-      p.counts[at] = s_c[tid];
-      p.prob[at] = P;
-      p.dprob[at] = f * per * (p.alpha / static_cast<float>(p.n_seq));
-      part = f * P;
+    if (tid < W) {
+      for (int i = 1; i < lanes; ++i) {
+        v += s_v[i * W + tid];
+        c += s_c[i * W + tid];
+      }
+      t = s_t[0];
+      for (int i = 1; i < static_cast<int>(blockDim.x) / kWave; ++i) t += s_t[i];
+      if (e < p.E) {
+        const float per = t > 0 ? 1.0f / static_cast<float>(t) : 0.0f;
+        const float f = static_cast<float>(c) * (static_cast<float>(p.E) / static_cast<float>(p.k)) * per;
+        const float P = v * per;
+        const int64_t at = (int64_t)s * p.E + e;
+        p.counts[at] = c;
+        p.prob[at] = P;
+        p.dprob[at] = f * per * (p.alpha / static_cast<float>(p.n_seq));
+        loss = __builtin_fmaf(f, P, loss);
+      }
     }
-    part = wave_sum(part);
+    if (s + static_cast<int>(gridDim.x) < p.n_seq) __syncthreads();
+  }
+  const int groups = gridDim.x * gridDim.y;
+  if (tid < kWave) {
+    loss = wave_sum(loss);
     if (tid == 0) {
-      const int total = gridDim.x * gridDim.y;
-      __hip_atomic_store(&p.part[blockIdx.x * gridDim.y + blockIdx.y], part, __ATOMIC_RELAXED,
+      __hip_atomic_store(&p.part[blockIdx.x * gridDim.y + blockIdx.y], loss, __ATOMIC_RELAXED,
                          __HIP_MEMORY_SCOPE_AGENT);
-      s_last = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
+      s_last = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == groups - 1;
     }
   }
   __syncthreads();
   if (!s_last || tid >= kWave) return;
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   float sum = 0.0f;
-  for (int i = tid; i < static_cast<int>(gridDim.x * gridDim.y); i += kWave)
+  for (int i = tid; i < groups; i += kWave)
     sum += __hip_atomic_load(&p.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   sum = wave_sum(sum);
   if (tid == 0) *p.loss = sum * (p.alpha / static_cast<float>(p.n_seq));
@@ -303,8 +346,7 @@ __global__ __launch_bounds__(kThreads) void balance_sum_kernel(const SumArgs p) 
 // ---------------------------------------------------------------- gradient
 struct GradArgs {
   int64_t T;
-  RowMap m;
-  int n_seq;
+  int E, log_lpt, n_seq;
   const float* logits;
   const float* offset;
   const int32_t* seq;
@@ -318,72 +360,57 @@ struct GradArgs {
 constexpr int kGradThreads = 256;
 constexpr int kGradWaves = kGradThreads / kWave;
 
-// A lane group takes U tokens, all their loads in flight before the first use.
-template <int NR, int U>
+// One token a lane group; the loads of its logits and of the gradient to add
+// are issued first, under the search for its sequence.
+template <int NR, bool FULL, bool ADD>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const GradArgs p) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int E = p.m.E, lpt = p.m.lpt, tpw = kWave / lpt, sub = lane & (lpt - 1), which = lane >> p.m.log_lpt;
-  const int64_t t0 = ((int64_t)blockIdx.x * kGradWaves + wave) * (U * tpw) + which;
-  float l[U][NR][4], x[U][NR][4];
-#pragma unroll
-  for (int v = 0; v < U; ++v) {
-    const int64_t t = t0 + v * tpw;
-    load_row<NR>(p.logits + t * E, p.m, sub, t < p.T, 0.0f, l[v]);
-    load_row<NR>(p.extra + t * E, p.m, sub, t < p.T && p.extra != nullptr, 0.0f, x[v]);
-  }
+  const RowMap<NR, FULL> m(p.E, p.log_lpt);
+  const int64_t t = ((int64_t)blockIdx.x * kGradWaves + (threadIdx.x >> 6)) * (kWave / m.lpt) + m.which;
+  const int64_t at = min(t, p.T - 1) * p.E;
+  float l[NR][4], x[NR][4] = {}, off[NR][4] = {}, dp[NR][4];
+  m.load(p.logits + at, l);
+  if constexpr (ADD) m.load(p.extra + at, x);
+  if (p.offset != nullptr) m.load(p.offset, off);
   const float g = p.grad == nullptr ? 1.0f : *p.grad;
+  const uint8_t on = p.mask == nullptr ? 1 : p.mask[min(t, p.T - 1)];
+  int s = sequence_of(t, p.T, p.seq, p.n_seq);
+  if (on == 0) s = -1;
+  m.load(p.dprob + (int64_t)max(s, 0) * p.E, dp);
+  float total = 0.0f, dot = 0.0f;
 #pragma unroll
-  for (int v = 0; v < U; ++v) {
-    const int64_t t = t0 + v * tpw;
-    int s = sequence_of(t, p.T, p.seq, p.n_seq);
-    if (s >= 0 && p.mask != nullptr && p.mask[t] == 0) s = -1;
-    float dp[NR][4], da[NR][4];
-    load_row<NR>(p.dprob + (int64_t)s * E, p.m, sub, s >= 0, 0.0f, dp);
-    float total = 0.0f, dot = 0.0f;
+  for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = r * 256 + sub * 4 + j;
-        if (p.offset != nullptr && e < E) l[v][r][j] += p.offset[e];
-        Affinity a = affinity<true>(l[v][r][j]);
-        if (e >= E) a.a = 0.0f;
-        da[r][j] = a.da;
-        total += a.a;
-        dot = __builtin_fmaf(dp[r][j], a.a, dot);
-      }
-    total = group_sum(total, lpt);
-    dot = group_sum(dot, lpt);
-    const bool some = s >= 0 && total > 0.0f;
-    const float inv = some ? 1.0f / total : 0.0f;
-    const float mean = dot * inv, scale = g * inv;
-    if (t >= p.T) continue;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int e = r * 256 + sub * 4;
-      u32x4 o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[j] = __float_as_uint(x[v][r][j] + (some ? scale * (dp[r][j] - mean) * da[r][j] : 0.0f));
-      float* at = p.dl + t * E + e;
-      if (e + 4 <= E) {
-        *reinterpret_cast<u32x4_a4*>(at) = o;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (e + j < E) at[j] = __uint_as_float(o[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const Affinity a = affinity<true>(l[r][j] + off[r][j]);
+      const float own = m.owns(r, j) ? a.a : 0.0f;
+      l[r][j] = a.da;
+      total += own;
+      dot = __builtin_fmaf(dp[r][j], own, dot);
     }
-  }
+  total = group_sum(total, m.lpt);
+  dot = group_sum(dot, m.lpt);
+  const bool some = s >= 0 && total > 0.0f;
+  const float inv = some ? 1.0f / total : 0.0f;
+  const float mean = dot * inv, scale = g * inv;
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = scale * (dp[r][j] - mean) * l[r][j];
+      x[r][j] += some ? v : 0.0f;
+    }
+  if (t < p.T) m.store(p.dl + at, x);
 }
 
-RowMap row_map(int E) {
-  int lpt = 1, lg = 0;
-  while (lpt < kWave && lpt * 4 < E) {
-    lpt <<= 1;
-    ++lg;
-  }
-  return {E, lpt, lg};
+// lanes of a token: a power of two that covers E in fours
+int lanes_log(int E) {
+  int lg = 0;
+  while (lg < 6 && (4 << lg) < E) ++lg;
+  return lg;
+}
+bool full_rows(int E) {
+  const int lane4 = 4 << lanes_log(E);
+  return E == lane4 || E == 512 || E == 1024;
 }
 
 // expert columns of a slice: 2^log_w
@@ -398,14 +425,14 @@ struct LossWs {
 };
 LossWs loss_ws(int64_t T, int E, int n_seq) {
   const size_t rows = static_cast<size_t>((T + kTile - 1) / kTile) + n_seq;
-  const size_t slices = (E + (1 << slice_log(E)) - 1) >> slice_log(E);
+  const size_t groups = static_cast<size_t>(kSumGroups) * ((E + (1 << slice_log(E)) - 1) >> slice_log(E));
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   LossWs w;
   w.psum = 0;
   w.pcnt = up(rows * E * sizeof(float));
   w.ptok = w.pcnt + up(rows * E * sizeof(int32_t));
   w.part = w.ptok + up(rows * sizeof(int32_t));
-  w.ticket = w.part + up(n_seq * slices * sizeof(float));
+  w.ticket = w.part + up(groups * sizeof(float));
   w.total = w.ticket + 256;
   return w;
 }
@@ -425,31 +452,47 @@ hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, con
   int* ticket = reinterpret_cast<int*>(base + w.ticket);
   // at least one work-group: it resets the ticket
   const int64_t tiles = T > 0 ? (T + kTile - 1) / kTile : 1;
-  const LossArgs a{T, row_map(E), k, n_seq, logits, offset, idx, seq, mask, psum, pcnt, ptok, ticket};
+  const LossArgs a{T, E, lanes_log(E), k, n_seq, logits, offset, idx, seq, mask, psum, pcnt, ptok, ticket};
   const dim3 grid(static_cast<unsigned>(tiles)), block(kThreads);
-  if (E <= 256) hipLaunchKernelGGL(balance_part_kernel<1>, grid, block, 0, s, a);
-  else if (E <= 512) hipLaunchKernelGGL(balance_part_kernel<2>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(balance_part_kernel<4>, grid, block, 0, s, a);
+  auto part = [&](auto full) {
+    constexpr bool F = decltype(full)::value;
+    if (E <= 256) hipLaunchKernelGGL((balance_part_kernel<1, F>), grid, block, 0, s, a);
+    else if (E <= 512) hipLaunchKernelGGL((balance_part_kernel<2, F>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((balance_part_kernel<4, F>), grid, block, 0, s, a);
+  };
+  if (full_rows(E)) part(std::true_type{});
+  else part(std::false_type{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int lg = slice_log(E);
   const SumArgs b{T,    E,    k,      n_seq, lg,    alpha,  seq, psum, pcnt,
                   ptok, counts, prob, dprob, reinterpret_cast<float*>(base + w.part), ticket, loss};
-  hipLaunchKernelGGL(balance_sum_kernel, dim3(n_seq, (E + (1 << lg) - 1) >> lg), block, 0, s, b);
+  // threads for about four parts each of a sequence of average length
+  int threads = kWave;
+  while (threads < kThreads && (threads >> lg) * 4 < tiles / n_seq) threads *= 2;
+  const dim3 sums(n_seq < kSumGroups ? n_seq : kSumGroups, (E + (1 << lg) - 1) >> lg);
+  hipLaunchKernelGGL(balance_sum_kernel, sums, dim3(threads), 0, s, b);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_loss_bwd(int64_t T, int E, const float* logits, const float* offset, const int32_t* seq,
                                    int n_seq, const uint8_t* mask, const float* dprob, const float* grad,
                                    const float* extra, float* dl, hipStream_t s) {
-  const GradArgs a{T, row_map(E), n_seq, logits, offset, seq, mask, dprob, grad, extra, dl};
-  auto go = [&](auto kernel, int u) {
-    const int64_t per = (int64_t)kGradWaves * u * (kWave / a.m.lpt);
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((T + per - 1) / per)), dim3(kGradThreads), 0, s, a);
+  const GradArgs a{T, E, lanes_log(E), n_seq, logits, offset, seq, mask, dprob, grad, extra, dl};
+  const int64_t per = (int64_t)kGradWaves * (kWave >> a.log_lpt);
+  const dim3 grid(static_cast<unsigned>((T + per - 1) / per)), block(kGradThreads);
+  auto go = [&](auto full, auto add) {
+    constexpr bool F = decltype(full)::value, A = decltype(add)::value;
+    if (E <= 256) hipLaunchKernelGGL((balance_grad_kernel<1, F, A>), grid, block, 0, s, a);
+    else if (E <= 512) hipLaunchKernelGGL((balance_grad_kernel<2, F, A>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((balance_grad_kernel<4, F, A>), grid, block, 0, s, a);
   };
-  if (E <= 256) go(balance_grad_kernel<1, 2>, 2);
-  else if (E <= 512) go(balance_grad_kernel<2, 1>, 1);
-  else go(balance_grad_kernel<4, 1>, 1);
+  auto with = [&](auto full) {
+    if (extra != nullptr) go(full, std::true_type{});
+    else go(full, std::false_type{});
+  };
+  if (full_rows(E)) with(std::true_type{});
+  else with(std::false_type{});
   return hipGetLastError();
 }
 

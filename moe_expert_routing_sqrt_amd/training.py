@@ -8,17 +8,24 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from . import (MOE_E4M3, MOE_F32, MOE_FP8_TILE, MOE_OP_LAYER_NORM_BACKWARD, MoeShape, _dt, _lib, _need, _ptr,
-               _stream, _ws_len, lib, workspace_bytes)
+from . import (MOE_E4M3, MOE_F32, MOE_FP8_TILE, MOE_OP_LAYER_NORM_BACKWARD, MoeShape, _dt, _lib, _need, _stream,
+               lib, workspace_bytes)
+from . import _ptr as _checked_ptr
 from .layer import MoELayer
 
-_f32 = torch.float32
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
 
 
-def _need_f32(t: Optional[torch.Tensor], numel: int, name: str):
-    if t is not None and t.dtype != _f32:
-        raise TypeError(f"{name} must be fp32")
-    _need(t, numel, name)
+def _arg(t: Optional[torch.Tensor], numel: int, name: str, dtype: Optional[torch.dtype] = None) -> int:
+    """The pointer of a tensor argument (0 for None) once its size, type, device
+    and layout are checked."""
+    if t is None:
+        return 0
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    if t.numel() < numel:
+        _need(t, numel, name)  # raises
+    return _checked_ptr(t)
 
 
 # ---------------------------------------------------------------- layer norm
@@ -33,28 +40,22 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     d = x.shape[-1]
     n = x.numel()
     rows = n // d if d else 0
-    dev = x.device
-    if residual is not None and residual.dtype != x.dtype:
-        raise TypeError("residual must have x's dtype")
+    dt = x.dtype
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out needs a residual")
+    r_p, w_p, b_p = _arg(residual, n, "residual", dt), _arg(weight, d, "weight", _f32), _arg(bias, d, "bias", _f32)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
+        y = torch.empty_like(x) if y_dtype is None or y_dtype == dt else torch.empty_like(x, dtype=y_dtype)
     if residual is not None and sum_out is None:
         sum_out = torch.empty_like(x)
-    if sum_out is not None and (residual is None or sum_out.dtype != x.dtype):
-        raise ValueError("sum_out needs a residual and x's dtype")
-    if keep_stats and mean is None:
-        mean = torch.empty(rows, dtype=_f32, device=dev)
-    if keep_stats and rstd is None:
-        rstd = torch.empty(rows, dtype=_f32, device=dev)
-    _need(residual, n, "residual")
-    _need(sum_out, n, "sum_out")
-    _need(y, n, "y")
-    _need_f32(weight, d, "weight")
-    _need_f32(bias, d, "bias")
-    _need_f32(mean, rows, "mean")
-    _need_f32(rstd, rows, "rstd")
-    st = lib().moe_layer_norm(rows, d, _ptr(x), _ptr(residual), _dt(x), _ptr(weight), _ptr(bias), eps, _ptr(sum_out),
-                              _ptr(y), _dt(y), _ptr(mean), _ptr(rstd), _stream())
+    if keep_stats:
+        if mean is None:
+            mean = weight.new_empty(rows)
+        if rstd is None:
+            rstd = weight.new_empty(rows)
+    st = lib().moe_layer_norm(rows, d, _arg(x, n, "x"), r_p, _dt(x), w_p, b_p, eps,
+                              _arg(sum_out, n, "sum_out", dt), _arg(y, n, "y"), _dt(y),
+                              _arg(mean, rows, "mean", _f32), _arg(rstd, rows, "rstd", _f32), _stream())
     _lib.check("moe_layer_norm", st)
     return y, x if residual is None else sum_out, mean, rstd
 
@@ -71,42 +72,33 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     d = x.shape[-1]
     n = x.numel()
     rows = n // d if d else 0
-    dev = x.device
-    if d_sum is not None and d_sum.dtype != x.dtype:
-        raise TypeError("d_sum must have x's dtype")
+    dt = x.dtype
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype if dx_dtype is None else dx_dtype, device=dev)
+        dx = torch.empty_like(x) if dx_dtype is None or dx_dtype == dt else torch.empty_like(x, dtype=dx_dtype)
     if dw is None:
-        dw = torch.empty(d, dtype=_f32, device=dev)
+        dw = torch.empty_like(weight)
     if db is None and has_bias:
-        db = torch.empty(d, dtype=_f32, device=dev)
+        db = torch.empty_like(weight)
     if ws is None and rows > 0:
-        sh = MoeShape(rows, d, 1, 1, 1, 1, 1, 1)
-        ws = torch.empty(workspace_bytes(MOE_OP_LAYER_NORM_BACKWARD, sh), dtype=torch.uint8, device=dev)
-    _need(dy, n, "dy")
-    _need(d_sum, n, "d_sum")
-    _need(dx, n, "dx")
-    _need_f32(weight, d, "weight")
-    _need_f32(mean, rows, "mean")
-    _need_f32(rstd, rows, "rstd")
-    _need_f32(dw, d, "dw")
-    _need_f32(db, d, "db")
-    st = lib().moe_layer_norm_backward(rows, d, _ptr(dy), _dt(dy), _ptr(x), _dt(x), _ptr(weight), _ptr(mean),
-                                       _ptr(rstd), _ptr(d_sum), _ptr(dx), _dt(dx), _ptr(dw), _ptr(db), _ptr(ws),
-                                       _ws_len(ws), _stream())
+        ws = weight.new_empty(workspace_bytes(MOE_OP_LAYER_NORM_BACKWARD, MoeShape(rows, d, 1, 1, 1, 1, 1, 1)) // 4)
+    st = lib().moe_layer_norm_backward(rows, d, _arg(dy, n, "dy"), _dt(dy), _arg(x, n, "x"), _dt(x),
+                                       _arg(weight, d, "weight", _f32), _arg(mean, rows, "mean", _f32),
+                                       _arg(rstd, rows, "rstd", _f32), _arg(d_sum, n, "d_sum", dt),
+                                       _arg(dx, n, "dx"), _dt(dx), _arg(dw, d, "dw", _f32), _arg(db, d, "db", _f32),
+                                       _arg(ws, 0, "ws"), 0 if ws is None else ws.numel() * ws.element_size(),
+                                       _stream())
     _lib.check("moe_layer_norm_backward", st)
     return dx, dw, db
 
 
 # ---------------------------------------------------------------- balance loss
 
-def _sequences(sh: MoeShape, seq_offsets, token_mask) -> int:
-    if seq_offsets is not None and seq_offsets.dtype != torch.int32:
-        raise TypeError("seq_offsets must be int32")
-    if token_mask is not None and token_mask.dtype not in (torch.bool, torch.uint8):
+def _sequences(T: int, seq_offsets, token_mask):
+    """(number of sequences, offsets pointer, mask pointer)"""
+    if token_mask is not None and token_mask.dtype not in (torch.bool, _u8):
         raise TypeError("token_mask must be bool or uint8")
-    _need(token_mask, sh.T, "token_mask")
-    return 1 if seq_offsets is None else seq_offsets.numel() - 1
+    n = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    return n, _arg(seq_offsets, 2, "seq_offsets", _i32), _arg(token_mask, T, "token_mask")
 
 
 def balance_loss(sh: MoeShape, logits: torch.Tensor, idx: torch.Tensor, alpha: float,
@@ -119,33 +111,25 @@ def balance_loss(sh: MoeShape, logits: torch.Tensor, idx: torch.Tensor, alpha: f
     [n, E], dprob [n, E]); dprob is what balance_loss_backward needs.
     Tokens outside the sequences or with token_mask 0 do not count."""
     T, E, k = sh.T, sh.E, sh.k
-    dev = logits.device
-    n = _sequences(sh, seq_offsets, token_mask)
-    if idx.dtype != torch.int32:
+    if idx.dtype != _i32:
         raise TypeError("idx must be int32")
+    n, off_p, mask_p = _sequences(T, seq_offsets, token_mask)
+    L, shape = lib(), ctypes.byref(sh)
     if loss is None:
-        loss = torch.empty(1, dtype=_f32, device=dev)
+        loss = logits.new_empty(1)
     if counts is None:
-        counts = torch.empty((n, E), dtype=torch.int32, device=dev)
+        counts = idx.new_empty((n, E))
     if prob is None:
-        prob = torch.empty((n, E), dtype=_f32, device=dev)
+        prob = logits.new_empty((n, E))
     if dprob is None:
-        dprob = torch.empty((n, E), dtype=_f32, device=dev)
+        dprob = torch.empty_like(prob)
     if ws is None:
-        ws = torch.empty(max(256, lib().moe_balance_loss_workspace_size(ctypes.byref(sh), n)), dtype=torch.uint8,
-                         device=dev)
-    if counts.dtype != torch.int32:
-        raise TypeError("counts must be int32")
-    _need_f32(logits, T * E, "logits")
-    _need(idx, T * k, "idx")
-    _need_f32(logit_offset, E, "logit_offset")
-    _need_f32(loss, 1, "loss")
-    _need(counts, n * E, "counts")
-    _need_f32(prob, n * E, "prob")
-    _need_f32(dprob, n * E, "dprob")
-    st = lib().moe_balance_loss(ctypes.byref(sh), _ptr(logits), _ptr(logit_offset), _ptr(idx), _ptr(seq_offsets), n,
-                                _ptr(token_mask), alpha, _ptr(counts), _ptr(prob), _ptr(dprob), _ptr(loss), _ptr(ws),
-                                _ws_len(ws), _stream())
+        ws = logits.new_empty(max(1, L.moe_balance_loss_workspace_size(shape, n) // 4))
+    m = n * E
+    st = L.moe_balance_loss(shape, _arg(logits, T * E, "logits", _f32), _arg(logit_offset, E, "logit_offset", _f32),
+                            _arg(idx, T * k, "idx"), off_p, n, mask_p, alpha, _arg(counts, m, "counts", _i32),
+                            _arg(prob, m, "prob", _f32), _arg(dprob, m, "dprob", _f32), _arg(loss, 1, "loss", _f32),
+                            _arg(ws, 0, "ws"), ws.numel() * ws.element_size(), _stream())
     _lib.check("moe_balance_loss", st)
     return loss, counts, prob, dprob
 
@@ -158,18 +142,15 @@ def balance_loss_backward(sh: MoeShape, logits: torch.Tensor, dprob: torch.Tenso
     """dlogits [T, E] = d_extra + the balance loss's gradient times grad_loss
     ([1] fp32 on the device; None: 1).  dlogits may be d_extra."""
     T, E = sh.T, sh.E
-    n = _sequences(sh, seq_offsets, token_mask)
+    n, off_p, mask_p = _sequences(T, seq_offsets, token_mask)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=_f32, device=logits.device)
-    _need_f32(logits, T * E, "logits")
-    _need_f32(logit_offset, E, "logit_offset")
-    _need_f32(dprob, n * E, "dprob")
-    _need_f32(grad_loss, 1, "grad_loss")
-    _need_f32(d_extra, T * E, "d_extra")
-    _need_f32(dlogits, T * E, "dlogits")
-    st = lib().moe_balance_loss_backward(ctypes.byref(sh), _ptr(logits), _ptr(logit_offset), _ptr(seq_offsets), n,
-                                         _ptr(token_mask), _ptr(dprob), _ptr(grad_loss), _ptr(d_extra),
-                                         _ptr(dlogits), _stream())
+        dlogits = logits.new_empty((T, E))
+    m = T * E
+    st = lib().moe_balance_loss_backward(ctypes.byref(sh), _arg(logits, m, "logits", _f32),
+                                         _arg(logit_offset, E, "logit_offset", _f32), off_p, n, mask_p,
+                                         _arg(dprob, n * E, "dprob", _f32), _arg(grad_loss, 1, "grad_loss", _f32),
+                                         _arg(d_extra, m, "d_extra", _f32), _arg(dlogits, m, "dlogits", _f32),
+                                         _stream())
     _lib.check("moe_balance_loss_backward", st)
     return dlogits
 
@@ -233,21 +214,20 @@ class AdamW:
             for t, name in ((self.grads[i], "grad"), (self.m[i], "m"), (self.v[i], "v")):
                 if t.numel() != k:
                     raise ValueError(f"{name} {i}: needs {k} elements, has {t.numel()}")
-            _need_f32(self.master[i], k, "master")
-            if eight[i]:
-                _need_f32(self.m_scale[i], tiles(p), "m_scale")
-                _need_f32(self.v_scale[i], tiles(p), "v_scale")
             self._items[i] = _lib.MoeAdamwTensor(
-                k, _ptr(p), _ptr(self.grads[i]), _ptr(self.master[i]), _ptr(self.m[i]), _ptr(self.v[i]),
-                _ptr(self.m_scale[i]), _ptr(self.v_scale[i]), wd[i], _dt(p), _dt(self.grads[i]), _dt(self.m[i]), 0)
+                k, _arg(p, k, "param"), _arg(self.grads[i], k, "grad"), _arg(self.master[i], k, "master", _f32),
+                _arg(self.m[i], k, "m"), _arg(self.v[i], k, "v"),
+                _arg(self.m_scale[i], tiles(p), "m_scale", _f32) if eight[i] else 0,
+                _arg(self.v_scale[i], tiles(p), "v_scale", _f32) if eight[i] else 0,
+                wd[i], _dt(p), _dt(self.grads[i]), _dt(self.m[i]), 0)
 
     def step(self, grad_scale: Optional[torch.Tensor] = None, lr: Optional[float] = None) -> None:
         """One step on what the gradient buffers hold, times grad_scale ([1]
         fp32 on the device).  lr: this step's rate (else the constructor's)."""
-        _need_f32(grad_scale, 1, "grad_scale")
         h = _lib.MoeAdamwParams(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
                                 self.step_count + 1)
-        st = lib().moe_adamw_step(len(self.params), self._items, ctypes.byref(h), _ptr(grad_scale), _stream())
+        st = lib().moe_adamw_step(len(self.params), self._items, ctypes.byref(h),
+                                  _arg(grad_scale, 1, "grad_scale", _f32), _stream())
         _lib.check("moe_adamw_step", st)
         self.step_count += 1
 
