@@ -39,13 +39,17 @@ __device__ __forceinline__ Piece piece_of(int i, int d) {
 }
 __device__ __forceinline__ bool owns(const Piece& q, int j) { return j >= q.lo && j < q.hi; }
 
-// loads the piece (zeros where there is none, or past hi)
+// Loads the piece (zeros where there is none, or past hi).  STREAM: past the
+// caches; without it data that is still in the 256 MB cache of the package, as
+// a kernel before left it, is found there.
+template <bool STREAM>
 __device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* p, const Piece& q) {
   r.a = u32x4{0, 0, 0, 0};
   if (q.lo >= 8) return;
   p += q.c;
   if (q.hi == 8) {
-    r.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+    if constexpr (STREAM) r.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+    else r.a = *reinterpret_cast<const u32x4_a2*>(p);
   } else {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -54,7 +58,7 @@ __device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* p, cons
     r.a = u32x4{w[0], w[1], w[2], w[3]};
   }
 }
-template <bool STREAM = true>
+template <bool STREAM>
 __device__ __forceinline__ void load8(Raw8<float>& r, const float* p, const Piece& q) {
   r.a = r.b = u32x4{0, 0, 0, 0};
   if (q.lo >= 8) return;
@@ -63,7 +67,7 @@ __device__ __forceinline__ void load8(Raw8<float>& r, const float* p, const Piec
     if constexpr (STREAM) {
       r.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p));
       r.b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p + 4));
-    } else {  // what many work-groups read
+    } else {
       r.a = *reinterpret_cast<const u32x4_a4*>(p);
       r.b = *reinterpret_cast<const u32x4_a4*>(p + 4);
     }
@@ -103,11 +107,11 @@ __device__ __forceinline__ void from_f32(Raw8<float>& r, const float (&f)[8]) {
   }
 }
 
-// stores the elements the piece owns
+// stores the elements the piece owns, past the caches
 __device__ __forceinline__ void store8(uint16_t* p, const Raw8<uint16_t>& r, const Piece& q) {
   p += q.c;
   if (q.lo == 0 && q.hi == 8) {
-    *reinterpret_cast<u32x4_a2*>(p) = r.a;
+    __builtin_nontemporal_store(r.a, reinterpret_cast<u32x4_a2*>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -117,8 +121,8 @@ __device__ __forceinline__ void store8(uint16_t* p, const Raw8<uint16_t>& r, con
 __device__ __forceinline__ void store8(float* p, const Raw8<float>& r, const Piece& q) {
   p += q.c;
   if (q.lo == 0 && q.hi == 8) {
-    *reinterpret_cast<u32x4_a4*>(p) = r.a;
-    *reinterpret_cast<u32x4_a4*>(p + 4) = r.b;
+    __builtin_nontemporal_store(r.a, reinterpret_cast<u32x4_a4*>(p));
+    __builtin_nontemporal_store(r.b, reinterpret_cast<u32x4_a4*>(p + 4));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
