@@ -14,6 +14,7 @@
 // then the centred squares are summed from registers; two sums instead of one
 // of squares keep the variance exact when the mean is large.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "stream8.h"
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_fwd_kernel(const NormAr
 // ---------------------------------------------------------------- backward
 struct NormBwdArgs {
   int64_t rows;
-  int d;
+  int d, wpr, rpb;  // waves per row, rows at once in a work-group
   const void* dy;
   const void* x;
   const float* w;
@@ -166,24 +167,25 @@ struct NormBwdArgs {
 // registers; their sums leave once at the end.  With one piece a lane the
 // weights stay there too, and the next row's loads are issued before this one
 // is reduced; wider rows have no registers for either (beyond d = 16384 they
-// spill).  MULTI (rows of one wave): each of the work-group's
-// waves takes rows of its own, and their sums are joined in LDS, so that the
-// parts stay one per work-group.
-constexpr int kMultiRows = 8;
+// spill).  MULTI (rows of at most 4 waves): the work-group's 8 waves take several
+// rows at once, side by side, and join their sums in LDS, so that the parts
+// stay one per work-group.
+constexpr int kMultiWaves = 8;
 template <typename TD, typename TX, typename TO, bool DS, int N, bool MULTI, bool STREAM>
 __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBwdArgs p) {
   __shared__ float s_red[2][2][kMaxWaves];
-  __shared__ float s_part[MULTI ? kMultiRows : 1][MULTI ? 8 * kWave : 1];
-  const int wave = threadIdx.x >> 6, waves = MULTI ? 1 : blockDim.x >> 6;
-  const int tid = MULTI ? threadIdx.x & 63 : threadIdx.x;  // thread within the row
+  __shared__ float s_part[MULTI ? kMultiWaves * kWave * 8 : 1];
+  const int wave = threadIdx.x >> 6, waves = MULTI ? p.wpr : blockDim.x >> 6;
+  const int slot = MULTI ? wave / waves : 0;  // the row's place in the work-group
   const int width = waves * kWave;
-  if (!MULTI && tid < 4 * kMaxWaves) (&s_red[0][0][0])[tid] = 0.0f;
+  const int tid = threadIdx.x - slot * width;  // thread within the row
+  if (threadIdx.x < 4 * kMaxWaves) (&s_red[0][0][0])[threadIdx.x] = 0.0f;
   __syncthreads();
   const TD* const dy = static_cast<const TD*>(p.dy);
   const TX* const x = static_cast<const TX*>(p.x);
   const TX* const ds = static_cast<const TX*>(p.ds);
-  const int64_t step = (int64_t)gridDim.x * (MULTI ? kMultiRows : 1);
-  int64_t row = MULTI ? (int64_t)blockIdx.x * kMultiRows + wave : blockIdx.x;
+  const int64_t step = (int64_t)gridDim.x * (MULTI ? p.rpb : 1);
+  int64_t row = MULTI ? (int64_t)blockIdx.x * p.rpb + slot : blockIdx.x;
   Piece q[N];
   Raw8<TD> rd[N];
   Raw8<TX> rx[N], rs[DS ? N : 1];
@@ -217,7 +219,9 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
     for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
   }
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  for (int buf = 0; row < p.rows; row += step, buf ^= 1) {
+  // row - slot: the same in all waves, which meet at the barriers
+  for (int buf = 0; row - slot < p.rows; row += step, buf ^= 1) {
+    const bool in = !MULTI || row < p.rows;
     const int64_t base = row * p.d;
     float xh[N][8], g[N][8], res[DS ? N : 1][8];
     float c1 = 0.0f, c2 = 0.0f;
@@ -225,6 +229,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
     const float rs1 = rstd;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      if (!in) break;
       if constexpr (!kAhead) weights(i, w[0]);
       float (&wi)[8] = w[0];
       to_f32(rd[i], g[i]);
@@ -252,9 +257,12 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
         s_red[buf][1][wave] = c2;
       }
       __syncthreads();  // the other buffer is free again once all waves are here
-      c1 = row16_sum(s_red[buf][0][tid & 15]);
-      c2 = row16_sum(s_red[buf][1][tid & 15]);
+      const bool mine = !MULTI || (tid & 15) < waves;
+      const int at = !mine ? 0 : MULTI ? slot * waves + (tid & 15) : tid & 15;
+      c1 = row16_sum(mine ? s_red[buf][0][at] : 0.0f);
+      c2 = row16_sum(mine ? s_red[buf][1][at] : 0.0f);
     }
+    if (!in) continue;
     c1 *= inv_d;
     c2 *= inv_d;
 #pragma unroll
@@ -275,12 +283,11 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (owns(q[0], j)) s_part[wave][q[0].c + j] = h == 0 ? dw[0][j] : db[0][j];
+        if (owns(q[0], j)) s_part[slot * p.d + q[0].c + j] = h == 0 ? dw[0][j] : db[0][j];
       __syncthreads();
-      for (int c = threadIdx.x; c < p.d; c += kMultiRows * kWave) {
-        float v = s_part[0][c];
-#pragma unroll
-        for (int k = 1; k < kMultiRows; ++k) v += s_part[k][c];
+      for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+        float v = s_part[c];
+        for (int k = 1; k < p.rpb; ++k) v += s_part[k * p.d + c];
         part[h * p.d + c] = v;
       }
       __syncthreads();
@@ -298,8 +305,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
 }
 
 // dw and db as the sums of the work-groups' parts: 64 columns a work-group, each
-// of its 16 waves adds every 16th part in order (8 loads in flight), then the
-// waves in order.
+// of its 16 waves adds every 16th part in order (16 loads in flight: all of them
+// at 256 parts), then the waves in order.
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(kSumWaves* kWave) void norm_param_grad_kernel(const float* part, int parts, int d,
                                                                           float* dw, float* db) {
@@ -307,18 +314,22 @@ __global__ __launch_bounds__(kSumWaves* kWave) void norm_param_grad_kernel(const
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * kWave + lane;  // column of [dw | db]
   float v = 0.0f;
-  if (c < 2 * d) {
+  if (c < 2 * d && parts > 0) {  // no rows: no parts to read, and no workspace
     const int64_t pitch = 2 * (int64_t)d;
     const float* at = part + c;
-    int g = wave;
-    for (; g + 7 * kSumWaves < parts; g += 8 * kSumWaves) {
-      float t[8];
+    auto batch = [&](auto n, int g) __attribute__((always_inline)) {
+      constexpr int B = decltype(n)::value;
+      float t[B];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = at[(g + i * kSumWaves) * pitch];
+      for (int i = 0; i < B; ++i) t[i] = at[min(g + i * kSumWaves, parts - 1) * pitch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v += t[i];
+      for (int i = 0; i < B; ++i) v += g + i * kSumWaves < parts ? t[i] : 0.0f;
+    };
+    if (parts <= 4 * kSumWaves) {
+      batch(std::integral_constant<int, 4>{}, wave);
+    } else {
+      for (int g = wave; g < parts; g += 16 * kSumWaves) batch(std::integral_constant<int, 16>{}, g);
     }
-    for (; g < parts; g += kSumWaves) v += at[g * pitch];
   }
   s_sum[wave][lane] = v;
   __syncthreads();
@@ -355,16 +366,18 @@ struct BwdShape {
   int64_t groups;
 };
 // One piece a lane while a row then fits 16 waves (d <= 8192): two need over
-// 128 registers (16384 x 7168: 206 us against 400).  One work-group per CU
-// keeps the parts few (256: 206 + 5 us, 512: 223 + 9); narrow rows take two, to
-// have enough loads in flight.
+// 128 registers (16384 x 7168: 206 us against 400).  Rows of up to 4 waves go
+// side by side in work-groups of 8 (16384 x 1024 bf16: 28 us against 35).  One
+// work-group per CU keeps the parts few (16384 x 7168: 206 + 5 us, 223 + 9 with
+// two; 65536 x 2048 fp32: 293 against 337); rows of one wave take two (16000 x
+// 257: 14.2 against 15.0).
 BwdShape bwd_shape(int64_t rows, int d) {
   const int pieces = (d + 7) / 8;
   int n = 1;
   while (pieces > n * kWave * kMaxWaves) n *= 2;
   const int waves = (pieces + n * kWave - 1) / (n * kWave);
-  const int rpb = waves == 1 ? kMultiRows : 1;
-  const int64_t need = (rows + rpb - 1) / rpb, fill = 256 * (waves < 4 ? 2 : 1);
+  const int rpb = waves <= kMultiWaves / 2 ? kMultiWaves / waves : 1;
+  const int64_t need = (rows + rpb - 1) / rpb, fill = waves == 1 ? 512 : 256;
   return {n, waves, rpb, need < fill ? need : fill};
 }
 
@@ -431,7 +444,7 @@ hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dty
                                  int dx_dtype, float* dw, float* db, float* ws, hipStream_t s) {
   const BwdShape b = bwd_shape(rows, d);
   if (b.groups > 0) {
-    const NormBwdArgs a{rows, d, dy, x, w, mean, rstd, ds, dx, ws};
+    const NormBwdArgs a{rows, d, b.waves, b.rpb, dy, x, w, mean, rstd, ds, dx, ws};
     const int key = (dy_dtype == MOE_BF16) | (x_dtype == MOE_BF16) << 1 | (dx_dtype == MOE_BF16) << 2;
     hipError_t e = hipSuccess;
     using B = uint16_t;
