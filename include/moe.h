@@ -568,10 +568,12 @@ int moe_layer_norm(int64_t rows, int32_t d, const void* x, const void* residual,
  *   dy       [rows, d] in dy_dtype;  x [rows, d] in x_dtype
  *   d_sum    [rows, d] in x_dtype or NULL: the gradient that reaches the sum
  *            past the norm; dx is then the gradient of both x and residual
- *   dx       [rows, d] in dx_dtype out; may be dy or d_sum where the types agree
+ *   dx       [rows, d] in dx_dtype out; may be d_sum where the types agree, not
+ *            dy or x
  *   dweight, dbias [d] fp32 out (dbias may be NULL); zeros with rows = 0
  *   ws       moe_workspace_size(MOE_OP_LAYER_NORM_BACKWARD, shape, 0) bytes
- *            with the shape's T = rows: the parts of dweight and dbias
+ *            with the shape's T = rows: the parts of dweight and dbias (0 for
+ *            few rows, which need none: ws may be NULL)
  * Each type MOE_BF16 or MOE_F32; d as moe_layer_norm.  All sums in fp32 and in
  * a fixed order (deterministic).
  */

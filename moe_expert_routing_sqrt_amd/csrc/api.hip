@@ -644,8 +644,9 @@ int moe_layer_norm_backward(int64_t rows, int32_t d, const void* dy, int dy_dtyp
   if (rows > 0) {
     if (dy == nullptr || x == nullptr || weight == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr)
       return MOE_ERR_INVALID_ARG;
-    if (ws == nullptr || ws_bytes < layer_norm_bwd_workspace_bytes(rows, d) || !aligned256(ws))
-      return MOE_ERR_WORKSPACE;
+    if (dx == dy || dx == x) return MOE_ERR_INVALID_ARG;  // both are read while dx is written
+    const size_t need = layer_norm_bwd_workspace_bytes(rows, d);
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned256(ws))) return MOE_ERR_WORKSPACE;
   }
   return hip_status(launch_layer_norm_bwd(rows, d, dy, dy_dtype, x, x_dtype, weight, mean, rstd, d_sum, dx, dx_dtype,
                                           dweight, dbias, static_cast<float*>(ws), as_stream(stream)));

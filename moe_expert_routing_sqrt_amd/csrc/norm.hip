@@ -359,11 +359,102 @@ hipError_t fwd_n(const NormArgs& a, int n, dim3 grid, dim3 block, hipStream_t s)
   return hipGetLastError();
 }
 
+// The same for few rows in one launch: the first `row_groups` work-groups form
+// dx, a row each, and the others dw and db, 64 columns each, from the rows
+// again (they are still in cache), which needs no parts and no second launch.
+template <typename TD, typename TX, typename TO, bool DS>
+__global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_few_kernel(const NormBwdArgs p, int row_groups, float* dw,
+                                                                       float* db) {
+  __shared__ float s_red[2][kMaxWaves][kWave];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const TD* const dy = static_cast<const TD*>(p.dy);
+  const TX* const x = static_cast<const TX*>(p.x);
+  if (static_cast<int>(blockIdx.x) >= row_groups) {
+    // columns: each wave adds every waves-th row, then the waves in order
+    constexpr int B = 8;  // rows in flight
+    const int c = (blockIdx.x - row_groups) * kWave + lane, at = min(c, p.d - 1);
+    const int rows = static_cast<int>(p.rows);
+    float sw = 0.0f, sb = 0.0f;
+    for (int r0 = wave; r0 < rows; r0 += B * waves) {
+      float g[B], v[B], mean[B], rstd[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int r = min(r0 + i * waves, rows - 1);
+        g[i] = one_f32(dy[(int64_t)r * p.d + at]);
+        v[i] = one_f32(x[(int64_t)r * p.d + at]);
+        mean[i] = p.mean[r];
+        rstd[i] = p.rstd[r];
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        if (r0 + i * waves >= rows) continue;
+        sw = __builtin_fmaf(g[i], (v[i] - mean[i]) * rstd[i], sw);
+        sb += g[i];
+      }
+    }
+    s_red[0][wave][lane] = sw;
+    s_red[1][wave][lane] = sb;
+    __syncthreads();
+    if (wave == 0 && c < p.d) {
+      for (int w = 1; w < waves; ++w) {
+        sw += s_red[0][w][lane];
+        sb += s_red[1][w][lane];
+      }
+      dw[c] = sw;
+      if (db != nullptr) db[c] = sb;
+    }
+    return;
+  }
+  const int64_t row = blockIdx.x, base = row * p.d;
+  const Piece q = piece_of(threadIdx.x, p.d);
+  Raw8<TD> rd;
+  Raw8<TX> rx, rs;
+  Raw8<float> rw;
+  load8<false>(rd, dy + base, q);
+  load8<false>(rx, x + base, q);
+  if constexpr (DS) load8<false>(rs, static_cast<const TX*>(p.ds) + base, q);
+  load8<false>(rw, p.w, q);
+  const float mean = p.mean[row], rstd = p.rstd[row], inv_d = 1.0f / static_cast<float>(p.d);
+  float g[8], xh[8], w[8], c1 = 0.0f, c2 = 0.0f;
+  to_f32(rd, g);
+  to_f32(rx, xh);
+  to_f32(rw, w);
+  mask8(g, q);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    xh[j] = (xh[j] - mean) * rstd;
+    g[j] *= w[j];
+    c1 += g[j];
+    c2 = __builtin_fmaf(g[j], xh[j], c2);
+  }
+  c1 = wave_sum(c1);
+  c2 = wave_sum(c2);
+  if (lane == 0) {
+    s_red[0][0][wave] = c1;
+    s_red[0][1][wave] = c2;
+  }
+  __syncthreads();
+  c1 = row16_sum((lane & 15) < waves ? s_red[0][0][lane & 15] : 0.0f) * inv_d;
+  c2 = row16_sum((lane & 15) < waves ? s_red[0][1][lane & 15] : 0.0f) * inv_d;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = rstd * (g[j] - c1 - xh[j] * c2);
+  if constexpr (DS) {
+    float res[8];
+    to_f32(rs, res);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] += res[j];
+  }
+  Raw8<TO> o;
+  from_f32(o, g);
+  store8(static_cast<TO*>(p.dx) + base, o, q);
+}
+
 // launch shape of the backward: pieces of 8 a lane holds, waves of a row, rows
 // at once in a work-group, work-groups (= parts of the parameter gradients)
 struct BwdShape {
   int n, waves, rpb;
   int64_t groups;
+  bool few;  // the one-launch form, which has no parts
 };
 // One piece a lane while a row then fits 16 waves (d <= 8192): two need over
 // 128 registers (16384 x 7168: 206 us against 400).  Rows of up to 4 waves go
@@ -371,6 +462,9 @@ struct BwdShape {
 // work-group per CU keeps the parts few (16384 x 7168: 206 + 5 us, 223 + 9 with
 // two; 65536 x 2048 fp32: 293 against 337); rows of one wave take two (16000 x
 // 257: 14.2 against 15.0).
+// Up to 384 rows one launch forms everything (64 x 7168: 3.3 us against 8.1; 400 x
+// 1024: 7.0 against 8.2, 400 x 200: 6.8 against 6.4).
+constexpr int kFewRows = 384;
 BwdShape bwd_shape(int64_t rows, int d) {
   const int pieces = (d + 7) / 8;
   int n = 1;
@@ -378,11 +472,18 @@ BwdShape bwd_shape(int64_t rows, int d) {
   const int waves = (pieces + n * kWave - 1) / (n * kWave);
   const int rpb = waves <= kMultiWaves / 2 ? kMultiWaves / waves : 1;
   const int64_t need = (rows + rpb - 1) / rpb, fill = waves == 1 ? 512 : 256;
-  return {n, waves, rpb, need < fill ? need : fill};
+  return {n, waves, rpb, need < fill ? need : fill, rows > 0 && rows <= kFewRows && n == 1};
 }
 
 template <typename TD, typename TX, typename TO, bool DS>
-hipError_t bwd_n(const NormBwdArgs& a, const BwdShape& b, hipStream_t s) {
+hipError_t bwd_n(const NormBwdArgs& a, const BwdShape& b, float* dw, float* db, hipStream_t s) {
+  if (b.few) {
+    // at least 8 waves: the columns' rows are split over them
+    const int waves = b.waves > 8 ? b.waves : 8, rows = static_cast<int>(a.rows);
+    hipLaunchKernelGGL((norm_bwd_few_kernel<TD, TX, TO, DS>), dim3(rows + (a.d + kWave - 1) / kWave),
+                       dim3(waves * kWave), 0, s, a, rows, dw, db);
+    return hipGetLastError();
+  }
   const dim3 grid(static_cast<unsigned>(b.groups)), block(b.waves * b.rpb * kWave);
   const bool st = streams(static_cast<double>(a.rows) * a.d * (sizeof(TD) + sizeof(TX) * (DS ? 2 : 1) + sizeof(TO)));
   if (b.rpb > 1) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, true, false>), grid, block, 0, s, a);
@@ -394,8 +495,8 @@ hipError_t bwd_n(const NormBwdArgs& a, const BwdShape& b, hipStream_t s) {
 }
 
 template <typename TD, typename TX, typename TO>
-hipError_t bwd_ds(const NormBwdArgs& a, const BwdShape& b, hipStream_t s) {
-  return a.ds != nullptr ? bwd_n<TD, TX, TO, true>(a, b, s) : bwd_n<TD, TX, TO, false>(a, b, s);
+hipError_t bwd_ds(const NormBwdArgs& a, const BwdShape& b, float* dw, float* db, hipStream_t s) {
+  return a.ds != nullptr ? bwd_n<TD, TX, TO, true>(a, b, dw, db, s) : bwd_n<TD, TX, TO, false>(a, b, dw, db, s);
 }
 
 }  // namespace
@@ -436,7 +537,8 @@ hipError_t launch_layer_norm(int64_t rows, int d, const void* x, const void* r, 
 }
 
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int d) {
-  return static_cast<size_t>(bwd_shape(rows, d).groups) * 2 * d * sizeof(float);
+  const BwdShape b = bwd_shape(rows, d);
+  return b.few ? 0 : static_cast<size_t>(b.groups) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dtype, const void* x, int x_dtype,
@@ -449,16 +551,16 @@ hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dty
     hipError_t e = hipSuccess;
     using B = uint16_t;
     switch (key) {
-      case 0: e = bwd_ds<float, float, float>(a, b, s); break;
-      case 1: e = bwd_ds<B, float, float>(a, b, s); break;
-      case 2: e = bwd_ds<float, B, float>(a, b, s); break;
-      case 3: e = bwd_ds<B, B, float>(a, b, s); break;
-      case 4: e = bwd_ds<float, float, B>(a, b, s); break;
-      case 5: e = bwd_ds<B, float, B>(a, b, s); break;
-      case 6: e = bwd_ds<float, B, B>(a, b, s); break;
-      default: e = bwd_ds<B, B, B>(a, b, s); break;
+      case 0: e = bwd_ds<float, float, float>(a, b, dw, db, s); break;
+      case 1: e = bwd_ds<B, float, float>(a, b, dw, db, s); break;
+      case 2: e = bwd_ds<float, B, float>(a, b, dw, db, s); break;
+      case 3: e = bwd_ds<B, B, float>(a, b, dw, db, s); break;
+      case 4: e = bwd_ds<float, float, B>(a, b, dw, db, s); break;
+      case 5: e = bwd_ds<B, float, B>(a, b, dw, db, s); break;
+      case 6: e = bwd_ds<float, B, B>(a, b, dw, db, s); break;
+      default: e = bwd_ds<B, B, B>(a, b, dw, db, s); break;
     }
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || b.few) return e;
   }
   hipLaunchKernelGGL(norm_param_grad_kernel, dim3((2 * d + kWave - 1) / kWave), dim3(kSumWaves * kWave), 0, s, ws,
                      static_cast<int>(b.groups), d, dw, db);

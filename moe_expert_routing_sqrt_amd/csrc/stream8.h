@@ -95,6 +95,9 @@ __device__ __forceinline__ void to_f32(const Raw8<float>& r, float (&f)[8]) {
   }
 }
 
+__device__ __forceinline__ float one_f32(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ float one_f32(float v) { return v; }
+
 // rounded to the stored type (nearest even; NaN stays NaN)
 __device__ __forceinline__ void from_f32(Raw8<uint16_t>& r, const float (&f)[8]) {
   r.a = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};

@@ -4,6 +4,7 @@ which runs them with a MoELayer."""
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -29,6 +30,11 @@ def _arg(t: Optional[torch.Tensor], numel: int, name: str, dtype: Optional[torch
 
 
 # ---------------------------------------------------------------- layer norm
+
+@functools.lru_cache(maxsize=1024)
+def _norm_ws_floats(rows: int, d: int) -> int:
+    return workspace_bytes(MOE_OP_LAYER_NORM_BACKWARD, MoeShape(rows, d, 1, 1, 1, 1, 1, 1)) // 4
+
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                residual: Optional[torch.Tensor] = None, eps: float = 1e-5, y_dtype: Optional[torch.dtype] = None,
@@ -79,8 +85,9 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
         dw = torch.empty_like(weight)
     if db is None and has_bias:
         db = torch.empty_like(weight)
-    if ws is None and rows > 0:
-        ws = weight.new_empty(workspace_bytes(MOE_OP_LAYER_NORM_BACKWARD, MoeShape(rows, d, 1, 1, 1, 1, 1, 1)) // 4)
+    need = 0 if ws is not None else _norm_ws_floats(rows, d)
+    if need:
+        ws = weight.new_empty(need)
     st = lib().moe_layer_norm_backward(rows, d, _arg(dy, n, "dy"), _dt(dy), _arg(x, n, "x"), _dt(x),
                                        _arg(weight, d, "weight", _f32), _arg(mean, rows, "mean", _f32),
                                        _arg(rstd, rows, "rstd", _f32), _arg(d_sum, n, "d_sum", dt),

@@ -24,7 +24,8 @@ DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 ROUND = {"f32": 2.0 ** -23, "bf16": 2.0 ** -8}
 
 SHAPES = [(1, 1), (1, 64), (3, 7), (2, 9), (5, 63), (7, 513), (4, 1000), (33, 1001), (9, 2048), (3, 4099),
-          (5, 7168), (2, 16384), (2, 20011), (1, 32768), (1500, 40), (700, 1024), (2051, 264)]
+          (5, 7168), (2, 16384), (2, 20011), (1, 32768), (1500, 40), (700, 1024), (2051, 264), (384, 333),
+          (385, 333), (1025, 2050), (600, 4097), (530, 9001)]
 
 
 def _rows(g, rows, d, dt, dev, offset=0.5, shift=0):
@@ -151,10 +152,11 @@ def test_backward(rows, d, gt, xt, ot, res):
     _check(db, rb, (rows + 64) * EPS * np.abs(hy).sum(0) + 1e-30)
 
 
-def test_backward_in_place_no_bias_and_repeat():
+@pytest.mark.parametrize("rows", [300, 3000])             # the one-launch form, and the one with parts
+def test_backward_in_place_no_bias_and_repeat(rows):
     dev = need_gpu()
     g = torch.Generator(device=dev).manual_seed(6)
-    x, dy, ds = (_rows(g, 300, 520, torch.bfloat16, dev) for _ in range(3))
+    x, dy, ds = (_rows(g, rows, 520, torch.bfloat16, dev) for _ in range(3))
     w = torch.randn(520, generator=g, device=dev)
     _, _, mean, rstd = M.layer_norm(x, w)
     dx, dw, db = M.layer_norm_backward(dy, x, w, mean, rstd, d_sum=ds)
@@ -163,9 +165,12 @@ def test_backward_in_place_no_bias_and_repeat():
         assert all(torch.equal(p, q) for p, q in zip(a, (dx, dw, db)))
     ex, ew, eb = M.layer_norm_backward(dy, x, w, mean, rstd, d_sum=ds, has_bias=False)
     assert eb is None and torch.equal(ex, dx) and torch.equal(ew, dw)
-    dyc, dsc = dy.clone(), ds.clone()
-    assert torch.equal(M.layer_norm_backward(dyc, x, w, mean, rstd, d_sum=ds, dx=dyc)[0], dx)
-    assert torch.equal(M.layer_norm_backward(dy, x, w, mean, rstd, d_sum=dsc, dx=dsc)[0], dx)
+    dsc = ds.clone()
+    got = M.layer_norm_backward(dy, x, w, mean, rstd, d_sum=dsc, dx=dsc)
+    assert all(torch.equal(p, q) for p, q in zip(got, (dx, dw, db)))
+    for bad in (dy, x):                                   # read while dx is written
+        with pytest.raises(M.MoeError):
+            M.layer_norm_backward(dy, x, w, mean, rstd, d_sum=ds, dx=bad)
 
 
 def test_backward_no_rows():

@@ -27,7 +27,10 @@ def test_layer_norm_refusals(kw, want):
     assert _norm(**kw) == want
 
 
-def _norm_bwd(rows=4, d=8, dy=FAKE, dt=1, x=FAKE, xt=1, w=FAKE, mean=FAKE, rstd=FAKE, ds=None, dx=FAKE, ot=1,
+DY, X = 0x2000, 0x3000
+
+
+def _norm_bwd(rows=1000, d=8, dy=DY, dt=1, x=X, xt=1, w=FAKE, mean=FAKE, rstd=FAKE, ds=None, dx=FAKE, ot=1,
               dw=FAKE, db=None, ws=FAKE, n=1 << 30):
     return L.moe_layer_norm_backward(rows, d, dy, dt, x, xt, w, mean, rstd, ds, dx, ot, dw, db, ws, n, None)
 
@@ -35,18 +38,20 @@ def _norm_bwd(rows=4, d=8, dy=FAKE, dt=1, x=FAKE, xt=1, w=FAKE, mean=FAKE, rstd=
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), INV), (dict(d=-3), INV), (dict(dy=None), INV), (dict(x=None), INV), (dict(w=None), INV),
     (dict(mean=None), INV), (dict(rstd=None), INV), (dict(dx=None), INV), (dict(dw=None), INV), (dict(dt=2), INV),
-    (dict(xt=-1), INV), (dict(ot=3), INV), (dict(d=40000), UNS), (dict(ws=None), WS), (dict(ws=FAKE + 8), WS),
+    (dict(xt=-1), INV), (dict(ot=3), INV), (dict(dx=DY), INV), (dict(dx=X), INV), (dict(d=40000), UNS), (dict(ws=None), WS), (dict(ws=FAKE + 8), WS),
     (dict(rows=0, dw=None), INV)])
 def test_layer_norm_backward_refusals(kw, want):
     assert _norm_bwd(**kw) == want
 
 
 def test_layer_norm_backward_workspace():
-    for rows, d in ((1, 1), (4, 8), (1000, 1001), (16384, 7168), (3, 32768)):
+    for rows, d in ((1000, 1), (500, 8), (1000, 1001), (16384, 7168), (3, 32768)):
         sh = _lib.MoeShape(rows, d, 1, 1, 1, 1, 1, 1)
         need = L.moe_workspace_size(_lib.MOE_OP_LAYER_NORM_BACKWARD, ctypes.byref(sh), 0)
         assert need >= 2 * d * 4
         assert _norm_bwd(rows=rows, d=d, n=need - 1) == WS
+    few = _lib.MoeShape(8, 7168, 1, 1, 1, 1, 1, 1)  # one launch forms everything: no parts
+    assert L.moe_workspace_size(_lib.MOE_OP_LAYER_NORM_BACKWARD, ctypes.byref(few), 0) == 0
     bad = _lib.MoeShape(1, 40000, 1, 1, 1, 1, 1, 1)
     assert L.moe_workspace_size(_lib.MOE_OP_LAYER_NORM_BACKWARD, ctypes.byref(bad), 0) == 0
 
