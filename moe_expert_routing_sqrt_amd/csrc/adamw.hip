@@ -18,9 +18,9 @@
 //
 // Bound by memory: 12 to 30 bytes an element, each touched once.  A lane takes 4
 // consecutive elements, so that every fp32 access of a wave is one solid
-// kilobyte (32 lanes share a tile's scale), loads and stores pass the caches by,
-// and a work-group ends after one quad a lane, the next one's loads filling its
-// place.  Measured on 113 M bf16 weights with fp32 masters, us (TB/s), fp32 /
+// kilobyte (32 lanes share a tile's scale), stores pass the caches by, as do the
+// loads of large launches, and a work-group ends after one quad a lane, the next
+// one's loads filling its place.  Measured on 113 M bf16 weights with fp32 masters, us (TB/s), fp32 /
 // 8-bit states:
 //   one quad, streaming loads and stores   581 (5.85) / 326 (6.31)
 //   stores through the caches              632 (5.37) / 374 (5.49)
@@ -105,11 +105,13 @@ struct Quad<uint8_t> {
 };
 
 // FULL: all 4 exist; else the first n (the others read as 0)
-template <bool FULL, typename T>
+template <bool FULL, bool STREAM, typename T>
 __device__ __forceinline__ typename Quad<T>::V load4(const T* p, int n) {
   typedef typename Quad<T>::A A;
-  if constexpr (FULL) {
+  if constexpr (FULL && STREAM) {
     return __builtin_nontemporal_load(reinterpret_cast<const A*>(p));
+  } else if constexpr (FULL) {
+    return *reinterpret_cast<const A*>(p);
   } else {
     T e[4] = {};
 #pragma unroll
@@ -177,7 +179,7 @@ __device__ __forceinline__ uint32_t encode(const float (&f)[4], float& scale) {
 }
 
 // The quad of elements [i, i + 4) of a tensor, of which n exist (FULL: all).
-template <typename TP, typename TG, bool MASTER, bool BITS8, bool FULL>
+template <typename TP, typename TG, bool MASTER, bool BITS8, bool STREAM, bool FULL>
 __device__ __forceinline__ void adamw_quad(const AdamArgs& a, const Item& it, int64_t i, int n, float scale) {
   typedef typename std::conditional<BITS8, uint8_t, float>::type TS;
   typedef typename std::conditional<MASTER, float, TP>::type TW;
@@ -185,10 +187,10 @@ __device__ __forceinline__ void adamw_quad(const AdamArgs& a, const Item& it, in
   TW* const pw = (MASTER ? reinterpret_cast<TW*>(it.w) : reinterpret_cast<TW*>(it.p)) + i;
   TS* const pm = static_cast<TS*>(it.m) + i;
   TS* const pv = static_cast<TS*>(it.v) + i;
-  const auto rg = load4<FULL>(static_cast<const TG*>(it.g) + i, n);
-  const auto rw = load4<FULL>(pw, n);
-  const auto rm = load4<FULL>(pm, n);
-  const auto rv = load4<FULL>(pv, n);
+  const auto rg = load4<FULL, STREAM>(static_cast<const TG*>(it.g) + i, n);
+  const auto rw = load4<FULL, STREAM>(pw, n);
+  const auto rm = load4<FULL, STREAM>(pm, n);
+  const auto rv = load4<FULL, STREAM>(pv, n);
   float g[4], w[4], m[4], v[4], r[4];
   if constexpr (BITS8) {
     decode(rm, n > 0 ? it.ms[i / 128] : 0.0f, m);
@@ -237,7 +239,7 @@ __device__ __forceinline__ void adamw_quad(const AdamArgs& a, const Item& it, in
 
 // TP: the weight's type; MASTER: fp32 weights in w, p their rounded copy;
 // BITS8: 8-bit states
-template <typename TP, typename TG, bool MASTER, bool BITS8>
+template <typename TP, typename TG, bool MASTER, bool BITS8, bool STREAM>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a) {
   // the work-group's tensor (uniform)
   int lo = 0, hi = a.count;
@@ -249,8 +251,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a) {
   const int64_t at = (blockIdx.x - a.first[lo]) * (int64_t)kPerGroup;  // a tile starts here
   const int64_t i = at + threadIdx.x * 4;
   const float scale = a.scale == nullptr ? 1.0f : *a.scale;
-  if (at + kPerGroup <= it.n) adamw_quad<TP, TG, MASTER, BITS8, true>(a, it, i, 4, scale);
-  else adamw_quad<TP, TG, MASTER, BITS8, false>(a, it, i, static_cast<int>(max((int64_t)0, min((int64_t)4, it.n - i))), scale);
+  if (at + kPerGroup <= it.n) adamw_quad<TP, TG, MASTER, BITS8, STREAM, true>(a, it, i, 4, scale);
+  else
+    adamw_quad<TP, TG, MASTER, BITS8, STREAM, false>(
+        a, it, i, static_cast<int>(max((int64_t)0, min((int64_t)4, it.n - i))), scale);
 }
 
 struct Kind {
@@ -261,10 +265,17 @@ struct Kind {
 
 template <typename TP, typename TG, bool MASTER>
 void launch_state(const AdamArgs& a, const Kind& k, dim3 grid, hipStream_t s) {
-  if (k.state == MOE_E4M3)
-    hipLaunchKernelGGL((adamw_kernel<TP, TG, MASTER, true>), grid, dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((adamw_kernel<TP, TG, MASTER, false>), grid, dim3(kThreads), 0, s, a);
+  // loads pass the caches by when the launch touches more than the package's
+  // 256 MB cache holds (28 M elements: 139 us against 156, 8-bit 83 against 89);
+  // below that the gradients at least may still be there (7 M: 27 against 36)
+  const double each = (k.state == MOE_E4M3 ? 4.125 : 16.0) + sizeof(TG) + 2.0 * sizeof(TP) + (MASTER ? 6.0 : 0.0);
+  const bool stream = static_cast<double>(a.first[a.count]) * kPerGroup * each > 256.0 * (1 << 20);
+  auto go = [&](auto bits8, auto st) {
+    hipLaunchKernelGGL((adamw_kernel<TP, TG, MASTER, decltype(bits8)::value, decltype(st)::value>), grid,
+                       dim3(kThreads), 0, s, a);
+  };
+  if (k.state == MOE_E4M3) stream ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+  else stream ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
 }
 
 template <typename TG>
