@@ -72,11 +72,11 @@ struct SequenceSearch {
   __device__ __forceinline__ SequenceSearch(int64_t T_, const int32_t* off_, int n_) : T(T_), off(off_), n(n_), v(0) {
     if (off != nullptr && n > kScalar && n <= kLanes) v = off[min(static_cast<int>(threadIdx.x & 63), n)];
   }
-  // (T fits an int, so tokens of a wave do too)
   __device__ __forceinline__ int operator()(int64_t t) const {
     if (off == nullptr) return t < T ? 0 : -1;
-    const int t_first = __builtin_amdgcn_readfirstlane(static_cast<int>(t));
-    const int t_last = __builtin_amdgcn_readlane(static_cast<int>(t), 63);
+    const int ti = static_cast<int>(min(t, T));  // T fits an int
+    const int t_first = __builtin_amdgcn_readfirstlane(ti);
+    const int t_last = __builtin_amdgcn_readlane(ti, 63);
     int s0, end;  // the first token's sequence, and where it ends
     if (n > kScalar && n <= kLanes) {
       s0 = __builtin_popcountll(__ballot((threadIdx.x & 63) <= n && v <= t_first)) - 1;
@@ -86,7 +86,7 @@ struct SequenceSearch {
       end = s0 >= 0 && s0 < n ? off[s0 + 1] : INT32_MIN;
     }
     if (t_last < end) return t < T ? s0 : -1;
-    const int s = last_at_most(static_cast<int>(t));
+    const int s = last_at_most(ti);
     return t < T && s < n ? s : -1;
   }
 

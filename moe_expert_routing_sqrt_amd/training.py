@@ -22,11 +22,12 @@ def _arg(t: Optional[torch.Tensor], numel: int, name: str, dtype: Optional[torch
     and layout are checked."""
     if t is None:
         return 0
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype)[6:]}")
-    if t.numel() < numel:
-        _need(t, numel, name)  # raises
-    return _checked_ptr(t)
+    if t.numel() >= numel and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, numel, name)
+    return _checked_ptr(t)  # raises
 
 
 # ---------------------------------------------------------------- layer norm
@@ -270,6 +271,7 @@ class MoEBlock:
                                    device=dev)
         self.opt_args = dict(lr=lr, betas=betas, states=states, weight_decay=weight_decay)
         self.master, self.opt = master, None
+        self._loss_bufs = {}  # of balance_loss, by the number of sequences
 
     def forward(self, delta: torch.Tensor, stream: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
                 token_mask: Optional[torch.Tensor] = None):
@@ -278,8 +280,14 @@ class MoEBlock:
         out = self.layer.forward(self.h, save_for_backward=True)
         la = self.layer
         self.seqs = (seq_offsets, token_mask)
+        n = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        if n not in self._loss_bufs:
+            new = la.logits.new_empty
+            size = lib().moe_balance_loss_workspace_size(ctypes.byref(la.sh), n)
+            self._loss_bufs[n] = dict(loss=new(1), counts=new((n, la.E), dtype=_i32), prob=new((n, la.E)),
+                                      dprob=new((n, la.E)), ws=new(max(1, size // 4)))
         self.loss, self.counts, self.prob, self.dprob = balance_loss(
-            la.sh, la.logits, la.idx, self.alpha, seq_offsets, token_mask, la.logit_offset)
+            la.sh, la.logits, la.idx, self.alpha, seq_offsets, token_mask, la.logit_offset, **self._loss_bufs[n])
         return out, self.stream
 
     def backward(self, d_out: torch.Tensor, d_stream: Optional[torch.Tensor] = None) -> torch.Tensor:

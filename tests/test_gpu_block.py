@@ -100,3 +100,12 @@ def test_training_lowers_the_loss(states):
     for p, m in zip(blk.opt.params, blk.opt.master):
         assert m is None or torch.equal(p, m.to(torch.bfloat16))
     assert blk.opt.step_count == 10
+
+
+def test_train_step_command(capsys):
+    need_gpu()
+    from moe_expert_routing_sqrt_amd import train_step
+    r = train_step.main(["--workload", "flash", "--tokens", "512", "--steps", "4", "--states", "e4m3"])
+    assert len(r["errors"]) == 4 and r["errors"][-1][0] < r["errors"][0][0]
+    assert all(t > 0 for t in r["ms"].values())
+    assert "squared error" in capsys.readouterr().out
