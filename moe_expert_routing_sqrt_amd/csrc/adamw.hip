@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPerGroup = kThreads * 4;  // elements of a work-group: one quad a lane
-constexpr int kMaxTensors = 32;       // per launch: the arguments stay under 4 KB
+constexpr int kMaxTensors = 48;       // per launch: the arguments stay under 4 KB
 
 struct Item {
   int64_t n;
@@ -256,6 +256,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a) {
     adamw_quad<TP, TG, MASTER, BITS8, STREAM, false>(
         a, it, i, static_cast<int>(max((int64_t)0, min((int64_t)4, it.n - i))), scale);
 }
+
+static_assert(sizeof(AdamArgs) <= 4096, "the arguments of a launch");
 
 struct Kind {
   int p, g, state;

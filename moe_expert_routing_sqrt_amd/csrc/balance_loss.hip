@@ -275,6 +275,99 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(const LossArgs p
   }
 }
 
+// The same for tiles of many short sequences (E <= 256).  The probabilities go to
+// LDS once (zeros for tokens that do not count), and so do the slot counts of
+// each run, a sequence's stretch of tokens in the tile; then every thread takes
+// a (run, expert) pair and adds the run's tokens in order: one pass whatever the
+// number of runs.
+template <bool FULL>
+__global__ __launch_bounds__(kThreads) void balance_part_short_kernel(const LossArgs p) {
+  constexpr int U = kTile / kWaves;  // tokens of a lane group (at one token a wave)
+  __shared__ __align__(16) float s_p[kTile * 256];
+  __shared__ uint32_t s_cnt[kTile * 256 / 2];  // counts of 16 bits: 64 k <= 1024
+  __shared__ int s_begin[kTile], s_seq[kTile], s_tok[kTile];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t0 = (int64_t)blockIdx.x * kTile;
+  const int ntok = static_cast<int>(min((int64_t)kTile, p.T - t0));
+  const int E = p.E;
+  const SequenceSearch sequence_of(p.T, p.seq, p.n_seq);
+  const RowMap<1, FULL> m(E, p.log_lpt);
+  const int tpw = kWave / m.lpt;
+  // every load of the tile before the first wait; a token that does not count
+  // may hold anything, also NaN: its row is read but never selected
+  float pr[U][1][4], off[1][4] = {};
+  if (ntok > 0) {
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      const int i = (v * kWaves + wave) * tpw + m.which;
+      m.load(p.logits + (t0 + min(i, ntok - 1)) * E, pr[v]);
+    }
+    if (p.offset != nullptr) m.load(p.offset, off);
+  }
+  const int my_tok = tid / p.k;  // a slot of the tile per thread: 64 k <= 1024
+  const int my_e = my_tok < ntok ? p.idx[t0 * p.k + tid] : -1;
+  const bool on = lane < ntok && (p.mask == nullptr || p.mask[t0 + lane] != 0);
+  const int seq = sequence_of(t0 + lane);
+  if (blockIdx.x == 0 && tid == 0) *p.total = 0;
+  // runs: a token starts one where its sequence is not the token's before it
+  const int before = __shfl_up(seq, 1, kWave);
+  const uint64_t starts = __ballot(seq >= 0 && (lane == 0 || before != seq));
+  const uint64_t ends = __ballot(seq < 0 && lane != 0 && before >= 0);  // a run followed by no sequence
+  const uint64_t counted = __ballot(on && seq >= 0);
+  const int runs = __builtin_popcountll(starts);
+  const int run = __builtin_popcountll(starts & ((2ull << lane) - 1)) - 1;  // of this lane's token
+  if (wave == 0 && ((starts >> lane) & 1) != 0) {
+    const uint64_t after = (starts | ends) & ~((2ull << lane) - 1);
+    const int end = after != 0 ? __builtin_ctzll(after) : ntok;
+    const uint64_t mine = (end >= 64 ? ~0ull : (1ull << end) - 1) & ~((1ull << lane) - 1);
+    s_begin[run] = lane | end << 8;
+    s_seq[run] = seq;
+    s_tok[run] = __builtin_popcountll(counted & mine);
+  }
+  for (int i = tid; i < (runs * E + 1) / 2; i += kThreads) s_cnt[i] = 0;
+  __syncthreads();
+  const int my_run = __shfl(run, my_tok & 63, kWave);
+  if (my_e >= 0 && my_e < E && ((counted >> (my_tok & 63)) & 1) != 0) {
+    const int at = my_run * E + my_e;
+    atomicAdd(&s_cnt[at / 2], 1u << (16 * (at & 1)));
+  }
+#pragma unroll
+  for (int v = 0; v < U; ++v) {
+    if ((v * kWaves + wave) * tpw >= ntok) break;  // uniform over the wave
+    const int i = (v * kWaves + wave) * tpw + m.which;
+    float total = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = affinity<false>(pr[v][0][j] + off[0][j]).a;
+      pr[v][0][j] = m.owns(0, j) ? a : 0.0f;
+      total += pr[v][0][j];
+    }
+    total = group_sum(total, m.lpt);
+    const bool some = i < ntok && ((counted >> (i & 63)) & 1) != 0 && total > 0.0f;
+    const float inv = some ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) pr[v][0][j] = some ? pr[v][0][j] * inv : 0.0f;
+    if (i < ntok) m.store(s_p + i * E, pr[v]);
+  }
+  __syncthreads();
+  for (int id = tid; id < runs * E; id += kThreads) {
+    const int r = id / E, e = id - r * E;
+    const int begin = s_begin[r] & 0xFF, end = s_begin[r] >> 8;
+    float v = 0.0f;
+    for (int i = begin; i < end; i += 8) {  // 8 reads in flight
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = s_p[min(i + j, end - 1) * E + e];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += i + j < end ? t[j] : 0.0f;
+    }
+    const int64_t row = (int64_t)blockIdx.x + s_seq[r];
+    p.psum[row * E + e] = v;
+    p.pcnt[row * E + e] = static_cast<int32_t>((s_cnt[id / 2] >> (16 * (id & 1))) & 0xFFFFu);
+    if (e == 0) p.ptok[row] = s_tok[r];
+  }
+}
+
 struct SumArgs {
   int64_t T;
   int E, k, n_seq, log_w, team;
@@ -506,9 +599,15 @@ hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, con
   const int64_t tiles = T > 0 ? (T + kTile - 1) / kTile : 1;
   const LossArgs a{T, E, lanes_log(E), k, n_seq, logits, offset, idx, seq, mask, psum, pcnt, ptok, total};
   const dim3 grid(static_cast<unsigned>(tiles)), block(kThreads);
+  // sequences of under a tile's length on average: each costs the first form a
+  // pass of its own (29 tokens in 49 sequences 40 us against 10.5; 16384 in 300,
+  // E = 100, 15.1 against 14.6), long ones the second its trip through LDS
+  // (16384 in 64, E = 256, 13.3 against 15.4; 65536 in 16 25.6 against 39.7)
+  const bool many = E <= 256 && T < static_cast<int64_t>(kTile) * n_seq;
   auto part = [&](auto full) {
     constexpr bool F = decltype(full)::value;
-    if (E <= 256) hipLaunchKernelGGL((balance_part_kernel<1, F>), grid, block, 0, s, a);
+    if (many) hipLaunchKernelGGL(balance_part_short_kernel<F>, grid, block, 0, s, a);
+    else if (E <= 256) hipLaunchKernelGGL((balance_part_kernel<1, F>), grid, block, 0, s, a);
     else if (E <= 512) hipLaunchKernelGGL((balance_part_kernel<2, F>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((balance_part_kernel<4, F>), grid, block, 0, s, a);
   };

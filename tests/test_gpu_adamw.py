@@ -125,7 +125,7 @@ def test_steps_bit_for_bit(p, g, bits, master):
 def test_many_tensors_of_mixed_kinds():
     """More tensors than one launch takes, every kind among them."""
     dev = need_gpu()
-    refs = [Ref(50 + 37 * i, *KINDS[i % len(KINDS)], seed=i) for i in range(100)]
+    refs = [Ref(50 + 5 * i, *KINDS[i % len(KINDS)], seed=i) for i in range(700)]
     params = [_tensor(r.p, DT[r.kind[0]], dev) for r in refs]
     grads = [_tensor(r.grad(), DT[r.kind[1]], dev) for r in refs]
     master = [_tensor(r.w, torch.float32, dev) if r.kind[3] else None for r in refs]

@@ -51,7 +51,8 @@ CASES = [  # T, E, k, sequences (0: no offsets), ragged, masked
     (1000, 256, 8, 7, True, True), (130, 7, 2, 100, True, False), (64, 5, 1, 64, False, True),
     (500, 100, 16, 3, True, False), (200, 300, 4, 4, True, True), (150, 513, 3, 2, False, False),
     (90, 1024, 16, 3, True, True), (4099, 64, 6, 1, False, False), (40, 24, 3, 1000, True, True),
-    (5000, 12, 2, 2, False, True)]
+    (5000, 12, 2, 2, False, True), (700, 256, 16, 40, True, True), (333, 30, 3, 60, True, False),
+    (64, 256, 16, 64, False, False), (900, 2, 2, 300, True, True), (3000, 200, 5, 9, True, True)]
 
 
 @pytest.mark.parametrize("T,E,k,n,ragged,masked", CASES)
