@@ -573,7 +573,7 @@ int moe_layer_norm(int64_t rows, int32_t d, const void* x, const void* residual,
  *   dweight, dbias [d] fp32 out (dbias may be NULL); zeros with rows = 0
  *   ws       moe_workspace_size(MOE_OP_LAYER_NORM_BACKWARD, shape, 0) bytes
  *            with the shape's T = rows: the parts of dweight and dbias (0 for
- *            few rows, which need none: ws may be NULL)
+ *            few or very wide rows, which need none: ws may be NULL)
  * Each type MOE_BF16 or MOE_F32; d as moe_layer_norm.  All sums in fp32 and in
  * a fixed order (deterministic).
  */

@@ -166,8 +166,7 @@ struct NormBwdArgs {
 // A work-group takes every gridDim.x-th row and keeps its columns' dw and db in
 // registers; their sums leave once at the end.  With one piece a lane the
 // weights stay there too, and the next row's loads are issued before this one
-// is reduced; wider rows have no registers for either (beyond d = 16384 they
-// spill).  MULTI (rows of at most 4 waves): the work-group's 8 waves take several
+// is reduced; rows of two (d > 8192) have no registers for either.  MULTI (rows of at most 4 waves): the work-group's 8 waves take several
 // rows at once, side by side, and join their sums in LDS, so that the parts
 // stay one per work-group.
 constexpr int kMultiWaves = 8;
@@ -359,11 +358,11 @@ hipError_t fwd_n(const NormArgs& a, int n, dim3 grid, dim3 block, hipStream_t s)
   return hipGetLastError();
 }
 
-// The same for few rows in one launch: the first `row_groups` work-groups form
-// dx, a row each, and the others dw and db, 64 columns each, from the rows
-// again (they are still in cache), which needs no parts and no second launch.
-template <typename TD, typename TX, typename TO, bool DS>
-__global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_few_kernel(const NormBwdArgs p, int row_groups, float* dw,
+// The same in one launch without parts, for few rows and for rows too wide to
+// keep dw and db in registers: the first `row_groups` work-groups form dx, a row
+// each, and the others dw and db, 64 columns each, from the rows again.
+template <typename TD, typename TX, typename TO, bool DS, int N>
+__global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_split_kernel(const NormBwdArgs p, int row_groups, float* dw,
                                                                        float* db) {
   __shared__ float s_red[2][kMaxWaves][kWave];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -406,26 +405,34 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_few_kernel(const No
     return;
   }
   const int64_t row = blockIdx.x, base = row * p.d;
-  const Piece q = piece_of(threadIdx.x, p.d);
-  Raw8<TD> rd;
-  Raw8<TX> rx, rs;
-  Raw8<float> rw;
-  load8<false>(rd, dy + base, q);
-  load8<false>(rx, x + base, q);
-  if constexpr (DS) load8<false>(rs, static_cast<const TX*>(p.ds) + base, q);
-  load8<false>(rw, p.w, q);
-  const float mean = p.mean[row], rstd = p.rstd[row], inv_d = 1.0f / static_cast<float>(p.d);
-  float g[8], xh[8], w[8], c1 = 0.0f, c2 = 0.0f;
-  to_f32(rd, g);
-  to_f32(rx, xh);
-  to_f32(rw, w);
-  mask8(g, q);
+  Piece q[N];
+  Raw8<TD> rd[N];
+  Raw8<TX> rx[N], rs[DS ? N : 1];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    xh[j] = (xh[j] - mean) * rstd;
-    g[j] *= w[j];
-    c1 += g[j];
-    c2 = __builtin_fmaf(g[j], xh[j], c2);
+  for (int i = 0; i < N; ++i) {
+    q[i] = piece_of(i * blockDim.x + threadIdx.x, p.d);
+    load8<false>(rd[i], dy + base, q[i]);
+    load8<false>(rx[i], x + base, q[i]);
+  }
+  const float mean = p.mean[row], rstd = p.rstd[row], inv_d = 1.0f / static_cast<float>(p.d);
+  float g[N][8], xh[N][8], c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    Raw8<float> rw;
+    float w[8];
+    load8<false>(rw, p.w, q[i]);
+    to_f32(rd[i], g[i]);
+    to_f32(rx[i], xh[i]);
+    to_f32(rw, w);
+    mask8(g[i], q[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      xh[i][j] = (xh[i][j] - mean) * rstd;
+      g[i][j] *= w[j];
+      c1 += g[i][j];
+      c2 = __builtin_fmaf(g[i][j], xh[i][j], c2);
+    }
+    if constexpr (DS) load8<false>(rs[i], static_cast<const TX*>(p.ds) + base, q[i]);
   }
   c1 = wave_sum(c1);
   c2 = wave_sum(c2);
@@ -437,16 +444,19 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_few_kernel(const No
   c1 = row16_sum((lane & 15) < waves ? s_red[0][0][lane & 15] : 0.0f) * inv_d;
   c2 = row16_sum((lane & 15) < waves ? s_red[0][1][lane & 15] : 0.0f) * inv_d;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) g[j] = rstd * (g[j] - c1 - xh[j] * c2);
-  if constexpr (DS) {
-    float res[8];
-    to_f32(rs, res);
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] += res[j];
+    for (int j = 0; j < 8; ++j) g[i][j] = rstd * (g[i][j] - c1 - xh[i][j] * c2);
+    if constexpr (DS) {
+      float res[8];
+      to_f32(rs[i], res);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] += res[j];
+    }
+    Raw8<TO> o;
+    from_f32(o, g[i]);
+    store8(static_cast<TO*>(p.dx) + base, o, q[i]);
   }
-  Raw8<TO> o;
-  from_f32(o, g);
-  store8(static_cast<TO*>(p.dx) + base, o, q);
 }
 
 // launch shape of the backward: pieces of 8 a lane holds, waves of a row, rows
@@ -454,7 +464,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_few_kernel(const No
 struct BwdShape {
   int n, waves, rpb;
   int64_t groups;
-  bool few;  // the one-launch form, which has no parts
+  bool split;  // the one-launch form, which has no parts
 };
 // One piece a lane while a row then fits 16 waves (d <= 8192): two need over
 // 128 registers (16384 x 7168: 206 us against 400).  Rows of up to 4 waves go
@@ -462,8 +472,9 @@ struct BwdShape {
 // work-group per CU keeps the parts few (16384 x 7168: 206 + 5 us, 223 + 9 with
 // two; 65536 x 2048 fp32: 293 against 337); rows of one wave take two (16000 x
 // 257: 14.2 against 15.0).
-// Up to 384 rows one launch forms everything (64 x 7168: 3.3 us against 8.1; 400 x
-// 1024: 7.0 against 8.2, 400 x 200: 6.8 against 6.4).
+// The one-launch form: up to 384 rows (64 x 7168: 3.3 us against 8.1; 400 x 1024:
+// 7.0 against 8.2, 400 x 200: 6.8 against 6.4), and rows of four pieces a lane,
+// where dw and db would spill (2000 x 20000 fp32: 157 us against 238).
 constexpr int kFewRows = 384;
 BwdShape bwd_shape(int64_t rows, int d) {
   const int pieces = (d + 7) / 8;
@@ -472,16 +483,18 @@ BwdShape bwd_shape(int64_t rows, int d) {
   const int waves = (pieces + n * kWave - 1) / (n * kWave);
   const int rpb = waves <= kMultiWaves / 2 ? kMultiWaves / waves : 1;
   const int64_t need = (rows + rpb - 1) / rpb, fill = waves == 1 ? 512 : 256;
-  return {n, waves, rpb, need < fill ? need : fill, rows > 0 && rows <= kFewRows && n == 1};
+  return {n, waves, rpb, need < fill ? need : fill, rows > 0 && (rows <= kFewRows || n > 2)};
 }
 
 template <typename TD, typename TX, typename TO, bool DS>
 hipError_t bwd_n(const NormBwdArgs& a, const BwdShape& b, float* dw, float* db, hipStream_t s) {
-  if (b.few) {
+  if (b.split) {
     // at least 8 waves: the columns' rows are split over them
-    const int waves = b.waves > 8 ? b.waves : 8, rows = static_cast<int>(a.rows);
-    hipLaunchKernelGGL((norm_bwd_few_kernel<TD, TX, TO, DS>), dim3(rows + (a.d + kWave - 1) / kWave),
-                       dim3(waves * kWave), 0, s, a, rows, dw, db);
+    const int rows = static_cast<int>(a.rows);
+    const dim3 all(rows + (a.d + kWave - 1) / kWave), wide((b.waves > 8 ? b.waves : 8) * kWave);
+    if (b.n == 1) hipLaunchKernelGGL((norm_bwd_split_kernel<TD, TX, TO, DS, 1>), all, wide, 0, s, a, rows, dw, db);
+    else if (b.n == 2) hipLaunchKernelGGL((norm_bwd_split_kernel<TD, TX, TO, DS, 2>), all, wide, 0, s, a, rows, dw, db);
+    else hipLaunchKernelGGL((norm_bwd_split_kernel<TD, TX, TO, DS, 4>), all, wide, 0, s, a, rows, dw, db);
     return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(b.groups)), block(b.waves * b.rpb * kWave);
@@ -489,8 +502,7 @@ hipError_t bwd_n(const NormBwdArgs& a, const BwdShape& b, float* dw, float* db, 
   if (b.rpb > 1) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, true, false>), grid, block, 0, s, a);
   else if (b.n == 1 && st) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, false, true>), grid, block, 0, s, a);
   else if (b.n == 1) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, false, false>), grid, block, 0, s, a);
-  else if (b.n == 2) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 2, false, false>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 4, false, false>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 2, false, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -538,7 +550,7 @@ hipError_t launch_layer_norm(int64_t rows, int d, const void* x, const void* r, 
 
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int d) {
   const BwdShape b = bwd_shape(rows, d);
-  return b.few ? 0 : static_cast<size_t>(b.groups) * 2 * d * sizeof(float);
+  return b.split ? 0 : static_cast<size_t>(b.groups) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dtype, const void* x, int x_dtype,
@@ -560,7 +572,7 @@ hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dty
       case 6: e = bwd_ds<float, B, B>(a, b, dw, db, s); break;
       default: e = bwd_ds<B, B, B>(a, b, dw, db, s); break;
     }
-    if (e != hipSuccess || b.few) return e;
+    if (e != hipSuccess || b.split) return e;
   }
   hipLaunchKernelGGL(norm_param_grad_kernel, dim3((2 * d + kWave - 1) / kWave), dim3(kSumWaves * kWave), 0, s, ws,
                      static_cast<int>(b.groups), d, dw, db);

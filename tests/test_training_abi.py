@@ -45,13 +45,14 @@ def test_layer_norm_backward_refusals(kw, want):
 
 
 def test_layer_norm_backward_workspace():
-    for rows, d in ((1000, 1), (500, 8), (1000, 1001), (16384, 7168), (3, 32768)):
+    for rows, d in ((1000, 1), (500, 8), (1000, 1001), (16384, 7168), (600, 16384)):
         sh = _lib.MoeShape(rows, d, 1, 1, 1, 1, 1, 1)
         need = L.moe_workspace_size(_lib.MOE_OP_LAYER_NORM_BACKWARD, ctypes.byref(sh), 0)
         assert need >= 2 * d * 4
         assert _norm_bwd(rows=rows, d=d, n=need - 1) == WS
-    few = _lib.MoeShape(8, 7168, 1, 1, 1, 1, 1, 1)  # one launch forms everything: no parts
-    assert L.moe_workspace_size(_lib.MOE_OP_LAYER_NORM_BACKWARD, ctypes.byref(few), 0) == 0
+    for rows, d in ((8, 7168), (2000, 20000)):       # one launch forms everything: no parts
+        few = _lib.MoeShape(rows, d, 1, 1, 1, 1, 1, 1)
+        assert L.moe_workspace_size(_lib.MOE_OP_LAYER_NORM_BACKWARD, ctypes.byref(few), 0) == 0
     bad = _lib.MoeShape(1, 40000, 1, 1, 1, 1, 1, 1)
     assert L.moe_workspace_size(_lib.MOE_OP_LAYER_NORM_BACKWARD, ctypes.byref(bad), 0) == 0
 
