@@ -16,6 +16,9 @@
  *                   expert as one group over all tokens)
  *   moe_combine     gate-weighted sum of expert rows back in token order
  *
+ * and around it its backward and a training step's other operators: the norm
+ * in front of the layer, a balance loss on the router, and the optimizer.
+ *
  * Conventions for every call
  *   - Pointers are device pointers unless marked "host".  The caller owns and
  *     allocates every buffer, including workspaces; the library never

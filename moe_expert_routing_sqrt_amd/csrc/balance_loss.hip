@@ -16,6 +16,10 @@
 // no cancellation, and no underflow before e^(l/2) itself.  Two
 // transcendental instructions and 16 others an element.
 // A row whose affinities all vanish has no probabilities: it adds 0.
+//
+// At T = 16384, E = 256, k = 8 (17 MB, 2.9 us of HBM) the forward takes 7.4 us for
+// the parts, 1.9 of them transcendentals and polynomial, and 4.7 us for the sums,
+// a chain of dependent loads; the gradient onto others' (50 MB, 8.5 us) 10.3 us.
 #include <type_traits>
 
 #include "launch.h"

@@ -13,6 +13,9 @@
 // lives in the registers of wpr waves (8 N elements a lane), so the mean and
 // then the centred squares are summed from registers; two sums instead of one
 // of squares keep the variance exact when the mean is large.
+// Measured at 16384 x 7168: forward (bf16 with residual, 940 MB) 156 us, backward
+// (fp32 gradient in, bf16 residual's added, 1.17 GB) 199 us: 6.0 and 5.9 TB/s,
+// where an elementwise add of that size runs at 5.95.
 #include <algorithm>
 #include <type_traits>
 
