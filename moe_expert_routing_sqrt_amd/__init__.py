@@ -71,11 +71,12 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
 # the current stream's handle without the Stream object around it (0.1 us
 # against 2.9 us a call), where this torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_index = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(device=None) -> int:
-    if device is None and _raw_stream is not None:
-        return _raw_stream(torch._C._cuda_getDevice())
+    if device is None and _raw_stream is not None and _device_index is not None:
+        return _raw_stream(_device_index())
     return torch.cuda.current_stream(device).cuda_stream
 
 

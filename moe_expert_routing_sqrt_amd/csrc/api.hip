@@ -572,17 +572,16 @@ int moe_bias_update(int64_t n_rows, int32_t E, const int32_t* counts, float gamm
 
 static bool is_float(int t) { return t == MOE_F32 || t == MOE_BF16; }
 
-// T, E and k of a balance loss, and its sequences
-static int balance_check(const moe_shape* s, int32_t n_seq, const int32_t* seq_offsets) {
+// T, E and k of a balance loss, and its number of sequences
+static int balance_check(const moe_shape* s, int32_t n_seq) {
   if (s == nullptr || s->T < 0 || s->E < 1 || s->k < 1 || s->k > s->E || n_seq < 1) return MOE_ERR_INVALID_ARG;
-  if (seq_offsets == nullptr && n_seq != 1) return MOE_ERR_INVALID_ARG;
   if (s->E > kMaxExperts || s->k > 16 || n_seq > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
   if (s->T > (int64_t)INT32_MAX / s->k) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
 size_t moe_balance_loss_workspace_size(const moe_shape* shape, int32_t n_seq) {
-  if (balance_check(shape, n_seq, reinterpret_cast<const int32_t*>(1)) != MOE_OK) return 0;
+  if (balance_check(shape, n_seq) != MOE_OK) return 0;
   return balance_loss_workspace_bytes(shape->T, shape->E, n_seq);
 }
 
@@ -590,8 +589,9 @@ int moe_balance_loss(const moe_shape* shape, const float* logits, const float* l
                      const int32_t* topk_idx, const int32_t* seq_offsets, int32_t n_seq,
                      const uint8_t* token_mask, float alpha, int32_t* counts, float* prob, float* dprob,
                      float* loss, void* ws, size_t ws_bytes, moe_stream_t stream) {
-  const int st = balance_check(shape, n_seq, seq_offsets);
+  const int st = balance_check(shape, n_seq);
   if (st != MOE_OK) return st;
+  if (seq_offsets == nullptr && n_seq != 1) return MOE_ERR_INVALID_ARG;
   if (!std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
   if (shape->T > 0 && (logits == nullptr || topk_idx == nullptr)) return MOE_ERR_INVALID_ARG;
   if (counts == nullptr || prob == nullptr || dprob == nullptr || loss == nullptr) return MOE_ERR_INVALID_ARG;
@@ -606,8 +606,9 @@ int moe_balance_loss_backward(const moe_shape* shape, const float* logits, const
                               const int32_t* seq_offsets, int32_t n_seq, const uint8_t* token_mask,
                               const float* dprob, const float* grad_loss, const float* d_extra, float* dlogits,
                               moe_stream_t stream) {
-  const int st = balance_check(shape, n_seq, seq_offsets);
+  const int st = balance_check(shape, n_seq);
   if (st != MOE_OK) return st;
+  if (seq_offsets == nullptr && n_seq != 1) return MOE_ERR_INVALID_ARG;
   if (shape->T == 0) return MOE_OK;
   if (logits == nullptr || dprob == nullptr || dlogits == nullptr) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_balance_loss_bwd(shape->T, shape->E, logits, logit_offset, seq_offsets, n_seq, token_mask,

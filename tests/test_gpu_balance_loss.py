@@ -247,3 +247,24 @@ def test_in_a_graph_and_on_another_stream():
         want = both()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want)), i
+
+
+def test_offsets_pass_32_bits():
+    """Over 2^31 logits, the counted tokens at the end: as the same tokens alone."""
+    dev = need_gpu()
+    T, E, k, tail = 2 ** 23 + 64 * 5, 256, 2, 64 * 7
+    assert T * E > 2 ** 31
+    logits = torch.zeros(T, E, device=dev)
+    idx = torch.zeros(T, k, dtype=torch.int32, device=dev)
+    logits[-tail:] = torch.randn(tail, E, device=dev)
+    idx[-tail:] = torch.randint(0, E, (tail, k), device=dev, dtype=torch.int32)
+    off = dev_i32([T - tail, T], dev)
+    a = M.balance_loss(_shape(T, E, k), logits, idx, 1.0, seq_offsets=off)
+    b = M.balance_loss(_shape(tail, E, k), logits[-tail:].contiguous(), idx[-tail:].contiguous(), 1.0)
+    ga = M.balance_loss_backward(_shape(T, E, k), logits, a[3], seq_offsets=off)
+    gb = M.balance_loss_backward(_shape(tail, E, k), logits[-tail:].contiguous(), b[3])
+    torch.cuda.synchronize()
+    assert torch.equal(a[1], b[1]) and torch.equal(a[3], b[3])
+    _close(a[0], host(b[0]), _rel(tail))
+    _close(a[2], host(b[2]), _rel(tail))
+    assert torch.equal(ga[-tail:], gb) and not ga[:-tail].any()

@@ -233,3 +233,21 @@ def test_on_another_stream_and_in_a_graph():
         d3 = M.layer_norm_backward(y3, s3, w, m3, r3, d_sum=r)
         torch.cuda.synchronize()
         assert torch.equal(y2, y3) and all(torch.equal(p, q) for p, q in zip(d2, d3)), i
+
+
+def test_offsets_pass_32_bits():
+    """Over 2^31 elements: the last rows are what the same rows give alone."""
+    dev = need_gpu()
+    rows, d, tail = 299_700, 7168, 400
+    assert rows * d > 2 ** 31
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device=dev)
+    x[-tail:] = torch.randn(tail, d, device=dev).to(torch.bfloat16)
+    w, b = torch.randn(d, device=dev), torch.randn(d, device=dev)
+    y, _, mean, rstd = M.layer_norm(x, w, b)
+    sy, _, smean, srstd = M.layer_norm(x[-tail:].contiguous(), w, b)
+    assert torch.equal(y[-tail:], sy) and torch.equal(mean[-tail:], smean) and torch.equal(rstd[-tail:], srstd)
+    dx, dw, db = M.layer_norm_backward(y, x, w, mean, rstd)
+    sx, _, _ = M.layer_norm_backward(sy, x[-tail:].contiguous(), w, smean, srstd)
+    torch.cuda.synchronize()
+    assert torch.equal(dx[-tail:], sx)
+    assert torch.isfinite(dw).all() and torch.isfinite(db).all()
