@@ -518,8 +518,8 @@ int moe_bias_update(int64_t n_rows, int32_t E, const int32_t* counts, float gamm
  *                indices may hold anything), or NULL
  *   counts [n_seq, E] int32, prob, dprob [n_seq, E] fp32, loss [1] fp32: out,
  *                written for every sequence, also with T = 0
- *   ws           moe_balance_loss_workspace_size(shape, n_seq) bytes; nothing
- *                in it needs to start at zero
+ *   ws           moe_balance_loss_workspace_size(shape, n_seq) bytes (0 for few
+ *                tokens: ws may be NULL); nothing in it needs to start at zero
  * The sums run in a fixed order (deterministic), in fp32.
  */
 #define MOE_MAX_SEQUENCES 65535

@@ -595,8 +595,8 @@ int moe_balance_loss(const moe_shape* shape, const float* logits, const float* l
   if (!std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
   if (shape->T > 0 && (logits == nullptr || topk_idx == nullptr)) return MOE_ERR_INVALID_ARG;
   if (counts == nullptr || prob == nullptr || dprob == nullptr || loss == nullptr) return MOE_ERR_INVALID_ARG;
-  if (ws == nullptr || ws_bytes < balance_loss_workspace_bytes(shape->T, shape->E, n_seq) || !aligned256(ws))
-    return MOE_ERR_WORKSPACE;
+  const size_t need = balance_loss_workspace_bytes(shape->T, shape->E, n_seq);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned256(ws))) return MOE_ERR_WORKSPACE;
   return hip_status(launch_balance_loss(shape->T, shape->E, shape->k, logits, logit_offset, topk_idx, seq_offsets,
                                         n_seq, token_mask, alpha, counts, prob, dprob, loss, ws,
                                         as_stream(stream)));

@@ -20,6 +20,7 @@
 // At T = 16384, E = 256, k = 8 (17 MB, 2.9 us of HBM) the forward takes 7.4 us for
 // the parts, 1.9 of them transcendentals and polynomial, and 4.7 us for the sums,
 // a chain of dependent loads; the gradient onto others' (50 MB, 8.5 us) 10.3 us.
+// At most 64 tokens take one launch (T = 16, E = 64: 4.1 us; two took 7.6).
 #include <type_traits>
 
 #include "launch.h"
@@ -279,64 +280,53 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(const LossArgs p
   }
 }
 
-// The same for tiles of many short sequences (E <= 256).  The probabilities go to
-// LDS once (zeros for tokens that do not count), and so do the slot counts of
-// each run, a sequence's stretch of tokens in the tile; then every thread takes
-// a (run, expert) pair and adds the run's tokens in order: one pass whatever the
-// number of runs.
+// The runs of a tile: a run is a sequence's stretch of tokens.  Lane i holds token
+// i's sequence (-1: none) and whether it counts.
+struct Runs {
+  uint64_t starts, ends, counted;
+  int run;  // of this lane's token
+  __device__ __forceinline__ Runs(int seq, bool on) {
+    const int lane = threadIdx.x & 63, before = __shfl_up(seq, 1, kWave);
+    starts = __ballot(seq >= 0 && (lane == 0 || before != seq));
+    ends = __ballot(seq < 0 && lane != 0 && before >= 0);  // a run followed by no sequence
+    counted = __ballot(on && seq >= 0);
+    run = __builtin_popcountll(starts & ((2ull << lane) - 1)) - 1;
+  }
+  __device__ __forceinline__ int count() const { return __builtin_popcountll(starts); }
+  __device__ __forceinline__ bool starts_here() const { return ((starts >> (threadIdx.x & 63)) & 1) != 0; }
+  // of the run that starts at this lane's token: its end, and its tokens that count
+  __device__ __forceinline__ int end(int ntok) const {
+    const uint64_t after = (starts | ends) & ~((2ull << (threadIdx.x & 63)) - 1);
+    return after != 0 ? __builtin_ctzll(after) : ntok;
+  }
+  __device__ __forceinline__ int tokens(int end) const {
+    const uint64_t mine = (end >= 64 ? ~0ull : (1ull << end) - 1) & ~((1ull << (threadIdx.x & 63)) - 1);
+    return __builtin_popcountll(counted & mine);
+  }
+};
+
+// Loads a tile's rows for tile_probabilities, every load before the first wait;
+// a token that does not count may hold anything, also NaN: its row is read but
+// never selected.
 template <bool FULL>
-__global__ __launch_bounds__(kThreads) void balance_part_short_kernel(const LossArgs p) {
-  constexpr int U = kTile / kWaves;  // tokens of a lane group (at one token a wave)
-  __shared__ __align__(16) float s_p[kTile * 256];
-  __shared__ uint32_t s_cnt[kTile * 256 / 2];  // counts of 16 bits: 64 k <= 1024
-  __shared__ int s_begin[kTile], s_seq[kTile], s_tok[kTile];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t t0 = (int64_t)blockIdx.x * kTile;
-  const int ntok = static_cast<int>(min((int64_t)kTile, p.T - t0));
-  const int E = p.E;
-  const SequenceSearch sequence_of(p.T, p.seq, p.n_seq);
-  const RowMap<1, FULL> m(E, p.log_lpt);
-  const int tpw = kWave / m.lpt;
-  // every load of the tile before the first wait; a token that does not count
-  // may hold anything, also NaN: its row is read but never selected
-  float pr[U][1][4], off[1][4] = {};
-  if (ntok > 0) {
+__device__ __forceinline__ void load_tile(const RowMap<1, FULL>& m, const float* logits, int ntok,
+                                          float (&pr)[kTile / kWaves][1][4]) {
+  const int wave = threadIdx.x >> 6, tpw = kWave / m.lpt;
 #pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int i = (v * kWaves + wave) * tpw + m.which;
-      m.load(p.logits + (t0 + min(i, ntok - 1)) * E, pr[v]);
-    }
-    if (p.offset != nullptr) m.load(p.offset, off);
+  for (int v = 0; v < kTile / kWaves; ++v) {
+    const int i = (v * kWaves + wave) * tpw + m.which;
+    m.load(logits + static_cast<int64_t>(min(i, ntok - 1)) * m.E, pr[v]);
   }
-  const int my_tok = tid / p.k;  // a slot of the tile per thread: 64 k <= 1024
-  const int my_e = my_tok < ntok ? p.idx[t0 * p.k + tid] : -1;
-  const bool on = lane < ntok && (p.mask == nullptr || p.mask[t0 + lane] != 0);
-  const int seq = sequence_of(t0 + lane);
-  if (blockIdx.x == 0 && tid == 0) *p.total = 0;
-  // runs: a token starts one where its sequence is not the token's before it
-  const int before = __shfl_up(seq, 1, kWave);
-  const uint64_t starts = __ballot(seq >= 0 && (lane == 0 || before != seq));
-  const uint64_t ends = __ballot(seq < 0 && lane != 0 && before >= 0);  // a run followed by no sequence
-  const uint64_t counted = __ballot(on && seq >= 0);
-  const int runs = __builtin_popcountll(starts);
-  const int run = __builtin_popcountll(starts & ((2ull << lane) - 1)) - 1;  // of this lane's token
-  if (wave == 0 && ((starts >> lane) & 1) != 0) {
-    const uint64_t after = (starts | ends) & ~((2ull << lane) - 1);
-    const int end = after != 0 ? __builtin_ctzll(after) : ntok;
-    const uint64_t mine = (end >= 64 ? ~0ull : (1ull << end) - 1) & ~((1ull << lane) - 1);
-    s_begin[run] = lane | end << 8;
-    s_seq[run] = seq;
-    s_tok[run] = __builtin_popcountll(counted & mine);
-  }
-  for (int i = tid; i < (runs * E + 1) / 2; i += kThreads) s_cnt[i] = 0;
-  __syncthreads();
-  const int my_run = __shfl(run, my_tok & 63, kWave);
-  if (my_e >= 0 && my_e < E && ((counted >> (my_tok & 63)) & 1) != 0) {
-    const int at = my_run * E + my_e;
-    atomicAdd(&s_cnt[at / 2], 1u << (16 * (at & 1)));
-  }
+}
+
+// The tile's probabilities into LDS, zeros for tokens that do not count.
+template <bool FULL>
+__device__ __forceinline__ void tile_probabilities(const RowMap<1, FULL>& m, int ntok, uint64_t counted,
+                                                   const float (&off)[1][4], float (&pr)[kTile / kWaves][1][4],
+                                                   float* s_p) {
+  const int wave = threadIdx.x >> 6, tpw = kWave / m.lpt;
 #pragma unroll
-  for (int v = 0; v < U; ++v) {
+  for (int v = 0; v < kTile / kWaves; ++v) {
     if ((v * kWaves + wave) * tpw >= ntok) break;  // uniform over the wave
     const int i = (v * kWaves + wave) * tpw + m.which;
     float total = 0.0f;
@@ -351,24 +341,149 @@ __global__ __launch_bounds__(kThreads) void balance_part_short_kernel(const Loss
     const float inv = some ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) pr[v][0][j] = some ? pr[v][0][j] * inv : 0.0f;
-    if (i < ntok) m.store(s_p + i * E, pr[v]);
+    if (i < ntok) m.store(s_p + i * m.E, pr[v]);
   }
+}
+
+// sum of column e over tokens [begin, end), in order
+__device__ __forceinline__ float run_sum(const float* s_p, int E, int e, int begin, int end) {
+  float v = 0.0f;
+  for (int i = begin; i < end; i += 8) {  // 8 reads in flight
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = s_p[min(i + j, end - 1) * E + e];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v += i + j < end ? t[j] : 0.0f;
+  }
+  return v;
+}
+
+// The parts for tiles of many short sequences (E <= 256).  The probabilities go to
+// LDS once, and so do the slot counts of each run; then every thread takes a
+// (run, expert) pair: one pass whatever the number of runs.
+template <bool FULL>
+__global__ __launch_bounds__(kThreads) void balance_part_short_kernel(const LossArgs p) {
+  __shared__ __align__(16) float s_p[kTile * 256];
+  __shared__ uint32_t s_cnt[kTile * 256 / 2];  // counts of 16 bits: 64 k <= 1024
+  __shared__ int s_begin[kTile], s_end[kTile], s_seq[kTile], s_tok[kTile];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t0 = (int64_t)blockIdx.x * kTile;
+  const int ntok = static_cast<int>(min((int64_t)kTile, p.T - t0));
+  const int E = p.E;
+  const SequenceSearch sequence_of(p.T, p.seq, p.n_seq);
+  const RowMap<1, FULL> m(E, p.log_lpt);
+  float pr[kTile / kWaves][1][4], off[1][4] = {};
+  if (ntok > 0) {
+    load_tile<FULL>(m, p.logits + t0 * E, ntok, pr);
+    if (p.offset != nullptr) m.load(p.offset, off);
+  }
+  const int my_tok = tid / p.k;  // a slot of the tile per thread: 64 k <= 1024
+  const int my_e = my_tok < ntok ? p.idx[t0 * p.k + tid] : -1;
+  const bool on = lane < ntok && (p.mask == nullptr || p.mask[t0 + lane] != 0);
+  const int seq = sequence_of(t0 + lane);
+  if (blockIdx.x == 0 && tid == 0) *p.total = 0;
+  const Runs runs(seq, on);
+  if (wave == 0 && runs.starts_here()) {
+    const int end = runs.end(ntok);
+    s_begin[runs.run] = lane;
+    s_end[runs.run] = end;
+    s_seq[runs.run] = seq;
+    s_tok[runs.run] = runs.tokens(end);
+  }
+  const int pairs = runs.count() * E;
+  for (int i = tid; i < (pairs + 1) / 2; i += kThreads) s_cnt[i] = 0;
   __syncthreads();
-  for (int id = tid; id < runs * E; id += kThreads) {
+  const int my_run = __shfl(runs.run, my_tok & 63, kWave);
+  if (my_e >= 0 && my_e < E && ((runs.counted >> (my_tok & 63)) & 1) != 0) {
+    const int at = my_run * E + my_e;
+    atomicAdd(&s_cnt[at / 2], 1u << (16 * (at & 1)));
+  }
+  tile_probabilities<FULL>(m, ntok, runs.counted, off, pr, s_p);
+  __syncthreads();
+  for (int id = tid; id < pairs; id += kThreads) {
     const int r = id / E, e = id - r * E;
-    const int begin = s_begin[r] & 0xFF, end = s_begin[r] >> 8;
-    float v = 0.0f;
-    for (int i = begin; i < end; i += 8) {  // 8 reads in flight
-      float t[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = s_p[min(i + j, end - 1) * E + e];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v += i + j < end ? t[j] : 0.0f;
-    }
     const int64_t row = (int64_t)blockIdx.x + s_seq[r];
-    p.psum[row * E + e] = v;
+    p.psum[row * E + e] = run_sum(s_p, E, e, s_begin[r], s_end[r]);
     p.pcnt[row * E + e] = static_cast<int32_t>((s_cnt[id / 2] >> (16 * (id & 1))) & 0xFFFFu);
     if (e == 0) p.ptok[row] = s_tok[r];
+  }
+}
+
+// At most a tile of tokens: everything in one work-group and one launch, without
+// parts; the sums and counts of all sequences stay in LDS.
+constexpr int kSmallTable = 8192, kSmallSeqs = 1024;  // sequences times experts; sequences
+
+struct SmallArgs {
+  LossArgs in;  // its parts are not used
+  float alpha;
+  int32_t* counts;
+  float* prob;
+  float* dprob;
+  float* loss;
+};
+
+template <bool FULL>
+__global__ __launch_bounds__(kThreads) void balance_small_kernel(const SmallArgs a) {
+  __shared__ __align__(16) float s_p[kTile * 256];
+  __shared__ float s_sum[kSmallTable];
+  __shared__ int s_cnt[kSmallTable];
+  __shared__ int s_tok[kSmallSeqs];
+  __shared__ int s_begin[kTile], s_end[kTile], s_seq[kTile];
+  __shared__ float s_red[kWaves];
+  const LossArgs& p = a.in;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int E = p.E, ntok = static_cast<int>(p.T), table = p.n_seq * E;
+  const SequenceSearch sequence_of(p.T, p.seq, p.n_seq);
+  const RowMap<1, FULL> m(E, p.log_lpt);
+  float pr[kTile / kWaves][1][4], off[1][4] = {};
+  if (ntok > 0) {
+    load_tile<FULL>(m, p.logits, ntok, pr);
+    if (p.offset != nullptr) m.load(p.offset, off);
+  }
+  const int my_tok = tid / p.k;  // a slot per thread: 64 k <= 1024
+  const int my_e = my_tok < ntok ? p.idx[tid] : -1;
+  const bool on = lane < ntok && (p.mask == nullptr || p.mask[lane] != 0);
+  const int seq = sequence_of(lane);
+  const Runs runs(seq, on);
+  for (int i = tid; i < table; i += kThreads) {
+    s_sum[i] = 0.0f;
+    s_cnt[i] = 0;
+  }
+  for (int i = tid; i < p.n_seq; i += kThreads) s_tok[i] = 0;
+  __syncthreads();
+  if (wave == 0 && runs.starts_here()) {
+    const int end = runs.end(ntok);
+    s_begin[runs.run] = lane;
+    s_end[runs.run] = end;
+    s_seq[runs.run] = seq;
+    s_tok[seq] = runs.tokens(end);
+  }
+  const int my_seq = __shfl(seq, my_tok & 63, kWave);
+  if (my_e >= 0 && my_e < E && ((runs.counted >> (my_tok & 63)) & 1) != 0) atomicAdd(&s_cnt[my_seq * E + my_e], 1);
+  tile_probabilities<FULL>(m, ntok, runs.counted, off, pr, s_p);
+  __syncthreads();
+  for (int id = tid; id < runs.count() * E; id += kThreads) {
+    const int r = id / E, e = id - r * E;
+    s_sum[s_seq[r] * E + e] = run_sum(s_p, E, e, s_begin[r], s_end[r]);
+  }
+  __syncthreads();
+  float loss = 0.0f;
+  for (int id = tid; id < table; id += kThreads) {
+    const int t = s_tok[id / E];
+    const float per = t > 0 ? 1.0f / static_cast<float>(t) : 0.0f;
+    const float f = static_cast<float>(s_cnt[id]) * (static_cast<float>(E) / static_cast<float>(p.k)) * per;
+    const float P = s_sum[id] * per;
+    a.counts[id] = s_cnt[id];
+    a.prob[id] = P;
+    a.dprob[id] = f * per * (a.alpha / static_cast<float>(p.n_seq));
+    loss = __builtin_fmaf(f, P, loss);
+  }
+  loss = wave_sum(loss);
+  if (lane == 0) s_red[wave] = loss;
+  __syncthreads();
+  if (tid < kWave) {
+    loss = row16_sum(s_red[lane & 15]);
+    if (tid == 0) *a.loss = loss * (a.alpha / static_cast<float>(p.n_seq));
   }
 }
 
@@ -588,11 +703,29 @@ LossWs loss_ws(int64_t T, int E, int n_seq) {
 
 }  // namespace
 
-size_t balance_loss_workspace_bytes(int64_t T, int E, int n_seq) { return loss_ws(T, E, n_seq).total; }
+// One work-group for at most a tile, where its tables fit in LDS: T = 1, E = 256
+// 4.0 us against 7.5 in two launches, 16 x 64 4.1 against 7.6, 64 x 256 7.9 against
+// 9.7; a second tile on the same CU loses (128 x 16 7.8 against 7.6, 256 x 16 12.7
+// against 7.9).
+static bool small_loss(int64_t T, int E, int n_seq) {
+  return E <= 256 && T <= kTile && n_seq <= kSmallSeqs && static_cast<int64_t>(n_seq) * E <= kSmallTable;
+}
+
+size_t balance_loss_workspace_bytes(int64_t T, int E, int n_seq) {
+  return small_loss(T, E, n_seq) ? 0 : loss_ws(T, E, n_seq).total;
+}
 
 hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, const float* offset, const int32_t* idx,
                                const int32_t* seq, int n_seq, const uint8_t* mask, float alpha, int32_t* counts,
                                float* prob, float* dprob, float* loss, void* ws, hipStream_t s) {
+  if (small_loss(T, E, n_seq)) {
+    const SmallArgs a{{T, E, lanes_log(E), k, n_seq, logits, offset, idx, seq, mask, nullptr, nullptr, nullptr,
+                       nullptr},
+                      alpha, counts, prob, dprob, loss};
+    if (full_rows(E)) hipLaunchKernelGGL(balance_small_kernel<true>, dim3(1), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL(balance_small_kernel<false>, dim3(1), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
   const LossWs w = loss_ws(T, E, n_seq);
   char* base = static_cast<char*>(ws);
   float* psum = reinterpret_cast<float*>(base + w.psum);

@@ -10,7 +10,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import (MOE_E4M3, MOE_F32, MOE_FP8_TILE, MOE_OP_LAYER_NORM_BACKWARD, MoeShape, _dt, _lib, _need, _stream,
-               lib, workspace_bytes)
+               _ws_len, lib, workspace_bytes)
 from . import _ptr as _checked_ptr
 from .layer import MoELayer
 
@@ -93,13 +93,18 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                                        _arg(weight, d, "weight", _f32), _arg(mean, rows, "mean", _f32),
                                        _arg(rstd, rows, "rstd", _f32), _arg(d_sum, n, "d_sum", dt),
                                        _arg(dx, n, "dx"), _dt(dx), _arg(dw, d, "dw", _f32), _arg(db, d, "db", _f32),
-                                       _arg(ws, 0, "ws"), 0 if ws is None else ws.numel() * ws.element_size(),
-                                       _stream())
+                                       _arg(ws, 0, "ws"), _ws_len(ws), _stream())
     _lib.check("moe_layer_norm_backward", st)
     return dx, dw, db
 
 
 # ---------------------------------------------------------------- balance loss
+
+@functools.lru_cache(maxsize=1024)
+def _loss_ws_floats(T: int, E: int, k: int, n: int) -> int:
+    sh = MoeShape(T, 1, E, 1, 1, k, 1, 1)
+    return lib().moe_balance_loss_workspace_size(ctypes.byref(sh), n) // 4
+
 
 def _sequences(T: int, seq_offsets, token_mask):
     """(number of sequences, offsets pointer, mask pointer)"""
@@ -122,7 +127,6 @@ def balance_loss(sh: MoeShape, logits: torch.Tensor, idx: torch.Tensor, alpha: f
     if idx.dtype != _i32:
         raise TypeError("idx must be int32")
     n, off_p, mask_p = _sequences(T, seq_offsets, token_mask)
-    L, shape = lib(), ctypes.byref(sh)
     if loss is None:
         loss = logits.new_empty(1)
     if counts is None:
@@ -131,13 +135,15 @@ def balance_loss(sh: MoeShape, logits: torch.Tensor, idx: torch.Tensor, alpha: f
         prob = logits.new_empty((n, E))
     if dprob is None:
         dprob = torch.empty_like(prob)
-    if ws is None:
-        ws = logits.new_empty(max(1, L.moe_balance_loss_workspace_size(shape, n) // 4))
+    need = 0 if ws is not None else _loss_ws_floats(T, E, k, n)
+    if need:
+        ws = logits.new_empty(need)
     m = n * E
-    st = L.moe_balance_loss(shape, _arg(logits, T * E, "logits", _f32), _arg(logit_offset, E, "logit_offset", _f32),
-                            _arg(idx, T * k, "idx"), off_p, n, mask_p, alpha, _arg(counts, m, "counts", _i32),
-                            _arg(prob, m, "prob", _f32), _arg(dprob, m, "dprob", _f32), _arg(loss, 1, "loss", _f32),
-                            _arg(ws, 0, "ws"), ws.numel() * ws.element_size(), _stream())
+    st = lib().moe_balance_loss(ctypes.byref(sh), _arg(logits, T * E, "logits", _f32),
+                                _arg(logit_offset, E, "logit_offset", _f32), _arg(idx, T * k, "idx"), off_p, n,
+                                mask_p, alpha, _arg(counts, m, "counts", _i32), _arg(prob, m, "prob", _f32),
+                                _arg(dprob, m, "dprob", _f32), _arg(loss, 1, "loss", _f32), _arg(ws, 0, "ws"),
+                                _ws_len(ws), _stream())
     _lib.check("moe_balance_loss", st)
     return loss, counts, prob, dprob
 
@@ -283,9 +289,8 @@ class MoEBlock:
         n = 1 if seq_offsets is None else seq_offsets.numel() - 1
         if n not in self._loss_bufs:
             new = la.logits.new_empty
-            size = lib().moe_balance_loss_workspace_size(ctypes.byref(la.sh), n)
             self._loss_bufs[n] = dict(loss=new(1), counts=new((n, la.E), dtype=_i32), prob=new((n, la.E)),
-                                      dprob=new((n, la.E)), ws=new(max(1, size // 4)))
+                                      dprob=new((n, la.E)), ws=new(max(1, _loss_ws_floats(la.T, la.E, la.k, n))))
         self.loss, self.counts, self.prob, self.dprob = balance_loss(
             la.sh, la.logits, la.idx, self.alpha, seq_offsets, token_mask, la.logit_offset, **self._loss_bufs[n])
         return out, self.stream

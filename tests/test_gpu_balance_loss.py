@@ -52,7 +52,11 @@ CASES = [  # T, E, k, sequences (0: no offsets), ragged, masked
     (500, 100, 16, 3, True, False), (200, 300, 4, 4, True, True), (150, 513, 3, 2, False, False),
     (90, 1024, 16, 3, True, True), (4099, 64, 6, 1, False, False), (40, 24, 3, 1000, True, True),
     (5000, 12, 2, 2, False, True), (700, 256, 16, 40, True, True), (333, 30, 3, 60, True, False),
-    (64, 256, 16, 64, False, False), (900, 2, 2, 300, True, True), (3000, 200, 5, 9, True, True)]
+    (64, 256, 16, 64, False, False), (900, 2, 2, 300, True, True), (3000, 200, 5, 9, True, True),
+    (64, 256, 8, 32, True, True), (64, 256, 8, 33, True, True), (65, 16, 2, 1, False, True),
+    (63, 127, 7, 3, True, True), (64, 16, 4, 9, True, True),
+    (129, 3, 2, 1000, True, True), (30, 3, 2, 1025, True, True), (64, 128, 16, 1, False, False),
+    (130, 64, 16, 20, True, True), (30, 7, 2, 1024, True, True)]
 
 
 @pytest.mark.parametrize("T,E,k,n,ragged,masked", CASES)

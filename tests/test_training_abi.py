@@ -63,7 +63,7 @@ def _sh(T=16, E=16, k=4):
 
 def _loss(sh=None, logits=FAKE, idx=FAKE, off=FAKE, n=2, alpha=0.1, counts=FAKE, prob=FAKE, dprob=FAKE, loss=FAKE,
           ws=FAKE, size=1 << 30):
-    sh = _sh() if sh is None else sh
+    sh = _sh(T=1000) if sh is None else sh
     return L.moe_balance_loss(ctypes.byref(sh), logits, None, idx, off, n, None, alpha, counts, prob, dprob, loss, ws,
                               size, None)
 
@@ -79,10 +79,12 @@ def test_balance_loss_refusals(kw, want):
 
 
 def test_balance_loss_workspace():
-    for T, E, n in ((0, 8, 1), (1, 8, 1), (5000, 256, 7)):
+    for T, E, n in ((65, 8, 1), (0, 512, 1), (10, 256, 40), (5000, 256, 7)):
         sh = _sh(T, E)
         need = L.moe_balance_loss_workspace_size(ctypes.byref(sh), n)
         assert need > 0 and _loss(sh=sh, n=n, size=need - 1) == WS
+    for T, E, n in ((0, 8, 1), (64, 256, 32), (1, 1, 1024)):  # one launch, no parts
+        assert L.moe_balance_loss_workspace_size(ctypes.byref(_sh(T, E, 1)), n) == 0
     assert L.moe_balance_loss_workspace_size(ctypes.byref(_sh()), 0) == 0
     assert L.moe_balance_loss_workspace_size(None, 1) == 0
 
