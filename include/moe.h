@@ -554,7 +554,8 @@ int moe_balance_loss_backward(const moe_shape* shape, const float* logits, const
  *   weight, bias [d] fp32; bias may be NULL
  *   sum          [rows, d] in x_dtype out: s (with a residual, else NULL); may
  *                be x or residual
- *   y            [rows, d] in y_dtype (MOE_BF16 or MOE_F32) out
+ *   y            [rows, d] in y_dtype (MOE_BF16 or MOE_F32) out; may be x or
+ *                residual where the types agree, not sum
  *   mean, rstd   [rows] fp32 out, both or neither (NULL)
  * 1 <= d <= 32768, any element alignment; eps >= 0.  Statistics in fp32.
  * rows = 0 is a no-op.

@@ -630,6 +630,7 @@ int moe_layer_norm(int64_t rows, int32_t d, const void* x, const void* residual,
   if ((residual == nullptr) != (sum == nullptr) || (mean == nullptr) != (rstd == nullptr)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   if (x == nullptr || weight == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
+  if (y == sum || ((y == x || y == residual) && y_dtype != x_dtype)) return MOE_ERR_INVALID_ARG;  // rows would overlap
   return hip_status(launch_layer_norm(rows, d, x, residual, x_dtype, weight, bias, eps, sum, y, y_dtype, mean, rstd,
                                       as_stream(stream)));
 }
@@ -646,6 +647,7 @@ int moe_layer_norm_backward(int64_t rows, int32_t d, const void* dy, int dy_dtyp
     if (dy == nullptr || x == nullptr || weight == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr)
       return MOE_ERR_INVALID_ARG;
     if (dx == dy || dx == x) return MOE_ERR_INVALID_ARG;  // both are read while dx is written
+    if (dx == d_sum && dx_dtype != x_dtype) return MOE_ERR_INVALID_ARG;
     const size_t need = layer_norm_bwd_workspace_bytes(rows, d);
     if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned256(ws))) return MOE_ERR_WORKSPACE;
   }

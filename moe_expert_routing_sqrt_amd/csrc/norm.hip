@@ -169,9 +169,9 @@ struct NormBwdArgs {
 // A work-group takes every gridDim.x-th row and keeps its columns' dw and db in
 // registers; their sums leave once at the end.  With one piece a lane the
 // weights stay there too, and the next row's loads are issued before this one
-// is reduced; rows of two (d > 8192) have no registers for either.  MULTI (rows of at most 4 waves): the work-group's 8 waves take several
-// rows at once, side by side, and join their sums in LDS, so that the parts
-// stay one per work-group.
+// is reduced; rows of two (d > 8192) have no registers for either.  MULTI (rows
+// of at most 4 waves): the work-group's 8 waves take several rows at once, side
+// by side, and join their sums in LDS, so that the parts stay one per work-group.
 constexpr int kMultiWaves = 8;
 template <typename TD, typename TX, typename TO, bool DS, int N, bool MULTI, bool STREAM>
 __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBwdArgs p) {

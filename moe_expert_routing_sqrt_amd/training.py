@@ -277,7 +277,8 @@ class MoEBlock:
                                    device=dev)
         self.opt_args = dict(lr=lr, betas=betas, states=states, weight_decay=weight_decay)
         self.master, self.opt = master, None
-        self._loss_bufs = {}  # of balance_loss, by the number of sequences
+        # balance_loss's buffers by the number of sequences: what a captured graph writes stays where it is
+        self._loss_bufs = {}
 
     def forward(self, delta: torch.Tensor, stream: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
                 token_mask: Optional[torch.Tensor] = None):

@@ -90,6 +90,27 @@ def test_forward_no_bias_no_stats_given_buffers():
     assert s2.data_ptr() == xa.data_ptr()
 
 
+@pytest.mark.parametrize("rows,d", [(1, 1), (900, 5), (300, 513), (700, 1025), (40, 8200), (3, 16385)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_forward_in_place(rows, d, dt):
+    """y or the sum over an input; 513, 1025 and 8200: a row's last piece begins a wave or a lane's second piece."""
+    dev = need_gpu()
+    g = torch.Generator(device=dev).manual_seed(5)
+    x, r = _rows(g, rows, d, dt, dev), _rows(g, rows, d, dt, dev)
+    w = torch.randn(d, generator=g, device=dev)
+    y0, s0, _, _ = M.layer_norm(x, w, residual=r)
+    for y, s in ((0, None), (1, None), (None, 0), (None, 1), (0, 1), (1, 0)):
+        ab = [x.clone(), r.clone()]
+        y1, s1, _, _ = M.layer_norm(ab[0], w, residual=ab[1], y=None if y is None else ab[y],
+                                    sum_out=None if s is None else ab[s])
+        assert torch.equal(y1, y0) and torch.equal(s1, s0)
+    xc = x.clone()
+    M.layer_norm(xc, w, y=xc)
+    assert torch.equal(xc, M.layer_norm(x, w)[0])
+    with pytest.raises(M.MoeError):
+        M.layer_norm(x, w, residual=r, y=xc, sum_out=xc)
+
+
 def test_forward_offset_rows():
     """A mean far above the spread: squares of the centred values keep the variance."""
     dev = need_gpu()

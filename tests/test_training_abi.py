@@ -22,6 +22,7 @@ def _norm(rows=4, d=8, x=FAKE, r=None, xt=1, w=FAKE, b=None, eps=1e-5, s=None, y
     (dict(rows=-1), INV), (dict(d=0), INV), (dict(x=None), INV), (dict(w=None), INV), (dict(y=None), INV),
     (dict(xt=2), INV), (dict(yt=7), INV), (dict(eps=-1e-9), INV), (dict(eps=NAN), INV), (dict(eps=INF), INV),
     (dict(r=FAKE), INV), (dict(s=FAKE), INV), (dict(mean=None), INV), (dict(rstd=None), INV),
+    (dict(xt=0), INV), (dict(x=0x2000, r=FAKE, s=0x3000, xt=0), INV), (dict(x=0x2000, r=0x3000, s=FAKE), INV),
     (dict(d=32769), UNS), (dict(rows=2 ** 31), UNS), (dict(rows=0, x=None, y=None), 0)])
 def test_layer_norm_refusals(kw, want):
     assert _norm(**kw) == want
@@ -38,8 +39,8 @@ def _norm_bwd(rows=1000, d=8, dy=DY, dt=1, x=X, xt=1, w=FAKE, mean=FAKE, rstd=FA
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), INV), (dict(d=-3), INV), (dict(dy=None), INV), (dict(x=None), INV), (dict(w=None), INV),
     (dict(mean=None), INV), (dict(rstd=None), INV), (dict(dx=None), INV), (dict(dw=None), INV), (dict(dt=2), INV),
-    (dict(xt=-1), INV), (dict(ot=3), INV), (dict(dx=DY), INV), (dict(dx=X), INV), (dict(d=40000), UNS), (dict(ws=None), WS), (dict(ws=FAKE + 8), WS),
-    (dict(rows=0, dw=None), INV)])
+    (dict(xt=-1), INV), (dict(ot=3), INV), (dict(dx=DY), INV), (dict(dx=X), INV), (dict(ds=FAKE, ot=0), INV),
+    (dict(d=40000), UNS), (dict(ws=None), WS), (dict(ws=FAKE + 8), WS), (dict(rows=0, dw=None), INV)])
 def test_layer_norm_backward_refusals(kw, want):
     assert _norm_bwd(**kw) == want
 
