@@ -20,8 +20,8 @@
 // consecutive elements, so that every fp32 access of a wave is one solid
 // kilobyte (32 lanes share a tile's scale), stores pass the caches by, as do the
 // loads of large launches, and a work-group ends after one quad a lane, the next
-// one's loads filling its place.  Measured on 113 M bf16 weights with fp32 masters, us (TB/s), fp32 /
-// 8-bit states:
+// one's loads filling its place.  Measured on 113 M bf16 weights with fp32
+// masters, us (TB/s), fp32 / 8-bit states:
 //   one quad, streaming loads and stores   581 (5.85) / 326 (6.31)
 //   stores through the caches              632 (5.37) / 374 (5.49)
 //   loads and stores through the caches    627 (5.42) / 369 (5.56)
@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPerGroup = kThreads * 4;  // elements of a work-group: one quad a lane
-constexpr int kMaxTensors = 48;       // per launch: the arguments stay under 4 KB
+constexpr int kMaxTensors = 48;         // per launch: the arguments stay under 4 KB
 
 struct Item {
   int64_t n;
@@ -297,7 +297,8 @@ hipError_t launch_kind(AdamArgs& a, const Kind& k, hipStream_t s) {
 
 }  // namespace
 
-// One launch per kind (weight, gradient and state types) and kMaxTensors tensors.
+// One launch per kind (weight, gradient and state types) and kMaxTensors tensors,
+// or as many of their elements as a launch reaches (17 G).
 hipError_t launch_adamw(int n_tensors, const moe_adamw_tensor* t, const moe_adamw_params& h, const float* grad_scale,
                         hipStream_t s) {
   AdamArgs a;
@@ -314,7 +315,8 @@ hipError_t launch_adamw(int n_tensors, const moe_adamw_tensor* t, const moe_adam
   auto kind = [](const moe_adamw_tensor& x) {
     return Kind{x.param_dtype, x.grad_dtype, x.state_dtype, x.master != nullptr};
   };
-  constexpr int64_t kMaxGroups = INT32_MAX;
+  constexpr int64_t kMaxGroups = UINT32_MAX / kThreads;  // a launch has under 2^32 threads
+  auto ahead = [](const void* q, int64_t bytes) { return static_cast<char*>(const_cast<void*>(q)) + bytes; };
   for (int i = 0; i < n_tensors; ++i) {
     const Kind k = kind(t[i]);
     bool first = t[i].n > 0;
@@ -326,14 +328,21 @@ hipError_t launch_adamw(int n_tensors, const moe_adamw_tensor* t, const moe_adam
     for (int j = i; j < n_tensors; ++j) {
       const moe_adamw_tensor& x = t[j];
       if (x.n == 0 || !(kind(x) == k)) continue;
-      const int64_t groups = (x.n + kPerGroup - 1) / kPerGroup;
-      if (a.count == kMaxTensors || (a.count > 0 && a.first[a.count] + groups > kMaxGroups)) {
-        if ((e = launch_kind(a, k, s)) != hipSuccess) return e;
+      const int64_t bp = k.p == MOE_F32 ? 4 : 2, bg = k.g == MOE_F32 ? 4 : 2, bs = k.state == MOE_F32 ? 4 : 1;
+      for (int64_t at = 0; at < x.n;) {  // at: whole work-groups, so whole tiles; one turn under 2^34 elements
+        if (a.count == kMaxTensors || (a.count > 0 && a.first[a.count] == kMaxGroups)) {
+          if ((e = launch_kind(a, k, s)) != hipSuccess) return e;
+        }
+        const int64_t left = (x.n - at + kPerGroup - 1) / kPerGroup, room = kMaxGroups - a.first[a.count];
+        const int64_t groups = left < room ? left : room, n = left <= room ? x.n - at : groups * kPerGroup;
+        const bool bits8 = k.state == MOE_E4M3;
+        a.item[a.count] = {n, ahead(x.param, at * bp), ahead(x.grad, at * bg), k.master ? x.master + at : nullptr,
+                           ahead(x.m, at * bs), ahead(x.v, at * bs), bits8 ? x.m_scale + at / 128 : nullptr,
+                           bits8 ? x.v_scale + at / 128 : nullptr, static_cast<float>(1.0 - h.lr * x.weight_decay)};
+        a.first[a.count + 1] = a.first[a.count] + groups;
+        ++a.count;
+        at += n;
       }
-      a.item[a.count] = {x.n, x.param, x.grad, x.master, x.m, x.v, x.m_scale, x.v_scale,
-                         static_cast<float>(1.0 - h.lr * x.weight_decay)};
-      a.first[a.count + 1] = a.first[a.count] + groups;
-      ++a.count;
     }
     if (a.count > 0 && (e = launch_kind(a, k, s)) != hipSuccess) return e;
   }

@@ -204,6 +204,37 @@ def test_large_tensor_offsets_pass_32_bits():
     assert torch.equal(a.m_scale[0][(n - tail) // 128:], b.m_scale[0])
 
 
+def test_more_elements_than_a_launch_reaches():
+    """Over 2^34 elements, the most 2^32 threads take at 4 each: around the place where the second launch begins
+    and at the end they are updated as small tensors of the same values are, and all others are left at zero."""
+    dev = need_gpu()
+    first, n = 5000, 2 ** 34 + 3000
+    if torch.cuda.mem_get_info()[0] < 120 * 2 ** 30:
+        pytest.skip("needs 120 GB of GPU memory")
+    places = [((2 ** 32 // 256 - 1 - 5) * 1024 - 2048, 4096), (n - 2000, 2000)]  # 5 work-groups go to the first tensor
+    places = [(at // 128 * 128, k) for at, k in places]
+    small = torch.randn(first, device=dev).to(torch.bfloat16)
+    p, g = (torch.zeros(n, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    refs = []
+    for at, k in places:
+        k = min(k, n - at)
+        p[at:at + k], g[at:at + k] = torch.randn(k, device=dev).to(p.dtype), torch.randn(k, device=dev).to(p.dtype)
+        refs.append((at, k, p[at:at + k].clone(), g[at:at + k].clone()))
+    a = M.AdamW([small, p], [small.clone(), g], lr=0.01, states="e4m3")
+    b = M.AdamW([r[2] for r in refs], [r[3] for r in refs], lr=0.01, states="e4m3")
+    a.step()
+    b.step()
+    torch.cuda.synchronize()
+    end = 0
+    for i, (at, k, want, _) in enumerate(refs):
+        assert not p[end:at].any() and not a.m[1][end:at].any()
+        assert torch.equal(p[at:at + k], want)
+        assert torch.equal(a.m[1][at:at + k], b.m[i]) and torch.equal(a.v[1][at:at + k], b.v[i])
+        assert torch.equal(a.v_scale[1][at // 128:-(-(at + k) // 128)], b.v_scale[i])
+        end = at + k
+    assert end == n or not p[end:].any()
+
+
 def test_on_another_stream_and_in_a_graph():
     """A captured step repeats its own step number on every replay."""
     dev = need_gpu()
