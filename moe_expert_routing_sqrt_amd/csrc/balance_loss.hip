@@ -162,17 +162,6 @@ struct RowMap {
   }
 };
 
-// sum over the aligned group of lpt lanes
-__device__ __forceinline__ float group_sum(float v, int lpt) {
-  if (lpt == kWave) return wave_sum(v);
-  if (lpt >= 2) v += dpp_f32<0xB1>(v);
-  if (lpt >= 4) v += dpp_f32<0x4E>(v);
-  if (lpt >= 8) v += dpp_f32<0x141>(v);
-  if (lpt >= 16) v += dpp_f32<0x140>(v);
-  if (lpt >= 32) v += __shfl_xor(v, 16, kWave);
-  return v;
-}
-
 // ---------------------------------------------------------------- forward
 struct LossArgs {
   int64_t T;

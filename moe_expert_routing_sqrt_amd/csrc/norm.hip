@@ -30,7 +30,7 @@ constexpr int kMaxWaves = 16;
 // ---------------------------------------------------------------- forward
 struct NormArgs {
   int64_t rows;
-  int d, wpr, rpb;  // waves per row, rows per work-group
+  int d, wpr, rpb, lg;  // waves per row, rows per work-group; wpr = 1: 2^lg lanes per row
   const void* x;
   const void* r;
   const float* w;
@@ -45,9 +45,9 @@ struct NormArgs {
 // Sum over the waves of a row, the same tree on every call.  s_red: 16 slots,
 // zero where there is no wave; every lane reads the slot of its place in its
 // 16-lane DPP row, so one LDS read and four DPP adds end it.
-__device__ __forceinline__ float row_sum(float v, float* s_red, int wpr) {
+__device__ __forceinline__ float row_sum(float v, float* s_red, int wpr, int lg) {
+  if (wpr == 1) return group_sum(v, 1 << lg);
   v = wave_sum(v);
-  if (wpr == 1) return v;
   if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
   __syncthreads();
   return row16_sum(s_red[threadIdx.x & 15]);
@@ -62,11 +62,11 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_fwd_kernel(const NormAr
   __shared__ float s_red[2][kMaxWaves];
   if (threadIdx.x < 2 * kMaxWaves) s_red[threadIdx.x / kMaxWaves][threadIdx.x % kMaxWaves] = 0.0f;
   __syncthreads();
-  const int slot = p.wpr == 1 ? threadIdx.x >> 6 : 0;
-  const int rt = p.wpr == 1 ? threadIdx.x & 63 : threadIdx.x;  // thread within the row
+  const int slot = p.wpr == 1 ? threadIdx.x >> p.lg : 0;
+  const int rt = threadIdx.x - (slot << p.lg);  // thread within the row
   const int64_t step = (int64_t)gridDim.x * p.rpb;
   int64_t row = (int64_t)blockIdx.x * p.rpb + slot;
-  if (row >= p.rows) return;  // whole waves, and no barrier follows where rpb > 1 (then wpr = 1)
+  if (row >= p.rows) return;  // whole rows, and no barrier follows where rpb > 1 (then wpr = 1)
   const TX* const x = static_cast<const TX*>(p.x);
   const TX* const r = static_cast<const TX*>(p.r);
   Piece q[N];
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_fwd_kernel(const NormAr
         if constexpr (RES) load8<STREAM>(rr[i], r + next, q[i]);
       }
     }
-    const float mean = row_sum(acc, s_red[0], p.wpr) * inv_d;
+    const float mean = row_sum(acc, s_red[0], p.wpr, p.lg) * inv_d;
     acc = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_fwd_kernel(const NormAr
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc = __builtin_fmaf(f[i][j], f[i][j], acc);
     }
-    const float var = row_sum(acc, s_red[1], p.wpr) * inv_d;
+    const float var = row_sum(acc, s_red[1], p.wpr, p.lg) * inv_d;
     const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
     if (rt == 0 && p.mean != nullptr) {
       p.mean[row] = mean;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_fwd_kernel(const NormAr
 // ---------------------------------------------------------------- backward
 struct NormBwdArgs {
   int64_t rows;
-  int d, wpr, rpb;  // waves per row, rows at once in a work-group
+  int d, wpr, rpb, lg;  // waves per row, rows at once in a work-group; wpr = 1: 2^lg lanes per row
   const void* dy;
   const void* x;
   const float* w;
@@ -171,15 +171,17 @@ struct NormBwdArgs {
 // weights stay there too, and the next row's loads are issued before this one
 // is reduced; rows of two (d > 8192) have no registers for either.  MULTI (rows
 // of at most 4 waves): the work-group's 8 waves take several rows at once, side
-// by side, and join their sums in LDS, so that the parts stay one per work-group.
+// by side (several in a wave where they fit), and join their sums in registers and
+// LDS, so that the parts stay one per work-group.
 constexpr int kMultiWaves = 8;
 template <typename TD, typename TX, typename TO, bool DS, int N, bool MULTI, bool STREAM>
 __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBwdArgs p) {
   __shared__ float s_red[2][2][kMaxWaves];
-  __shared__ float s_part[MULTI ? kMultiWaves * kWave * 8 : 1];
+  __shared__ float s_part[MULTI ? 2 : 1][MULTI ? kMultiWaves * kWave * 8 : 1];
   const int wave = threadIdx.x >> 6, waves = MULTI ? p.wpr : blockDim.x >> 6;
-  const int slot = MULTI ? wave / waves : 0;  // the row's place in the work-group
-  const int width = waves * kWave;
+  const bool packed = MULTI && waves == 1;    // rows side by side also within a wave
+  const int slot = packed ? threadIdx.x >> p.lg : MULTI ? wave / waves : 0;  // the row's place in the work-group
+  const int width = packed ? 1 << p.lg : waves * kWave;
   const int tid = threadIdx.x - slot * width;  // thread within the row
   if (threadIdx.x < 4 * kMaxWaves) (&s_red[0][0][0])[threadIdx.x] = 0.0f;
   __syncthreads();
@@ -251,8 +253,13 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
     if constexpr (kAhead) {
       if (row + step < p.rows) load(row + step);
     }
-    c1 = wave_sum(c1);
-    c2 = wave_sum(c2);
+    if (packed) {
+      c1 = group_sum(c1, width);
+      c2 = group_sum(c2, width);
+    } else {
+      c1 = wave_sum(c1);
+      c2 = wave_sum(c2);
+    }
     if (waves > 1) {
       if ((tid & 63) == 0) {
         s_red[buf][0][wave] = c1;
@@ -281,18 +288,31 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_kernel(const NormBw
   }
   float* part = p.part + (int64_t)blockIdx.x * 2 * p.d;
   if constexpr (MULTI) {
+    const int at = packed ? wave : slot, n = kMultiWaves / waves;
+    for (int o = width; o < kWave; o <<= 1) {  // the rows of a wave
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (owns(q[0], j)) s_part[slot * p.d + q[0].c + j] = h == 0 ? dw[0][j] : db[0][j];
-      __syncthreads();
-      for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
-        float v = s_part[c];
-        for (int k = 1; k < p.rpb; ++k) v += s_part[k * p.d + c];
-        part[h * p.d + c] = v;
+      for (int j = 0; j < 8; ++j) {
+        dw[0][j] += __shfl_xor(dw[0][j], o, kWave);
+        db[0][j] += __shfl_xor(db[0][j], o, kWave);
       }
-      __syncthreads();
+    }
+    if (!packed || (threadIdx.x & 63) < width) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!owns(q[0], j)) continue;
+        s_part[0][at * p.d + q[0].c + j] = dw[0][j];
+        s_part[1][at * p.d + q[0].c + j] = db[0][j];
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.d; c += blockDim.x) {
+      const int h = c >= p.d ? 1 : 0;
+      float t[kMultiWaves], v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMultiWaves; ++k) t[k] = s_part[h][min(k, n - 1) * p.d + c - h * p.d];
+#pragma unroll
+      for (int k = 0; k < kMultiWaves; ++k) v += k < n ? t[k] : 0.0f;
+      part[c] = v;
     }
     return;
   }
@@ -462,10 +482,19 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void norm_bwd_split_kernel(const 
   }
 }
 
+// Lanes of a row that fits a wave: a power of two of them that covers its pieces,
+// rows side by side in the wave (500000 x 128 bf16: forward 49 us against 106 with
+// a wave per row, backward 79 against 153; 16384 x 128 4.2 against 7.7).
+int row_lanes_log(int pieces) {
+  int lg = 0;
+  while (lg < 6 && (1 << lg) < pieces) ++lg;
+  return lg;
+}
+
 // launch shape of the backward: pieces of 8 a lane holds, waves of a row, rows
 // at once in a work-group, work-groups (= parts of the parameter gradients)
 struct BwdShape {
-  int n, waves, rpb;
+  int n, waves, rpb, lg;
   int64_t groups;
   bool split;  // the one-launch form, which has no parts
 };
@@ -473,8 +502,9 @@ struct BwdShape {
 // 128 registers (16384 x 7168: 206 us against 400).  Rows of up to 4 waves go
 // side by side in work-groups of 8 (16384 x 1024 bf16: 28 us against 35).  One
 // work-group per CU keeps the parts few (16384 x 7168: 206 + 5 us, 223 + 9 with
-// two; 65536 x 2048 fp32: 293 against 337); rows of one wave take two (16000 x
-// 257: 14.2 against 15.0).
+// two; 65536 x 2048 fp32: 293 against 337); rows of at most one wave take two
+// where there are many (16000 x 257: 14.2 against 15.0; 250000 x 256 75.7 against
+// 79.6, but 16384 x 256 13.9 against 12.7).
 // The one-launch form: up to 384 rows (64 x 7168: 3.3 us against 8.1; 400 x 1024:
 // 7.0 against 8.2, 400 x 200: 6.8 against 6.4), and rows of four pieces a lane,
 // where dw and db would spill (2000 x 20000 fp32: 157 us against 238).
@@ -484,9 +514,10 @@ BwdShape bwd_shape(int64_t rows, int d) {
   int n = 1;
   while (pieces > n * kWave * kMaxWaves) n *= 2;
   const int waves = (pieces + n * kWave - 1) / (n * kWave);
-  const int rpb = waves <= kMultiWaves / 2 ? kMultiWaves / waves : 1;
-  const int64_t need = (rows + rpb - 1) / rpb, fill = waves == 1 ? 512 : 256;
-  return {n, waves, rpb, need < fill ? need : fill, rows > 0 && (rows <= kFewRows || n > 2)};
+  const int lg = row_lanes_log(pieces);
+  const int rpb = waves == 1 ? kMultiWaves * kWave >> lg : waves <= kMultiWaves / 2 ? kMultiWaves / waves : 1;
+  const int64_t need = (rows + rpb - 1) / rpb, fill = waves == 1 && need > 4 * 256 ? 512 : 256;
+  return {n, waves, rpb, lg, need < fill ? need : fill, rows > 0 && (rows <= kFewRows || n > 2)};
 }
 
 template <typename TD, typename TX, typename TO, bool DS>
@@ -500,7 +531,7 @@ hipError_t bwd_n(const NormBwdArgs& a, const BwdShape& b, float* dw, float* db, 
     else hipLaunchKernelGGL((norm_bwd_split_kernel<TD, TX, TO, DS, 4>), all, wide, 0, s, a, rows, dw, db);
     return hipGetLastError();
   }
-  const dim3 grid(static_cast<unsigned>(b.groups)), block(b.waves * b.rpb * kWave);
+  const dim3 grid(static_cast<unsigned>(b.groups)), block((b.rpb > 1 ? kMultiWaves / b.waves : 1) * b.waves * kWave);
   const bool st = streams(static_cast<double>(a.rows) * a.d * (sizeof(TD) + sizeof(TX) * (DS ? 2 : 1) + sizeof(TO)));
   if (b.rpb > 1) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, true, false>), grid, block, 0, s, a);
   else if (b.n == 1 && st) hipLaunchKernelGGL((norm_bwd_kernel<TD, TX, TO, DS, 1, false, true>), grid, block, 0, s, a);
@@ -524,20 +555,21 @@ hipError_t launch_layer_norm(int64_t rows, int d, const void* x, const void* r, 
   const int pieces = (d + 7) / 8;
   int n = d <= 2048 ? 1 : 2;
   while (pieces > n * kWave * kMaxWaves) n *= 2;
-  const int waves = (pieces + n * kWave - 1) / (n * kWave), rpb = waves == 1 ? 4 : 1;
+  const int waves = (pieces + n * kWave - 1) / (n * kWave), lg = row_lanes_log(pieces);
+  const int wg_waves = waves == 1 ? 4 : waves, rpb = waves == 1 ? wg_waves * kWave >> lg : 1;
   // Work-groups: all at once while the chip holds them; else about 24 KB of
   // loads per CU in flight (more only lengthens the queues: 16384 x 7168 bf16
   // 164 us with 256 work-groups, 180 with 512), in passes of equal length.
   const int64_t need = (rows + rpb - 1) / rpb;
   int64_t groups = need;
-  if (need * waves * rpb > 256 * 16) {
+  if (need * wg_waves > 256 * 16) {
     const int64_t bytes = (int64_t)rpb * d * (x_dtype == MOE_BF16 ? 2 : 4) * (r != nullptr ? 2 : 1);
     const int64_t most = 256 * std::max<int64_t>(1, (24576 + bytes / 2) / bytes);
     const int64_t passes = (need + most - 1) / most;
     groups = (need + passes - 1) / passes;
   }
-  const NormArgs a{rows, d, waves, rpb, x, r, w, b, eps, sum, y, mean, rstd};
-  const dim3 grid(static_cast<unsigned>(groups)), block(waves * rpb * kWave);
+  const NormArgs a{rows, d, waves, rpb, lg, x, r, w, b, eps, sum, y, mean, rstd};
+  const dim3 grid(static_cast<unsigned>(groups)), block(wg_waves * kWave);
   const bool xb = x_dtype == MOE_BF16, yb = y_dtype == MOE_BF16;
   if (r != nullptr) {
     if (xb) return yb ? fwd_n<uint16_t, uint16_t, true>(a, n, grid, block, s)
@@ -561,7 +593,7 @@ hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dty
                                  int dx_dtype, float* dw, float* db, float* ws, hipStream_t s) {
   const BwdShape b = bwd_shape(rows, d);
   if (b.groups > 0) {
-    const NormBwdArgs a{rows, d, b.waves, b.rpb, dy, x, w, mean, rstd, ds, dx, ws};
+    const NormBwdArgs a{rows, d, b.waves, b.rpb, b.lg, dy, x, w, mean, rstd, ds, dx, ws};
     const int key = (dy_dtype == MOE_BF16) | (x_dtype == MOE_BF16) << 1 | (dx_dtype == MOE_BF16) << 2;
     hipError_t e = hipSuccess;
     using B = uint16_t;

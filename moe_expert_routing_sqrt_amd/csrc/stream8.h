@@ -1,6 +1,6 @@
 // Rows of bf16 or fp32 in pieces of 8 elements, at any element alignment, and
 // wave sums in a fixed order: what the row-streaming kernels (layer norm,
-// optimizer) share.
+// optimizer, balance loss) share.
 #pragma once
 
 #include "common.h"
@@ -158,6 +158,18 @@ __device__ __forceinline__ float wave_sum(float v) {
   v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
   const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// the same over aligned groups of lpt lanes (a power of two); the lanes of a
+// group must be active, all 64 of them for lpt = 64
+__device__ __forceinline__ float group_sum(float v, int lpt) {
+  if (lpt == kWave) return wave_sum(v);
+  if (lpt >= 2) v += dpp_f32<0xB1>(v);
+  if (lpt >= 4) v += dpp_f32<0x4E>(v);
+  if (lpt >= 8) v += dpp_f32<0x141>(v);
+  if (lpt >= 16) v += dpp_f32<0x140>(v);
+  if (lpt >= 32) v += __shfl_xor(v, 16, kWave);
+  return v;
 }
 
 }  // namespace moe

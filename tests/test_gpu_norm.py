@@ -25,7 +25,9 @@ ROUND = {"f32": 2.0 ** -23, "bf16": 2.0 ** -8}
 
 SHAPES = [(1, 1), (1, 64), (3, 7), (2, 9), (5, 63), (7, 513), (4, 1000), (33, 1001), (9, 2048), (3, 4099),
           (5, 7168), (2, 16384), (2, 20011), (1, 32768), (1500, 40), (700, 1024), (2051, 264), (384, 333),
-          (385, 333), (1025, 2050), (600, 4097), (530, 9001)]
+          (385, 333), (1025, 2050), (600, 4097), (530, 9001),
+          # rows side by side in a wave
+          (1000, 64), (777, 128), (500, 5), (4097, 9), (3000, 33), (1234, 256), (100003, 17), (40007, 100)]
 
 
 def _rows(g, rows, d, dt, dev, offset=0.5, shift=0):
