@@ -51,18 +51,23 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     if sum_out is not None and residual is None:
         raise ValueError("sum_out needs a residual")
     r_p, w_p, b_p = _arg(residual, n, "residual", dt), _arg(weight, d, "weight", _f32), _arg(bias, d, "bias", _f32)
-    if y is None:
+    s_p, y_p = _arg(sum_out, n, "sum_out", dt), _arg(y, n, "y")
+    m_p, i_p = _arg(mean, rows, "mean", _f32), _arg(rstd, rows, "rstd", _f32)
+    if y is None:  # what is made here needs no check
         y = torch.empty_like(x) if y_dtype is None or y_dtype == dt else torch.empty_like(x, dtype=y_dtype)
+        y_p = y.data_ptr()
     if residual is not None and sum_out is None:
         sum_out = torch.empty_like(x)
+        s_p = sum_out.data_ptr()
     if keep_stats:
         if mean is None:
             mean = weight.new_empty(rows)
+            m_p = mean.data_ptr()
         if rstd is None:
             rstd = weight.new_empty(rows)
-    st = lib().moe_layer_norm(rows, d, _arg(x, n, "x"), r_p, _dt(x), w_p, b_p, eps,
-                              _arg(sum_out, n, "sum_out", dt), _arg(y, n, "y"), _dt(y),
-                              _arg(mean, rows, "mean", _f32), _arg(rstd, rows, "rstd", _f32), _stream())
+            i_p = rstd.data_ptr()
+    st = lib().moe_layer_norm(rows, d, _arg(x, n, "x"), r_p, _dt(x), w_p, b_p, eps, s_p, y_p, _dt(y), m_p, i_p,
+                              _stream())
     _lib.check("moe_layer_norm", st)
     return y, x if residual is None else sum_out, mean, rstd
 
@@ -80,20 +85,24 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     n = x.numel()
     rows = n // d if d else 0
     dt = x.dtype
+    w_p, x_p = _arg(weight, d, "weight", _f32), _arg(x, n, "x")
+    dx_p, dw_p, db_p = _arg(dx, n, "dx"), _arg(dw, d, "dw", _f32), _arg(db, d, "db", _f32)
     if dx is None:
         dx = torch.empty_like(x) if dx_dtype is None or dx_dtype == dt else torch.empty_like(x, dtype=dx_dtype)
+        dx_p = dx.data_ptr()
     if dw is None:
         dw = torch.empty_like(weight)
+        dw_p = dw.data_ptr()
     if db is None and has_bias:
         db = torch.empty_like(weight)
+        db_p = db.data_ptr()
     need = 0 if ws is not None else _norm_ws_floats(rows, d)
     if need:
         ws = weight.new_empty(need)
-    st = lib().moe_layer_norm_backward(rows, d, _arg(dy, n, "dy"), _dt(dy), _arg(x, n, "x"), _dt(x),
-                                       _arg(weight, d, "weight", _f32), _arg(mean, rows, "mean", _f32),
-                                       _arg(rstd, rows, "rstd", _f32), _arg(d_sum, n, "d_sum", dt),
-                                       _arg(dx, n, "dx"), _dt(dx), _arg(dw, d, "dw", _f32), _arg(db, d, "db", _f32),
-                                       _arg(ws, 0, "ws"), _ws_len(ws), _stream())
+    st = lib().moe_layer_norm_backward(rows, d, _arg(dy, n, "dy"), _dt(dy), x_p, _dt(x), w_p,
+                                       _arg(mean, rows, "mean", _f32), _arg(rstd, rows, "rstd", _f32),
+                                       _arg(d_sum, n, "d_sum", dt), dx_p, _dt(dx), dw_p, db_p, _arg(ws, 0, "ws"),
+                                       _ws_len(ws), _stream())
     _lib.check("moe_layer_norm_backward", st)
     return dx, dw, db
 
@@ -127,23 +136,28 @@ def balance_loss(sh: MoeShape, logits: torch.Tensor, idx: torch.Tensor, alpha: f
     if idx.dtype != _i32:
         raise TypeError("idx must be int32")
     n, off_p, mask_p = _sequences(T, seq_offsets, token_mask)
-    if loss is None:
+    m = n * E
+    l_p, i_p = _arg(logits, T * E, "logits", _f32), _arg(idx, T * k, "idx")
+    o_p = _arg(logit_offset, E, "logit_offset", _f32)
+    loss_p, c_p = _arg(loss, 1, "loss", _f32), _arg(counts, m, "counts", _i32)
+    p_p, d_p = _arg(prob, m, "prob", _f32), _arg(dprob, m, "dprob", _f32)
+    if loss is None:  # what is made here needs no check
         loss = logits.new_empty(1)
+        loss_p = loss.data_ptr()
     if counts is None:
         counts = idx.new_empty((n, E))
+        c_p = counts.data_ptr()
     if prob is None:
         prob = logits.new_empty((n, E))
+        p_p = prob.data_ptr()
     if dprob is None:
         dprob = torch.empty_like(prob)
+        d_p = dprob.data_ptr()
     need = 0 if ws is not None else _loss_ws_floats(T, E, k, n)
     if need:
         ws = logits.new_empty(need)
-    m = n * E
-    st = lib().moe_balance_loss(ctypes.byref(sh), _arg(logits, T * E, "logits", _f32),
-                                _arg(logit_offset, E, "logit_offset", _f32), _arg(idx, T * k, "idx"), off_p, n,
-                                mask_p, alpha, _arg(counts, m, "counts", _i32), _arg(prob, m, "prob", _f32),
-                                _arg(dprob, m, "dprob", _f32), _arg(loss, 1, "loss", _f32), _arg(ws, 0, "ws"),
-                                _ws_len(ws), _stream())
+    st = lib().moe_balance_loss(ctypes.byref(sh), l_p, o_p, i_p, off_p, n, mask_p, alpha, c_p, p_p, d_p, loss_p,
+                                _arg(ws, 0, "ws"), _ws_len(ws), _stream())
     _lib.check("moe_balance_loss", st)
     return loss, counts, prob, dprob
 
@@ -157,14 +171,15 @@ def balance_loss_backward(sh: MoeShape, logits: torch.Tensor, dprob: torch.Tenso
     ([1] fp32 on the device; None: 1).  dlogits may be d_extra."""
     T, E = sh.T, sh.E
     n, off_p, mask_p = _sequences(T, seq_offsets, token_mask)
+    m = T * E
+    out_p = _arg(dlogits, m, "dlogits", _f32)
     if dlogits is None:
         dlogits = logits.new_empty((T, E))
-    m = T * E
+        out_p = dlogits.data_ptr()
     st = lib().moe_balance_loss_backward(ctypes.byref(sh), _arg(logits, m, "logits", _f32),
                                          _arg(logit_offset, E, "logit_offset", _f32), off_p, n, mask_p,
                                          _arg(dprob, n * E, "dprob", _f32), _arg(grad_loss, 1, "grad_loss", _f32),
-                                         _arg(d_extra, m, "d_extra", _f32), _arg(dlogits, m, "dlogits", _f32),
-                                         _stream())
+                                         _arg(d_extra, m, "d_extra", _f32), out_p, _stream())
     _lib.check("moe_balance_loss_backward", st)
     return dlogits
 
