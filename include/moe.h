@@ -501,7 +501,8 @@ int moe_bias_update(int64_t n_rows, int32_t E, const int32_t* counts, float gamm
  * moe_balance_loss - the router's balance loss and the per-expert counts, for
  * n_seq sequences packed along the tokens.  With p[t,e] = a[t,e] / sum_e
  * a[t,e], a = sqrt(softplus(logits + logit_offset)) (0 for a row whose
- * affinities all vanish), and for sequence s its T_s counted tokens:
+ * affinities all vanish, NaN for a row with a NaN), and for sequence s its T_s
+ * counted tokens:
  *     counts[s,e] = slots (t, j) of counted tokens with topk_idx[t,j] = e
  *     f[s,e] = E counts[s,e] / (k T_s),   prob[s,e] = sum_t p[t,e] / T_s
  *     loss = alpha / n_seq * sum_s sum_e f[s,e] prob[s,e]

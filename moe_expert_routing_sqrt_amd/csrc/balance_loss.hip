@@ -15,7 +15,8 @@
 //   a = sqrt(l + u q) for l >= 0 and h sqrt(q) for l < 0:
 // no cancellation, and no underflow before e^(l/2) itself.  Two
 // transcendental instructions and 16 others an element.
-// A row whose affinities all vanish has no probabilities: it adds 0.
+// A row whose affinities all vanish has no probabilities: it adds 0.  A counted
+// row with a NaN has NaN for each, in the sums and in its gradient.
 //
 // At T = 16384, E = 256, k = 8 (17 MB, 2.9 us of HBM) the forward takes 7.4 us for
 // the parts, 1.9 of them transcendentals and polynomial, and 4.7 us for the sums,
@@ -61,6 +62,10 @@ __device__ __forceinline__ Affinity affinity(float l) {
   r.da = GRAD ? 0.5f * c * __builtin_amdgcn_rcpf(__builtin_fmaf(u, t, t)) : 0.0f;
   return r;
 }
+
+// Whether a row's affinities, whose sum this is, make probabilities: not where
+// all vanish.  A sum that is no number does, and makes the row's NaN.
+__device__ __forceinline__ bool has_share(float total) { return total != 0.0f; }
 
 // The sequence of a lane's token t among the offsets (nullptr: one sequence of
 // all T tokens); -1 for a token outside them.  Tokens must not fall from lane to
@@ -224,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(const LossArgs p
         total += pr[v][r][j];
       }
     total = group_sum(total, m.lpt);
-    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    const float inv = has_share(total) ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -326,7 +331,7 @@ __device__ __forceinline__ void tile_probabilities(const RowMap<1, FULL>& m, int
       total += pr[v][0][j];
     }
     total = group_sum(total, m.lpt);
-    const bool some = i < ntok && ((counted >> (i & 63)) & 1) != 0 && total > 0.0f;
+    const bool some = i < ntok && ((counted >> (i & 63)) & 1) != 0 && has_share(total);
     const float inv = some ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) pr[v][0][j] = some ? pr[v][0][j] * inv : 0.0f;
@@ -644,7 +649,7 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(const GradAr
     }
   total = group_sum(total, m.lpt);
   dot = group_sum(dot, m.lpt);
-  const bool some = s >= 0 && total > 0.0f;
+  const bool some = s >= 0 && has_share(total);
   const float inv = some ? 1.0f / total : 0.0f;
   const float mean = dot * inv, scale = g * inv;
 #pragma unroll

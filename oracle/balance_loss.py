@@ -42,7 +42,7 @@ def forward(logits, idx, alpha, offsets=None, mask=None):
             continue
         for t in tokens:
             a = affinity(logits[t])
-            if a.sum() > 0:
+            if a.sum() != 0:  # NaN too: such a row has probabilities, and they are NaN
                 prob[s] += a / a.sum()
             for e in idx[t]:
                 if 0 <= e < E:
@@ -72,5 +72,5 @@ def backward(logits, dprob, offsets=None, mask=None, grad_loss=1.0, d_extra=None
             da = grad_loss * (dprob[s] - (dprob[s] * a).sum() / S) / S
             with np.errstate(over="ignore"):
                 sig = np.where(l >= 0, 1.0 / (1.0 + np.exp(-np.abs(l))), np.exp(-np.abs(l)) / (1.0 + np.exp(-np.abs(l))))
-            out[t] += np.where(a > 0, da * sig / (2.0 * np.where(a > 0, a, 1.0)), 0.0)
+            out[t] += np.where(a != 0, da * sig / (2.0 * np.where(a != 0, a, 1.0)), 0.0)
     return out
