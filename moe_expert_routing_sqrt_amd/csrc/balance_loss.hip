@@ -13,8 +13,11 @@
 //   log1p(u) = u q(u),  q the degree-8 interpolant of log1p(u)/u at the nine
 //   Chebyshev nodes of [0, 1] (relative error 3.4e-8),
 //   a = sqrt(l + u q) for l >= 0 and h sqrt(q) for l < 0:
-// no cancellation, and no underflow before e^(l/2) itself.  Two
-// transcendental instructions and 16 others an element.
+// no cancellation, and no underflow before e^(l/2) itself, at a logit of -174.
+// Rounding the exponent once would cost h |l| 2^-24 of itself (rms error of a
+// probability at logits near -165 8e-7); its low part is carried, and an
+// affinity holds 7 2^-24 at any logit.  Two transcendental instructions and 22
+// others an element.
 // A row whose affinities all vanish has no probabilities: it adds 0.  A counted
 // row with a NaN has NaN for each, in the sums and in its gradient.
 //
@@ -42,7 +45,13 @@ struct Affinity {
 
 template <bool GRAD>
 __device__ __forceinline__ Affinity affinity(float l) {
-  const float h = __builtin_amdgcn_exp2f(__builtin_fabsf(l) * -0.72134752f);  // -log2(e)/2
+  // h = 2^e with e = -|l| log2(e)/2, the part of e past 24 bits as a factor
+  // 1 + ln2 lo.  The bound on |l| keeps lo finite; h is 0 long before it.
+  const float x = __builtin_fminf(__builtin_fabsf(l), 512.0f);
+  const float e = x * -0x1.715476p-1f;
+  const float lo = __builtin_fmaf(x, -0x1.4ae0c0p-27f, __builtin_fmaf(x, -0x1.715476p-1f, -e));
+  const float h2 = __builtin_amdgcn_exp2f(e);
+  const float h = __builtin_fmaf(h2, lo * 0x1.62e430p-1f, h2);
   const float u = h * h;
   float q = 0x1.4ff1bap-8f;
   q = __builtin_fmaf(q, u, -0x1.dc5978p-6f);
