@@ -188,8 +188,15 @@ struct LossArgs {
   float* psum;    // [tiles + n_seq][E]
   int32_t* pcnt;  // [tiles + n_seq][E]
   int32_t* ptok;  // [tiles + n_seq]
-  unsigned long long* total;  // of the sums that follow: reset here
+  unsigned long long* total;  // of the sums that follow, and their `groups` slots for
+  float* left;                // shares: reset here
+  int groups;
 };
+
+__device__ __forceinline__ void reset_shares(const LossArgs& p) {
+  if (threadIdx.x == 0) *p.total = 0;
+  for (int i = threadIdx.x; i < p.groups; i += kThreads) p.left[i] = 0.0f;
+}
 
 // One work-group per tile of 64 tokens: their probabilities are formed once, in
 // registers.  Lane i of every wave knows token i's sequence, so that a
@@ -223,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(const LossArgs p
   const int my_e = my_tok < ntok ? p.idx[t0 * p.k + tid] : -1;
   const bool on = lane < ntok && (p.mask == nullptr || p.mask[t0 + lane] != 0);
   const int seq = sequence_of(t0 + lane);
-  if (blockIdx.x == 0 && tid == 0) *p.total = 0;
+  if (blockIdx.x == 0) reset_shares(p);
   for (int e = tid; e < E; e += kThreads) s_cnt[e] = 0;
 #pragma unroll
   for (int v = 0; v < U; ++v) {
@@ -384,7 +391,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_short_kernel(const Loss
   const int my_e = my_tok < ntok ? p.idx[t0 * p.k + tid] : -1;
   const bool on = lane < ntok && (p.mask == nullptr || p.mask[t0 + lane] != 0);
   const int seq = sequence_of(t0 + lane);
-  if (blockIdx.x == 0 && tid == 0) *p.total = 0;
+  if (blockIdx.x == 0) reset_shares(p);
   const Runs runs(seq, on);
   if (wave == 0 && runs.starts_here()) {
     const int end = runs.end(ntok);
@@ -501,23 +508,23 @@ struct SumArgs {
   int32_t* counts;
   float* prob;
   float* dprob;
+  float one;  // 1 in units of the total
   unsigned long long* total;
+  float* left;  // [gridDim.x * gridDim.y]
   float* loss;
 };
 
-// The work-groups' shares of the loss meet in one 64-bit integer, so their sum
-// does not depend on their order and the last one to come has it without
-// another round trip: finished work-groups (11 bits, at most 32 x 32), those
-// whose share is not a number in range (11 bits), and the sum of share / n_seq
-// (at most E <= 1024; 31 bits of fraction).
-constexpr int kShareBits = 42, kBadShift = 42, kDoneShift = 53;
-constexpr double kShareOne = 2147483648.0;
-__device__ __forceinline__ unsigned long long pack_share(float share) {
-  const bool ok = share >= 0.0f && share <= 1025.0f;
-  const unsigned long long v =
-      ok ? static_cast<unsigned long long>(static_cast<double>(share) * kShareOne + 0.5) : 1ull << kBadShift;
-  return v + (1ull << kDoneShift);
-}
+// The work-groups' shares of loss / alpha meet in one 64-bit integer, so their
+// sum does not depend on their order and the last one to come has it without
+// another round trip: finished work-groups (11 bits, at most 32 x 32), those that
+// left their share in memory instead (11 bits), and the sum of the others in
+// units of 1 / one = 2^(ceil(log2 E) - 41).  The shares add up to E at most, and
+// one of at least 2^23 units is a whole number of them: nothing is rounded.
+// Smaller ones (a loss far below 1) and those that are no number are left in
+// fp32, and the last work-group adds them in the order of the work-groups; that
+// takes a release at each and an acquire (16384 x 256, four sequences: 1.1 us).
+constexpr int kShareBits = 42, kLeftShift = 42, kDoneShift = 53;
+constexpr float kWhole = 0x1p23f, kMostUnits = 0x1.01p41f;
 
 // Work-group (x, y): slice y of W = 2^log_w experts.  Its waves form teams of
 // `team` waves (enough for about 16 parts a thread of a sequence of average
@@ -597,18 +604,44 @@ __global__ __launch_bounds__(kThreads) void balance_sum_kernel(const SumArgs p) 
   loss = wave_sum(loss);  // 0 in a team's other waves
   if ((tid & 63) == 0) s_loss[wave] = loss;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    loss = s_loss[0];
-    for (int i = 1; i < waves; ++i) loss += s_loss[i];
-    const unsigned long long mine = pack_share(loss / static_cast<float>(p.n_seq));
-    const unsigned long long all =
-        __hip_atomic_fetch_add(p.total, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + mine;
-    if ((all >> kDoneShift) == gridDim.x * gridDim.y) {
-      const bool bad = ((all >> kBadShift) & ((1u << (kDoneShift - kBadShift)) - 1)) != 0;
-      const double sum = static_cast<double>(all & ((1ull << kShareBits) - 1)) / kShareOne;
-      *p.loss = bad ? __builtin_nanf("") : static_cast<float>(sum * static_cast<double>(p.alpha));
+  if (wave != 0) return;
+  const int lane = threadIdx.x & 63, groups = gridDim.x * gridDim.y;
+  loss = row16_sum((lane & 15) < waves ? s_loss[lane & 15] : 0.0f) / static_cast<float>(p.n_seq);
+  if (groups > 1) {
+    const float units = loss * p.one;  // exact: a power of two
+    const bool whole = units == 0.0f || (units >= kWhole && units <= kMostUnits);
+    const unsigned long long mine =
+        (1ull << kDoneShift) + (whole ? static_cast<unsigned long long>(units) : 1ull << kLeftShift);
+    unsigned long long all = 0;
+    if (lane == 0) {
+      if (whole) {
+        all = __hip_atomic_fetch_add(p.total, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + mine;
+      } else {
+        __hip_atomic_store(p.left + blockIdx.y * gridDim.x + blockIdx.x, loss, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+        all = __hip_atomic_fetch_add(p.total, mine, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT) + mine;
+      }
+    }
+    all = (static_cast<unsigned long long>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(all >> 32))) << 32) |
+          static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(all)));
+    if (static_cast<int>(all >> kDoneShift) != groups) return;
+    loss = static_cast<float>(static_cast<double>(all & ((1ull << kShareBits) - 1)) / static_cast<double>(p.one));
+    if (((all >> kLeftShift) & ((1u << (kDoneShift - kLeftShift)) - 1)) != 0) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      float v = 0.0f;
+      for (int i = lane; i < groups; i += 4 * kWave) {  // 4 loads in flight
+        float t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          t[j] = __hip_atomic_load(p.left + min(i + j * kWave, groups - 1), __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v += i + j * kWave < groups ? t[j] : 0.0f;
+      }
+      loss += wave_sum(v);
     }
   }
+  if (lane == 0) *p.loss = loss * p.alpha;
 }
 
 // ---------------------------------------------------------------- gradient
@@ -682,15 +715,16 @@ bool full_rows(int E) {
   return E == lane4 || E == 512 || E == 1024;
 }
 
-// expert columns of a slice: 2^log_w
+// expert columns of a slice: 2^log_w, at most kSlice
+constexpr int kSlice = 32;
 int slice_log(int E) {
   int lg = 0;
-  while (lg < 5 && (1 << lg) < E) ++lg;
+  while ((1 << lg) < kSlice && (1 << lg) < E) ++lg;
   return lg;
 }
 
 struct LossWs {
-  size_t psum, pcnt, ptok, share, total;
+  size_t psum, pcnt, ptok, sum, left, total;
 };
 LossWs loss_ws(int64_t T, int E, int n_seq) {
   const size_t rows = static_cast<size_t>((T + kTile - 1) / kTile) + n_seq;
@@ -699,8 +733,9 @@ LossWs loss_ws(int64_t T, int E, int n_seq) {
   w.psum = 0;
   w.pcnt = up(rows * E * sizeof(float));
   w.ptok = w.pcnt + up(rows * E * sizeof(int32_t));
-  w.share = w.ptok + up(rows * sizeof(int32_t));
-  w.total = w.share + 256;
+  w.sum = w.ptok + up(rows * sizeof(int32_t));
+  w.left = w.sum + 256;
+  w.total = w.left + up(kSumGroups * (kMaxExperts / kSlice) * sizeof(float));
   return w;
 }
 
@@ -723,7 +758,7 @@ hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, con
                                float* prob, float* dprob, float* loss, void* ws, hipStream_t s) {
   if (small_loss(T, E, n_seq)) {
     const SmallArgs a{{T, E, lanes_log(E), k, n_seq, logits, offset, idx, seq, mask, nullptr, nullptr, nullptr,
-                       nullptr},
+                       nullptr, nullptr, 0},
                       alpha, counts, prob, dprob, loss};
     if (full_rows(E)) hipLaunchKernelGGL(balance_small_kernel<true>, dim3(1), dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL(balance_small_kernel<false>, dim3(1), dim3(kThreads), 0, s, a);
@@ -734,10 +769,21 @@ hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, con
   float* psum = reinterpret_cast<float*>(base + w.psum);
   int32_t* pcnt = reinterpret_cast<int32_t*>(base + w.pcnt);
   int32_t* ptok = reinterpret_cast<int32_t*>(base + w.ptok);
-  auto* total = reinterpret_cast<unsigned long long*>(base + w.share);
-  // at least one work-group: it resets the total
+  auto* total = reinterpret_cast<unsigned long long*>(base + w.sum);
+  float* left = reinterpret_cast<float*>(base + w.left);
+  // at least one work-group: it resets what the shares of the loss meet in
   const int64_t tiles = T > 0 ? (T + kTile - 1) / kTile : 1;
-  const LossArgs a{T, E, lanes_log(E), k, n_seq, logits, offset, idx, seq, mask, psum, pcnt, ptok, total};
+  const int lg = slice_log(E);
+  int team = 1;
+  while (team < kWaves && ((team * kWave) >> lg) * 16 < tiles / n_seq) team *= 2;
+  // one team a work-group while all sequences then run at once (a small
+  // work-group starts sooner: 12.4 us against 14.1 at T = 16384, E = 256, four
+  // sequences), else 16 waves of them
+  const int teams = n_seq <= kSumGroups ? 1 : kWaves / team;
+  const int groups = (n_seq + teams - 1) / teams;
+  const dim3 sums(groups < kSumGroups ? groups : kSumGroups, (E + (1 << lg) - 1) >> lg);
+  const LossArgs a{T, E, lanes_log(E), k, n_seq, logits, offset, idx, seq, mask, psum, pcnt, ptok, total, left,
+                   static_cast<int>(sums.x * sums.y)};
   const dim3 grid(static_cast<unsigned>(tiles)), block(kThreads);
   // sequences of under a tile's length on average: each costs the first form a
   // pass of its own (29 tokens in 49 sequences 40 us against 10.5; 16384 in 300,
@@ -755,16 +801,10 @@ hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, con
   else part(std::false_type{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int lg = slice_log(E);
-  int team = 1;
-  while (team < kWaves && ((team * kWave) >> lg) * 16 < tiles / n_seq) team *= 2;
-  const SumArgs b{T, E, k, n_seq, lg, team, alpha, seq, psum, pcnt, ptok, counts, prob, dprob, total, loss};
-  // one team a work-group while all sequences then run at once (a small
-  // work-group starts sooner: 12.4 us against 14.1 at T = 16384, E = 256, four
-  // sequences), else 16 waves of them
-  const int teams = n_seq <= kSumGroups ? 1 : kWaves / team;
-  const int groups = (n_seq + teams - 1) / teams;
-  const dim3 sums(groups < kSumGroups ? groups : kSumGroups, (E + (1 << lg) - 1) >> lg);
+  float one = 0x1p41f;
+  for (int e2 = 1; e2 < E; e2 *= 2) one *= 0.5f;
+  const SumArgs b{T,    E,   k,      n_seq, lg,    team, alpha, seq, psum, pcnt, ptok, counts,
+                  prob, dprob, one, total, left, loss};
   hipLaunchKernelGGL(balance_sum_kernel, sums, dim3(teams * team * kWave), 0, s, b);
   return hipGetLastError();
 }
