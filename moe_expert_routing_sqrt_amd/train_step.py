@@ -48,7 +48,9 @@ def main(argv=None) -> dict:
     delta, stream, target = new(), new(), new()
     seqs = torch.arange(a.sequences + 1, device=dev, dtype=torch.int32) * cfg.T // a.sequences
     seqs = seqs.to(torch.int32)
-    scale = torch.full((1,), 1.0 / cfg.T, device=dev)
+    # d_out is the gradient of T times the loss; the balance loss's carries T too
+    factor = torch.full((1,), float(cfg.T), device=dev)
+    scale = 1.0 / factor
     names = ("forward", "loss", "backward", "bias update", "optimizer")
     ev = [torch.cuda.Event(enable_timing=True) for _ in range(len(names) + 1)]
     times = dict.fromkeys(names, 0.0)
@@ -60,7 +62,7 @@ def main(argv=None) -> dict:
         diff = out - target
         err = diff.float().square().mean()
         ev[2].record()
-        blk.backward(diff)
+        blk.backward(diff, grad_loss=factor)
         ev[3].record()
         blk.layer.update_bias(1e-3)
         ev[4].record()

@@ -269,8 +269,8 @@ class MoEBlock:
 
     forward(delta, stream) returns (out, stream'): the next block adds them in
     its own norm, so no pass of its own is spent on the residual add.
-    backward(d_out, d_stream) leaves the gradients of every weight in the
-    block's buffers and returns the gradient of delta and stream.
+    backward(d_out, d_stream, grad_loss) leaves the gradients of every weight in
+    the block's buffers and returns the gradient of delta and stream.
     step() is the AdamW step on them."""
 
     def __init__(self, layer: MoELayer, norm_w: torch.Tensor, norm_b: torch.Tensor, eps: float = 1e-5,
@@ -311,10 +311,14 @@ class MoEBlock:
             la.sh, la.logits, la.idx, self.alpha, seq_offsets, token_mask, la.logit_offset, **self._loss_bufs[n])
         return out, self.stream
 
-    def backward(self, d_out: torch.Tensor, d_stream: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def backward(self, d_out: torch.Tensor, d_stream: Optional[torch.Tensor] = None,
+                 grad_loss: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """grad_loss ([1] fp32 on the device; None: 1): the gradient of the balance
+        loss, that is, the factor that d_out carries (a loss scale) and that
+        step()'s grad_scale takes off again."""
         la = self.layer
         dl = la._bwd_ws(d_out.device)["dlogits"]
-        balance_loss_backward(la.sh, la.logits, self.dprob, *self.seqs, la.logit_offset, dlogits=dl)
+        balance_loss_backward(la.sh, la.logits, self.dprob, *self.seqs, la.logit_offset, grad_loss, dlogits=dl)
         self.grads = la.backward(self.h, d_out, add_dlogits=True)
         layer_norm_backward(self.grads["dx"], self.stream, self.norm_w, self.mean, self.rstd, d_sum=d_stream,
                             dx=self.dx, dw=self.d_norm_w, db=self.d_norm_b, ws=self.norm_ws)
