@@ -271,7 +271,12 @@ class MoEBlock:
     its own norm, so no pass of its own is spent on the residual add.
     backward(d_out, d_stream, grad_loss) leaves the gradients of every weight in
     the block's buffers and returns the gradient of delta and stream.
-    step() is the AdamW step on them."""
+    step() is the AdamW step on them.
+
+    Whatever forward and backward leave or return (out, stream, loss, counts,
+    prob, dprob, grads and the input's gradient) are buffers of the block that
+    the next forward and backward write again: read or copy a value that is to
+    be kept (losses.append(float(blk.loss)), or blk.loss.clone())."""
 
     def __init__(self, layer: MoELayer, norm_w: torch.Tensor, norm_b: torch.Tensor, eps: float = 1e-5,
                  alpha: float = 1e-3, lr: float = 3e-4, betas: Tuple[float, float] = (0.9, 0.95),
@@ -292,7 +297,8 @@ class MoEBlock:
                                    device=dev)
         self.opt_args = dict(lr=lr, betas=betas, states=states, weight_decay=weight_decay)
         self.master, self.opt = master, None
-        # balance_loss's buffers by the number of sequences: what a captured graph writes stays where it is
+        # balance_loss's buffers by the number of sequences they hold, a power of two: what a captured graph
+        # writes stays where it is, and there are at most 17 sets of them
         self._loss_bufs = {}
 
     def forward(self, delta: torch.Tensor, stream: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
@@ -303,13 +309,23 @@ class MoEBlock:
         la = self.layer
         self.seqs = (seq_offsets, token_mask)
         n = 1 if seq_offsets is None else seq_offsets.numel() - 1
-        if n not in self._loss_bufs:
-            new = la.logits.new_empty
-            self._loss_bufs[n] = dict(loss=new(1), counts=new((n, la.E), dtype=_i32), prob=new((n, la.E)),
-                                      dprob=new((n, la.E)), ws=new(max(1, _loss_ws_floats(la.T, la.E, la.k, n))))
         self.loss, self.counts, self.prob, self.dprob = balance_loss(
-            la.sh, la.logits, la.idx, self.alpha, seq_offsets, token_mask, la.logit_offset, **self._loss_bufs[n])
+            la.sh, la.logits, la.idx, self.alpha, seq_offsets, token_mask, la.logit_offset, **self._loss_buffers(n))
         return out, self.stream
+
+    def _loss_buffers(self, n: int) -> dict:
+        if n > _lib.MOE_MAX_SEQUENCES:
+            return {}  # refused by the call
+        la, room = self.layer, min(1 << max(n - 1, 0).bit_length(), _lib.MOE_MAX_SEQUENCES)
+        if room not in self._loss_bufs:
+            new = la.logits.new_empty
+            self._loss_bufs[room] = dict(loss=new(1), counts=new((room, la.E), dtype=_i32), prob=new((room, la.E)),
+                                         dprob=new((room, la.E)),
+                                         ws=new(max(1, _loss_ws_floats(la.T, la.E, la.k, room))))
+        b = dict(self._loss_bufs[room])
+        for name in ("counts", "prob", "dprob"):
+            b[name] = b[name][:n]
+        return b
 
     def backward(self, d_out: torch.Tensor, d_stream: Optional[torch.Tensor] = None,
                  grad_loss: Optional[torch.Tensor] = None) -> torch.Tensor:
