@@ -303,6 +303,7 @@ class MoEBlock:
 
     def forward(self, delta: torch.Tensor, stream: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
                 token_mask: Optional[torch.Tensor] = None):
+        self._rows(delta=delta, stream=stream)
         layer_norm(delta, self.norm_w, self.norm_b, residual=stream, eps=self.eps, y=self.h, sum_out=self.stream,
                    mean=self.mean, rstd=self.rstd)
         out = self.layer.forward(self.h, save_for_backward=True)
@@ -312,6 +313,13 @@ class MoEBlock:
         self.loss, self.counts, self.prob, self.dprob = balance_loss(
             la.sh, la.logits, la.idx, self.alpha, seq_offsets, token_mask, la.logit_offset, **self._loss_buffers(n))
         return out, self.stream
+
+    def _rows(self, **tensors) -> None:
+        """Every tensor has the layer's T rows of d: of fewer, the others would keep
+        what an earlier call left in the block's buffers."""
+        for name, t in tensors.items():
+            if t is not None and t.numel() != self.layer.T * self.layer.d:
+                raise ValueError(f"{name}: needs {self.layer.T} rows of {self.layer.d}, has shape {tuple(t.shape)}")
 
     def _loss_buffers(self, n: int) -> dict:
         if n > _lib.MOE_MAX_SEQUENCES:
@@ -332,6 +340,7 @@ class MoEBlock:
         """grad_loss ([1] fp32 on the device; None: 1): the gradient of the balance
         loss, that is, the factor that d_out carries (a loss scale) and that
         step()'s grad_scale takes off again."""
+        self._rows(d_out=d_out, d_stream=d_stream)
         la = self.layer
         dl = la._bwd_ws(d_out.device)["dlogits"]
         balance_loss_backward(la.sh, la.logits, self.dprob, *self.seqs, la.logit_offset, grad_loss, dlogits=dl)
