@@ -508,7 +508,7 @@ int moe_bias_update(int64_t n_rows, int32_t E, const int32_t* counts, float gamm
  *     loss = alpha / n_seq * sum_s sum_e f[s,e] prob[s,e]
  *     dprob[s,e] = alpha f[s,e] / (n_seq T_s)  = d loss / d p[t,e] for t in s
  * A sequence without a counted token adds 0 (its rows are 0).
- *   shape        uses T, E, k (k <= E; E <= 1024, k <= 16, T < 2^26)
+ *   shape        uses T, E, k (k <= E; E <= 1024, k <= 16, T <= 2^26 - 4)
  *   logits       [T, E] fp32 as moe_route wrote them; logit_offset [E] or NULL
  *   topk_idx     [T, k] int32; an index outside [0, E) is not counted
  *   seq_offsets  [n_seq + 1] int32, non-decreasing: sequence s holds tokens

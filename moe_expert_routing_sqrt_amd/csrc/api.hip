@@ -576,7 +576,8 @@ static bool is_float(int t) { return t == MOE_F32 || t == MOE_BF16; }
 static int balance_check(const moe_shape* s, int32_t n_seq) {
   if (s == nullptr || s->T < 0 || s->E < 1 || s->k < 1 || s->k > s->E || n_seq < 1) return MOE_ERR_INVALID_ARG;
   if (s->E > kMaxExperts || s->k > 16 || n_seq > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
-  if (s->T >= int64_t{1} << 26) return MOE_ERR_UNSUPPORTED;  // 64 lanes a token in a launch of under 2^32 threads
+  // the gradient's launch: 256 threads for 4 tokens, under 2^32 threads in all
+  if (s->T > 4 * int64_t{UINT32_MAX / 256}) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
