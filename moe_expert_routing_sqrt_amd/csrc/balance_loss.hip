@@ -14,17 +14,18 @@
 //   Chebyshev nodes of [0, 1] (relative error 3.4e-8),
 //   a = sqrt(l + u q) for l >= 0 and h sqrt(q) for l < 0:
 // no cancellation, and no underflow before e^(l/2) itself, at a logit of -174.
-// Rounding the exponent once would cost h |l| 2^-24 of itself (rms error of a
-// probability at logits near -165 8e-7); its low part is carried, and an
-// affinity holds 7 2^-24 at any logit.  Two transcendental instructions and 22
-// others an element.
+// Rounding the exponent once would cost h |l| 2^-24 of itself (a probability's
+// rms error 1.5e-6 at logits near -165, 1.8e-7 near -12); its low part is carried,
+// and an affinity holds 7 2^-24 at any logit (rms 7e-8 everywhere).  Two
+// transcendental instructions and 22 others an element.
 // A row whose affinities all vanish has no probabilities: it adds 0.  A counted
 // row with a NaN has NaN for each, in the sums and in its gradient.
 //
-// At T = 16384, E = 256, k = 8 (17 MB, 2.9 us of HBM) the forward takes 7.4 us for
-// the parts, 1.9 of them transcendentals and polynomial, and 4.7 us for the sums,
-// a chain of dependent loads; the gradient onto others' (50 MB, 8.5 us) 10.3 us.
-// At most 64 tokens take one launch (T = 16, E = 64: 4.1 us; two took 7.6).
+// At T = 16384, E = 256, k = 8 (17 MB, 2.9 us of HBM) the forward takes 12.2 us:
+// parts whose work-groups load, compute (2.5 us), join and store one after the
+// other, two thirds of it, and sums, a chain of dependent loads; the gradient
+// onto others' (50 MB, 8.5 us) takes 10.5 us.  At most 64 tokens take one launch
+// (T = 16, E = 64: 4.1 us against 7.3 in two).
 #include <type_traits>
 
 #include "launch.h"
@@ -742,8 +743,8 @@ LossWs loss_ws(int64_t T, int E, int n_seq) {
 }  // namespace
 
 // One work-group for at most a tile, where its tables fit in LDS: T = 1, E = 256
-// 4.0 us against 7.5 in two launches, 16 x 64 4.1 against 7.6, 64 x 256 7.9 against
-// 9.7; a second tile on the same CU loses (128 x 16 7.8 against 7.6, 256 x 16 12.7
+// 4.1 us against 7.5 in two launches, 16 x 64 4.1 against 7.3, 64 x 256 8.3 against
+// 10.2; a second tile on the same CU loses (128 x 16 7.8 against 7.6, 256 x 16 12.7
 // against 7.9).
 static bool small_loss(int64_t T, int E, int n_seq) {
   return E <= 256 && T <= kTile && n_seq <= kSmallSeqs && static_cast<int64_t>(n_seq) * E <= kSmallTable;
@@ -777,7 +778,7 @@ hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, con
   int team = 1;
   while (team < kWaves && ((team * kWave) >> lg) * 16 < tiles / n_seq) team *= 2;
   // one team a work-group while all sequences then run at once (a small
-  // work-group starts sooner: 12.4 us against 14.1 at T = 16384, E = 256, four
+  // work-group starts sooner: 12.0 us against 12.6 at T = 16384, E = 256, four
   // sequences), else 16 waves of them
   const int teams = n_seq <= kSumGroups ? 1 : kWaves / team;
   const int groups = (n_seq + teams - 1) / teams;
@@ -786,9 +787,12 @@ hipError_t launch_balance_loss(int64_t T, int E, int k, const float* logits, con
                    static_cast<int>(sums.x * sums.y)};
   const dim3 grid(static_cast<unsigned>(tiles)), block(kThreads);
   // sequences of under a tile's length on average: each costs the first form a
-  // pass of its own (29 tokens in 49 sequences 40 us against 10.5; 16384 in 300,
-  // E = 100, 15.1 against 14.6), long ones the second its trip through LDS
-  // (16384 in 64, E = 256, 13.3 against 15.4; 65536 in 16 25.6 against 39.7)
+  // pass of its own (29 tokens in 49 sequences, were they no single launch, 40 us
+  // against 10.1; 16384 in 300, E = 100, 15.1 against 14.2), long ones the second
+  // its trip through LDS (16384 in 64, E = 256, 12.7 against 14.7; 65536 in 16 25.6
+  // against 40.7).  By the average alone: one long sequence among a thousand short
+  // or empty ones pays for it, here and in its team below (65536 tokens in one
+  // sequence 31 us, beside 1000 empty ones 59).
   const bool many = E <= 256 && T < static_cast<int64_t>(kTile) * n_seq;
   auto part = [&](auto full) {
     constexpr bool F = decltype(full)::value;

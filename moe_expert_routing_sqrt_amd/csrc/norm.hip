@@ -55,7 +55,8 @@ __device__ __forceinline__ float row_sum(float v, float* s_red, int wpr, int lg)
 
 // A work-group walks rows gridDim.x * rpb apart and issues the next row's loads
 // before it reduces this one's.  Its columns' weights stay in registers up to
-// N = 2; wider rows read them again from cache.
+// N = 2; wider rows (d > 16384) read them again from cache, and with a residual
+// they spill: 76 to 228 bytes a lane (fp32 to bf16 without one 20).
 template <typename TX, typename TY, bool RES, int N, bool STREAM>
 __global__ __launch_bounds__(kMaxWaves* kWave) void norm_fwd_kernel(const NormArgs p) {
   constexpr bool kKeep = N <= 2;
@@ -507,7 +508,9 @@ struct BwdShape {
 // 79.6, but 16384 x 256 13.9 against 12.7).
 // The one-launch form: up to 384 rows (64 x 7168: 3.3 us against 8.1; 400 x 1024:
 // 7.0 against 8.2, 400 x 200: 6.8 against 6.4), and rows of four pieces a lane,
-// where dw and db would spill (2000 x 20000 fp32: 157 us against 238).
+// whose dw and db alone would be 64 registers of 128 (2000 x 20000 fp32: 157 us
+// against 238 with parts).  With d_sum both forms spill beyond 8192 columns: rows
+// of two pieces 16 to 44 bytes a lane, of four 36 to 128.
 constexpr int kFewRows = 384;
 BwdShape bwd_shape(int64_t rows, int d) {
   const int pieces = (d + 7) / 8;
