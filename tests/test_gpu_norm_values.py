@@ -8,7 +8,6 @@ in a lane (the rows that its work-group's slot takes), joined over at most 8
 waves, 64 lanes and 512 parts by 16 waves: (rows / (groups * rows at once) + 96)
 eps sum|term|, with at least 256 work-groups (or one for every row) that take at
 least one row at once."""
-import numpy as np
 import pytest
 import torch
 
