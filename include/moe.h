@@ -17,7 +17,9 @@
  *   moe_combine     gate-weighted sum of expert rows back in token order
  *
  * and around it its backward and a training step's other operators: the norm
- * in front of the layer, a balance loss on the router, and the optimizer.
+ * in front of the layer, a balance loss on the router, and the optimizer; and
+ * the step's two ends on tokens: the embedding, and losses on a vocabulary's
+ * logits.
  *
  * Conventions for every call
  *   - Pointers are device pointers unless marked "host".  The caller owns and
@@ -632,6 +634,119 @@ typedef struct moe_adamw_params {
 } moe_adamw_params;
 int moe_adamw_step(int32_t n_tensors, const moe_adamw_tensor* tensors, const moe_adamw_params* params,
                    const float* grad_scale, moe_stream_t stream);
+
+/*
+ * ------------------------------------------------- tokens in, losses on logits
+ * The two ends of a training step on tokens: rows of a table by token id, and
+ * losses on the logits [T, V] of a vocabulary with their gradients.
+ * 1 <= V <= MOE_MAX_VOCAB, T < 2^26; any element alignment.
+ */
+#define MOE_MAX_VOCAB 16777216
+#define MOE_MAX_TEACHER_TOP 256
+
+/*
+ * moe_embedding - out[t] = scale * table[token_ids[t]], zeros for an id outside
+ * [0, V) (padding).  The product is formed in fp32 and rounded once.
+ *   token_ids [T] int32;  table [V, d] in table_dtype;  out [T, d] in out_dtype
+ *   (each MOE_BF16 or MOE_F32).  d >= 1.  T = 0 is a no-op.
+ */
+int moe_embedding(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* table, int table_dtype,
+                  float scale, void* out, int out_dtype, moe_stream_t stream);
+
+/*
+ * moe_embedding_backward - d_table[v] = scale * sum over t with token_ids[t] = v
+ * of d_out[t]; ids outside [0, V) have no gradient.
+ *   d_out    [T, d] in d_out_dtype
+ *   d_table  [V, d] in d_table_dtype.  accumulate = 0: written, zeros for rows
+ *            without a token (also with T = 0).  1: added to what is there (a
+ *            tied head's gradient, earlier micro-batches); only the rows of the
+ *            batch's ids are touched
+ *   ws       moe_embedding_backward_workspace_size(T, V, d) bytes; nothing in it
+ *            needs to start at zero
+ * The sums are fp32 over runs of the batch sorted by id, in token order
+ * (deterministic).
+ */
+size_t moe_embedding_backward_workspace_size(int64_t T, int64_t V, int32_t d);
+int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* d_out,
+                           int d_out_dtype, float scale, void* d_table, int d_table_dtype, int accumulate, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_distill_loss - distillation from a teacher's top logits.  With q =
+ * softmax(logits / temperature) over V and p = softmax(teacher / temperature)
+ * over the row's entries:
+ *     row_loss[t] = temperature^2 sum_j p_j (log p_j - log q[topk_idx_j])
+ *     loss = sum_t weight[t] row_loss[t]
+ *     dlogits[t,v] = grad_loss weight[t] temperature (q[v] - sum_{j: topk_idx_j = v} p_j)
+ *   logits    [T, V] in logits_dtype (MOE_BF16 or MOE_F32)
+ *   topk_idx  [T, K] int32, teacher [T, K] in teacher_dtype: an index outside
+ *             [0, V) or a teacher logit of -inf is no entry; an index may repeat.
+ *             1 <= K <= MOE_MAX_TEACHER_TOP
+ *   weight    [T] fp32, or NULL: 1/T each.  A row of weight 0, or without an
+ *             entry, does not count: its loss, statistics and gradient are 0 and
+ *             its logits may hold anything
+ *   grad_loss [1] fp32 device, or NULL: 1 (used with dlogits)
+ *   loss [1], row_loss [T] fp32 out
+ *   stats     [T, 2] fp32 out, for the backward: the row's largest logit m and
+ *             sum_v exp((logits - m) / temperature)
+ *   dlogits   [T, V] in dlogits_dtype out, or NULL: the loss alone.  May be
+ *             logits where the types agree.  One reading of the logits serves
+ *             both.
+ * A counted row with a NaN, a +inf or no finite logit gives NaN.  The sums run in
+ * a fixed order (deterministic), the softmax's in fp32, a row's loss and the sum
+ * over rows in fp64.  T = 0: loss = 0.
+ */
+int moe_distill_loss(int64_t T, int64_t V, int32_t K, const void* logits, int logits_dtype, const int32_t* topk_idx,
+                     const void* teacher, int teacher_dtype, double temperature, const float* weight,
+                     const float* grad_loss, float* loss, float* row_loss, float* stats, void* dlogits,
+                     int dlogits_dtype, moe_stream_t stream);
+
+/*
+ * moe_distill_loss_backward - dlogits alone, from the logits and the forward's
+ * stats.  dlogits must not be logits.
+ */
+int moe_distill_loss_backward(int64_t T, int64_t V, int32_t K, const void* logits, int logits_dtype,
+                              const float* stats, const int32_t* topk_idx, const void* teacher, int teacher_dtype,
+                              double temperature, const float* weight, const float* grad_loss, void* dlogits,
+                              int dlogits_dtype, moe_stream_t stream);
+
+/*
+ * moe_policy_loss - the clipped policy loss with a KL term, per token.  With
+ * logp = log softmax(logits / temperature)[token], r = exp(logp - old_logp),
+ * d = ref_logp - logp and A the advantage:
+ *     row_loss[t] = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(d) - d - 1)
+ *     loss = sum_t weight[t] row_loss[t]
+ *     dlogits[t,v] = grad_loss weight[t] / temperature dl/dlogp ([v = token] - softmax[v])
+ *     dl/dlogp = -r A (0 where the clamped term is the smaller) + kl (1 - exp(d))
+ *   logits    [T, V] in logits_dtype;  tokens [T] int32
+ *   old_logp, advantage [T] fp32;  ref_logp [T] fp32, or NULL with kl = 0
+ *   params    host: temperature > 0, clip_low, clip_high, kl >= 0, all finite
+ *   weight    [T] fp32, or NULL: 1/T each.  A row of weight 0, or with a token
+ *             outside [0, V), does not count: its loss, logp, statistics and
+ *             gradient are 0, and it may hold anything
+ *   logp      [T] fp32 out
+ *   the rest, and NaN, as moe_distill_loss
+ */
+typedef struct moe_policy_params {
+  double temperature, clip_low, clip_high, kl;
+} moe_policy_params;
+int moe_policy_loss(int64_t T, int64_t V, const void* logits, int logits_dtype, const int32_t* tokens,
+                    const float* old_logp, const float* advantage, const float* ref_logp,
+                    const moe_policy_params* params, const float* weight, const float* grad_loss, float* loss,
+                    float* row_loss, float* logp, float* stats, void* dlogits, int dlogits_dtype, moe_stream_t stream);
+/* moe_policy_loss_backward - as moe_distill_loss_backward */
+int moe_policy_loss_backward(int64_t T, int64_t V, const void* logits, int logits_dtype, const float* stats,
+                             const int32_t* tokens, const float* old_logp, const float* advantage,
+                             const float* ref_logp, const moe_policy_params* params, const float* weight,
+                             const float* grad_loss, void* dlogits, int dlogits_dtype, moe_stream_t stream);
+
+/*
+ * moe_token_logp - moe_policy_loss's logp and stats alone (what the policy that
+ * samples, or the reference policy, keeps of its tokens): 0 for a token outside
+ * [0, V).
+ */
+int moe_token_logp(int64_t T, int64_t V, const void* logits, int logits_dtype, const int32_t* tokens,
+                   double temperature, float* logp, float* stats, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,10 @@ library is missing, or a tensor is not on the GPU, calls raise.
     balance_loss(shape, logits, idx, alpha)  -> loss, counts, prob, dprob; balance_loss_backward -> dlogits
     AdamW                                    many tensors, 32-bit or 8-bit states; step() = one call
     MoEBlock                                 norm + MoELayer + balance loss + AdamW: a training step
+    embedding(ids, table, scale)             -> rows; embedding_backward -> the table's gradient
+    distill_loss(logits, idx, teacher)       -> loss, row_loss, stats, dlogits; distill_loss_backward -> dlogits
+    policy_loss(logits, tokens, old_logp, advantage) -> loss, row_loss, logp, stats, dlogits;
+                                             policy_loss_backward -> dlogits; token_logp -> logp, stats
 """
 from __future__ import annotations
 
@@ -39,7 +43,9 @@ __all__ = ["shape", "workspace_bytes", "workspace", "route", "route_hash", "disp
            "expert_ffn_train",
            "expert_ffn_backward", "dispatch_backward", "route_backward", "expert_ffn", "combine",
            "quantize_blocks_e4m3", "quantize_rows_e4m3", "bias_update", "MoELayer", "MoeError", "lib",
-           "layer_norm", "layer_norm_backward", "balance_loss", "balance_loss_backward", "AdamW", "MoEBlock"]
+           "layer_norm", "layer_norm_backward", "balance_loss", "balance_loss_backward", "AdamW", "MoEBlock",
+           "embedding", "embedding_backward", "distill_loss", "distill_loss_backward", "policy_loss",
+           "policy_loss_backward", "token_logp"]
 
 
 def lib():
@@ -508,3 +514,5 @@ def bias_update(counts: torch.Tensor, bias: torch.Tensor, gamma: float,
 from .layer import MoELayer  # noqa: E402
 from .training import (AdamW, MoEBlock, balance_loss, balance_loss_backward, layer_norm,  # noqa: E402
                        layer_norm_backward)
+from .tokens import (distill_loss, distill_loss_backward, embedding, embedding_backward, policy_loss,  # noqa: E402
+                     policy_loss_backward, token_logp)

@@ -27,6 +27,8 @@ MOE_OP_ROUTE, MOE_OP_DISPATCH, MOE_OP_EXPERT_FFN, MOE_OP_COMBINE = 1, 2, 3, 4
 MOE_OP_ROUTE_BACKWARD, MOE_OP_EXPERT_FFN_BACKWARD = 5, 6
 MOE_OP_LAYER_NORM_BACKWARD = 7
 MOE_MAX_SEQUENCES = 65535
+MOE_MAX_VOCAB = 1 << 24
+MOE_MAX_TEACHER_TOP = 256
 
 
 class MoeShape(ctypes.Structure):
@@ -57,6 +59,12 @@ class MoeAdamwParams(ctypes.Structure):
                 ("eps", ctypes.c_double), ("step", ctypes.c_int64)]
 
 
+class MoePolicyParams(ctypes.Structure):
+    """moe_policy_params: what a policy loss is computed with."""
+    _fields_ = [("temperature", ctypes.c_double), ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("kl", ctypes.c_double)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn, status, msg):
         super().__init__(f"{fn} failed: {msg} ({status})")
@@ -65,6 +73,7 @@ class MoeError(RuntimeError):
 
 _P = ctypes.c_void_p
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
@@ -103,6 +112,16 @@ SIGNATURES = {
     "moe_layer_norm_backward": (_INT, [_I64, _I32, _P, _INT, _P, _INT, _P, _P, _P, _P, _P, _INT, _P, _P, _P, _SZ,
                                        _P]),
     "moe_adamw_step": (_INT, [_I32, ctypes.POINTER(MoeAdamwTensor), ctypes.POINTER(MoeAdamwParams), _P, _P]),
+    "moe_embedding": (_INT, [_I64, _I64, _I32, _P, _P, _INT, _F32, _P, _INT, _P]),
+    "moe_embedding_backward_workspace_size": (_SZ, [_I64, _I64, _I32]),
+    "moe_embedding_backward": (_INT, [_I64, _I64, _I32, _P, _P, _INT, _F32, _P, _INT, _INT, _P, _SZ, _P]),
+    "moe_distill_loss": (_INT, [_I64, _I64, _I32, _P, _INT, _P, _P, _INT, _F64, _P, _P, _P, _P, _P, _P, _INT, _P]),
+    "moe_distill_loss_backward": (_INT, [_I64, _I64, _I32, _P, _INT, _P, _P, _P, _INT, _F64, _P, _P, _P, _INT, _P]),
+    "moe_policy_loss": (_INT, [_I64, _I64, _P, _INT, _P, _P, _P, _P, ctypes.POINTER(MoePolicyParams), _P, _P, _P, _P,
+                               _P, _P, _P, _INT, _P]),
+    "moe_policy_loss_backward": (_INT, [_I64, _I64, _P, _INT, _P, _P, _P, _P, _P, ctypes.POINTER(MoePolicyParams), _P,
+                                        _P, _P, _INT, _P]),
+    "moe_token_logp": (_INT, [_I64, _I64, _P, _INT, _P, _F64, _P, _P, _P]),
 }
 
 _lib = None

@@ -678,6 +678,149 @@ int moe_adamw_step(int32_t n_tensors, const moe_adamw_tensor* tensors, const moe
   return hip_status(launch_adamw(n_tensors, tensors, h, grad_scale, as_stream(stream)));
 }
 
+// T tokens and a vocabulary of V
+static int vocab_check(int64_t T, int64_t V) {
+  if (T < 0 || V < 1) return MOE_ERR_INVALID_ARG;
+  if (T >= (int64_t{1} << 26) || V > MOE_MAX_VOCAB) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int moe_embedding(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* table, int table_dtype,
+                  float scale, void* out, int out_dtype, moe_stream_t stream) {
+  if (!is_float(table_dtype) || !is_float(out_dtype) || !std::isfinite(scale) || d < 1) return MOE_ERR_INVALID_ARG;
+  const int st = vocab_check(T, V);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (token_ids == nullptr || table == nullptr || out == nullptr || out == table) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_embedding(T, static_cast<int>(V), d, token_ids, table, table_dtype, scale, out, out_dtype,
+                                     as_stream(stream)));
+}
+
+size_t moe_embedding_backward_workspace_size(int64_t T, int64_t V, int32_t d) {
+  if (vocab_check(T, V) != MOE_OK || d < 1) return 0;
+  return embedding_bwd_workspace_bytes(T, V, d);
+}
+
+int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* d_out,
+                           int d_out_dtype, float scale, void* d_table, int d_table_dtype, int accumulate, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  if (!is_float(d_out_dtype) || !is_float(d_table_dtype) || !std::isfinite(scale) || d < 1 ||
+      (accumulate != 0 && accumulate != 1))
+    return MOE_ERR_INVALID_ARG;
+  const int st = vocab_check(T, V);
+  if (st != MOE_OK) return st;
+  if (T > 0 && (token_ids == nullptr || d_out == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (d_table == nullptr || d_table == d_out) return MOE_ERR_INVALID_ARG;
+  if (ws == nullptr || ws_bytes < embedding_bwd_workspace_bytes(T, V, d) || !aligned256(ws)) return MOE_ERR_WORKSPACE;
+  return hip_status(launch_embedding_bwd(T, static_cast<int>(V), d, token_ids, d_out, d_out_dtype, scale, d_table,
+                                         d_table_dtype, accumulate != 0, ws, as_stream(stream)));
+}
+
+// a softmax temperature whose log2(e)/temperature fp32 holds
+static bool is_temperature(double t) {
+  return std::isfinite(t) && t > 0.0 && std::isnormal(static_cast<float>(1.4426950408889634 / t)) &&
+         std::isnormal(static_cast<float>(t));
+}
+
+// what the losses on logits share: types, sizes, logits and dlogits
+static int loss_check(int64_t T, int64_t V, const void* x, int x_dtype, const void* dx, int dx_dtype) {
+  if (!is_float(x_dtype) || (dx != nullptr && !is_float(dx_dtype))) return MOE_ERR_INVALID_ARG;
+  const int st = vocab_check(T, V);
+  if (st != MOE_OK) return st;
+  if (T > 0 && x == nullptr) return MOE_ERR_INVALID_ARG;
+  if (dx != nullptr && dx == x && dx_dtype != x_dtype) return MOE_ERR_INVALID_ARG;  // rows would overlap
+  return MOE_OK;
+}
+
+static int distill_check(int64_t T, int32_t K, const int32_t* idx, const void* teacher, int t_dtype, double tau) {
+  if (K < 1 || !is_float(t_dtype) || !is_temperature(tau)) return MOE_ERR_INVALID_ARG;
+  if (K > MOE_MAX_TEACHER_TOP) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (idx == nullptr || teacher == nullptr)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int moe_distill_loss(int64_t T, int64_t V, int32_t K, const void* logits, int logits_dtype, const int32_t* topk_idx,
+                     const void* teacher, int teacher_dtype, double temperature, const float* weight,
+                     const float* grad_loss, float* loss, float* row_loss, float* stats, void* dlogits,
+                     int dlogits_dtype, moe_stream_t stream) {
+  int st = loss_check(T, V, logits, logits_dtype, dlogits, dlogits_dtype);
+  if (st == MOE_OK) st = distill_check(T, K, topk_idx, teacher, teacher_dtype, temperature);
+  if (st != MOE_OK) return st;
+  if (loss == nullptr || (T > 0 && (row_loss == nullptr || stats == nullptr))) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_distill_loss(T, static_cast<int>(V), K, logits, logits_dtype, topk_idx, teacher,
+                                        teacher_dtype, temperature, weight, grad_loss, loss, row_loss, stats, dlogits,
+                                        dlogits_dtype, as_stream(stream)));
+}
+
+int moe_distill_loss_backward(int64_t T, int64_t V, int32_t K, const void* logits, int logits_dtype,
+                              const float* stats, const int32_t* topk_idx, const void* teacher, int teacher_dtype,
+                              double temperature, const float* weight, const float* grad_loss, void* dlogits,
+                              int dlogits_dtype, moe_stream_t stream) {
+  int st = loss_check(T, V, logits, logits_dtype, dlogits, dlogits_dtype);
+  if (st == MOE_OK) st = distill_check(T, K, topk_idx, teacher, teacher_dtype, temperature);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  // the row's entries are read while others' gradients are written
+  if (stats == nullptr || dlogits == nullptr || dlogits == logits) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_distill_loss_bwd(T, static_cast<int>(V), K, logits, logits_dtype, stats, topk_idx, teacher,
+                                            teacher_dtype, temperature, weight, grad_loss, dlogits, dlogits_dtype,
+                                            as_stream(stream)));
+}
+
+static int policy_check(int64_t T, const int32_t* tokens, const float* old_logp, const float* adv, const float* ref,
+                        const moe_policy_params* h) {
+  if (h == nullptr || !is_temperature(h->temperature) || !std::isfinite(h->clip_low) || h->clip_low < 0.0 ||
+      !std::isfinite(h->clip_high) || h->clip_high < 0.0 || !std::isfinite(h->kl) || h->kl < 0.0)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (tokens == nullptr || old_logp == nullptr || adv == nullptr) return MOE_ERR_INVALID_ARG;
+  if (h->kl > 0.0 && ref == nullptr) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int moe_policy_loss(int64_t T, int64_t V, const void* logits, int logits_dtype, const int32_t* tokens,
+                    const float* old_logp, const float* advantage, const float* ref_logp,
+                    const moe_policy_params* params, const float* weight, const float* grad_loss, float* loss,
+                    float* row_loss, float* logp, float* stats, void* dlogits, int dlogits_dtype,
+                    moe_stream_t stream) {
+  int st = loss_check(T, V, logits, logits_dtype, dlogits, dlogits_dtype);
+  if (st == MOE_OK) st = policy_check(T, tokens, old_logp, advantage, ref_logp, params);
+  if (st != MOE_OK) return st;
+  if (loss == nullptr || (T > 0 && (row_loss == nullptr || logp == nullptr || stats == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_policy_loss(T, static_cast<int>(V), logits, logits_dtype, tokens, old_logp, advantage,
+                                       params->kl > 0.0 ? ref_logp : nullptr, params->clip_low, params->clip_high,
+                                       params->kl, params->temperature, weight, grad_loss, loss, row_loss, logp, stats,
+                                       dlogits, dlogits_dtype, as_stream(stream)));
+}
+
+int moe_policy_loss_backward(int64_t T, int64_t V, const void* logits, int logits_dtype, const float* stats,
+                             const int32_t* tokens, const float* old_logp, const float* advantage,
+                             const float* ref_logp, const moe_policy_params* params, const float* weight,
+                             const float* grad_loss, void* dlogits, int dlogits_dtype, moe_stream_t stream) {
+  int st = loss_check(T, V, logits, logits_dtype, dlogits, dlogits_dtype);
+  if (st == MOE_OK) st = policy_check(T, tokens, old_logp, advantage, ref_logp, params);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (stats == nullptr || dlogits == nullptr || dlogits == logits) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_policy_loss_bwd(T, static_cast<int>(V), logits, logits_dtype, stats, tokens, old_logp,
+                                           advantage, params->kl > 0.0 ? ref_logp : nullptr, params->clip_low,
+                                           params->clip_high, params->kl, params->temperature, weight, grad_loss,
+                                           dlogits, dlogits_dtype, as_stream(stream)));
+}
+
+int moe_token_logp(int64_t T, int64_t V, const void* logits, int logits_dtype, const int32_t* tokens,
+                   double temperature, float* logp, float* stats, moe_stream_t stream) {
+  const int st = loss_check(T, V, logits, logits_dtype, nullptr, 0);
+  if (st != MOE_OK) return st;
+  if (!is_temperature(temperature)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (tokens == nullptr || logp == nullptr || stats == nullptr) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_policy_loss(T, static_cast<int>(V), logits, logits_dtype, tokens, nullptr, nullptr, nullptr,
+                                       0.0, 0.0, 0.0, temperature, nullptr, nullptr, nullptr, nullptr, logp, stats,
+                                       nullptr, 0, as_stream(stream)));
+}
+
 size_t moe_workspace_size(int op, const moe_shape* shape, int dtype) {
   switch (op) {
     case MOE_OP_ROUTE:

@@ -1,0 +1,240 @@
+// Distillation from a teacher's top logits.  For a row's entries (index i_j,
+// teacher logit t_j) with an index inside the vocabulary and a logit above -inf:
+//     p = softmax(t / tau) over the entries,   q = softmax(x / tau) over V
+//     l = tau^2 sum_j p_j (log p_j - log q[i_j])
+//     dl/dx[v] = tau (q[v] - sum_{j: i_j = v} p_j)
+// Without an entry, or with weight 0, a row adds nothing.  Indices may repeat.
+#include "vocab_loss.h"
+
+namespace moe {
+namespace {
+
+using vocab::exp2_of;
+using vocab::Logits;
+
+constexpr int kSlots = kMaxTeacher / kWave;  // entries a lane
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+
+struct Distill {
+  struct Args {
+    const int* idx;
+    const void* teacher;
+    int K, wide;  // wide: the teacher's logits are fp32
+  };
+  // The entries, and for each thread a list of those among the logits it stores.
+  template <int NT>
+  struct Shared {
+    int counted, K;
+    float sum;              // of the teacher's exponentials
+    float p[kMaxTeacher];   // probability (0: no entry)
+    float u[kMaxTeacher];   // teacher's logit less the largest
+    float x[kMaxTeacher];   // the student's logit
+    int at[kMaxTeacher];
+    int16_t next[kMaxTeacher];
+    int head[NT];
+    static constexpr int kThreads = NT;
+  };
+  static constexpr bool kLateFactor = false;
+
+  template <typename S>
+  static __device__ __forceinline__ void init(S& sh, int tid) {
+    sh.head[tid] = -1;
+  }
+  static __device__ __forceinline__ bool live(const Args&, int64_t, int) { return true; }
+
+  template <typename TX, int E, typename S>
+  static __device__ __forceinline__ void begin(const Logits& p, const Args& k, int64_t row, const TX* x, bool grad,
+                                               int lane, S& sh) {
+    int id[kSlots];
+    float t[kSlots];
+    bool ok[kSlots];
+    float top = -FLT_MAX;
+#pragma unroll
+    for (int e = 0; e < kSlots; ++e) {
+      ok[e] = false;
+      if (e * kWave >= k.K) continue;
+      const int j = e * kWave + lane;
+      const int64_t from = row * k.K + min(j, k.K - 1);
+      id[e] = k.idx[from];
+      t[e] = k.wide ? static_cast<const float*>(k.teacher)[from] : bf16_to_f32(static_cast<const uint16_t*>(k.teacher)[from]);
+      ok[e] = j < k.K && static_cast<unsigned>(id[e]) < static_cast<unsigned>(p.V) && t[e] != -INFINITY;
+      if (ok[e]) top = fmaxf(top, t[e]);
+    }
+    float xs[kSlots];
+#pragma unroll
+    for (int e = 0; e < kSlots; ++e) {
+      if (e * kWave >= k.K) continue;
+      xs[e] = one_f32(x[ok[e] ? id[e] : 0]);
+    }
+    top = wave_max(top);
+    float sum = 0.0f;
+    uint64_t any = 0;
+#pragma unroll
+    for (int e = 0; e < kSlots; ++e) {
+      if (e * kWave >= k.K) continue;
+      t[e] -= top;
+      sum += ok[e] ? exp2_of(t[e] * p.c) : 0.0f;
+      any |= __ballot(ok[e]);
+    }
+    sum = wave_sum(sum);
+#pragma unroll
+    for (int e = 0; e < kSlots; ++e) {
+      const int j = e * kWave + lane;
+      if (j >= k.K) continue;
+      sh.p[j] = ok[e] ? exp2_of(t[e] * p.c) / sum : 0.0f;
+      sh.u[j] = t[e];
+      sh.x[j] = xs[e];
+      sh.at[j] = ok[e] ? id[e] : -1;
+      if (grad && ok[e]) {
+        const int piece = id[e] / E, pieces = p.V / E;
+        const int owner = piece < pieces ? piece & (S::kThreads - 1) : id[e] - pieces * E;
+        sh.next[j] = static_cast<int16_t>(atomicExch(&sh.head[owner], j));
+      }
+    }
+    if (lane == 0) {
+      sh.counted = any != 0;
+      sh.K = k.K;
+      sh.sum = sum;
+    }
+  }
+
+  template <typename S>
+  static __device__ __forceinline__ void finish(const Logits& p, const Args& k, int64_t row, float, float m, float sum,
+                                                int lane, S& sh, bool) {
+    // fp64: the loss is a small difference of large logarithms where student and teacher agree
+    const bool counted = sh.counted != 0;
+    const double shift = vocab::ln_of(sum) - vocab::ln_of(sh.sum);
+    double l = 0.0;
+    for (int j = lane; j < k.K; j += kWave) {
+      const float pj = sh.p[j];
+      if (pj != 0.0f) {
+        const double d = static_cast<double>(sh.u[j]) - (static_cast<double>(sh.x[j]) - static_cast<double>(m));
+        l += pj * (d * p.inv_tau + shift);
+      }
+    }
+    l = wave_sum_f64(l);
+    if (lane == 0) {
+      p.row_loss[row] = counted ? static_cast<float>(l * p.tau * p.tau) : 0.0f;
+      p.stats[2 * row] = counted ? m : 0.0f;
+      p.stats[2 * row + 1] = counted ? sum : 0.0f;
+    }
+  }
+
+  template <typename S>
+  static __device__ __forceinline__ float factor(const Logits& p, float gw, const S& sh) {
+    return sh.counted ? gw * static_cast<float>(p.tau) : 0.0f;
+  }
+
+  // An index that comes several times is stored once, with the probabilities'
+  // sum in units of 2^-60, whose order does not matter.
+  template <int E, int NT, typename TD, typename S>
+  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, int lo, int hi, int tid, float m, float ks,
+                                               float kr, S& sh) {
+    int j = sh.head[tid];
+    if (j < 0) return;
+    sh.head[tid] = -1;
+    for (; j >= 0; j = sh.next[j]) {
+      const int v = sh.at[j];
+      if (v < lo || v >= hi || kr == 0.0f) continue;
+      float pj = sh.p[j];
+      uint64_t units = 0;
+      for (int i = sh.next[j]; i >= 0; i = sh.next[i]) {
+        if (sh.at[i] != v) continue;
+        if (units == 0) units = in_units(pj);
+        units += in_units(sh.p[i]);
+        sh.at[i] = -1;
+      }
+      if (units != 0 && pj == pj) pj = static_cast<float>(units) * 0x1p-60f;  // (NaN stays)
+      put_one(dx + v, ks * exp2_of((sh.x[j] - m) * p.c) - kr * pj);
+    }
+  }
+  static __device__ __forceinline__ uint64_t in_units(float v) { return static_cast<uint64_t>(v * 0x1p60f); }
+
+  static __device__ __forceinline__ void none(const Logits& p, const Args&, int64_t row) {
+    p.row_loss[row] = p.stats[2 * row] = p.stats[2 * row + 1] = 0.0f;
+  }
+};
+
+// 1024 threads add every 1024th row in fp64, then a fixed tree.
+__global__ __launch_bounds__(1024) void loss_sum_kernel(int64_t rows, const float* row_loss, const float* weight,
+                                                        float even, float* loss) {
+  constexpr int B = 8;
+  __shared__ double s_sum[16];
+  double v = 0.0;
+  for (int64_t t0 = threadIdx.x; t0 < rows; t0 += B * 1024) {
+    float l[B], w[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int64_t t = min(t0 + i * 1024, rows - 1);
+      l[i] = row_loss[t];
+      w[i] = weight != nullptr ? weight[t] : even;
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (t0 + i * 1024 < rows && w[i] != 0.0f) v += static_cast<double>(w[i]) * static_cast<double>(l[i]);
+    }
+  }
+  v = wave_sum_f64(v);
+  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  v = wave_sum_f64(threadIdx.x < 16 ? s_sum[threadIdx.x] : 0.0);
+  if (threadIdx.x == 0) *loss = static_cast<float>(v);
+}
+
+}  // namespace
+
+hipError_t launch_loss_sum(int64_t rows, const float* row_loss, const float* weight, float even, float* loss,
+                           hipStream_t s) {
+  hipLaunchKernelGGL(loss_sum_kernel, dim3(1), dim3(1024), 0, s, rows, row_loss, weight, even, loss);
+  return hipGetLastError();
+}
+
+static Logits distill_logits(int64_t rows, int V, double tau, const float* weight, const float* grad) {
+  Logits p{};
+  p.rows = rows;
+  p.V = V;
+  p.weight = weight;
+  p.grad = grad;
+  p.even = static_cast<float>(1.0 / static_cast<double>(rows));
+  p.tau = tau;
+  p.inv_tau = 1.0 / tau;
+  p.inv_tau_f = static_cast<float>(1.0 / tau);
+  p.c = static_cast<float>(1.4426950408889634 / tau);
+  return p;
+}
+
+hipError_t launch_distill_loss(int64_t rows, int V, int K, const void* x, int x_dtype, const int32_t* idx,
+                               const void* teacher, int t_dtype, double tau, const float* weight, const float* grad,
+                               float* loss, float* row_loss, float* stats, void* dx, int dx_dtype, hipStream_t s) {
+  if (rows > 0) {
+    Logits p = distill_logits(rows, V, tau, weight, grad);
+    p.x = x;
+    p.dx = dx;
+    p.stats = stats;
+    p.row_loss = row_loss;
+    const Distill::Args k{idx, teacher, K, t_dtype == MOE_F32};
+    const hipError_t e = vocab::loss_dtypes<Distill>(p, k, x_dtype, dx_dtype, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_loss_sum(rows, row_loss, weight, rows > 0 ? static_cast<float>(1.0 / static_cast<double>(rows)) : 0.0f,
+                         loss, s);
+}
+
+hipError_t launch_distill_loss_bwd(int64_t rows, int V, int K, const void* x, int x_dtype, const float* stats,
+                                   const int32_t* idx, const void* teacher, int t_dtype, double tau,
+                                   const float* weight, const float* grad, void* dx, int dx_dtype, hipStream_t s) {
+  Logits p = distill_logits(rows, V, tau, weight, grad);
+  p.x = x;
+  p.dx = dx;
+  p.stats = const_cast<float*>(stats);  // read only
+  const Distill::Args k{idx, teacher, K, t_dtype == MOE_F32};
+  return vocab::grad_dtypes<Distill>(p, k, x_dtype, dx_dtype, s);
+}
+
+}  // namespace moe

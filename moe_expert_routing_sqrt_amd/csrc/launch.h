@@ -154,4 +154,30 @@ hipError_t launch_layer_norm_bwd(int64_t rows, int d, const void* dy, int dy_dty
 hipError_t launch_adamw(int n_tensors, const moe_adamw_tensor* t, const moe_adamw_params& h, const float* grad_scale,
                         hipStream_t s);
 
+// embedding (embedding.hip)
+hipError_t launch_embedding(int64_t T, int V, int d, const int32_t* ids, const void* table, int table_dtype,
+                            float scale, void* out, int out_dtype, hipStream_t s);
+size_t embedding_bwd_workspace_bytes(int64_t T, int64_t V, int d);
+hipError_t launch_embedding_bwd(int64_t T, int V, int d, const int32_t* ids, const void* dy, int dy_dtype, float scale,
+                                void* d_table, int d_table_dtype, bool add, void* ws, hipStream_t s);
+
+// losses on logits (distill_loss.hip, policy_loss.hip); dx nullptr: the loss
+// alone; weight, grad, ref: nullptr for even weights, 1, no KL term
+constexpr int kMaxTeacher = MOE_MAX_TEACHER_TOP;
+hipError_t launch_distill_loss(int64_t rows, int V, int K, const void* x, int x_dtype, const int32_t* idx,
+                               const void* teacher, int t_dtype, double tau, const float* weight, const float* grad,
+                               float* loss, float* row_loss, float* stats, void* dx, int dx_dtype, hipStream_t s);
+hipError_t launch_distill_loss_bwd(int64_t rows, int V, int K, const void* x, int x_dtype, const float* stats,
+                                   const int32_t* idx, const void* teacher, int t_dtype, double tau,
+                                   const float* weight, const float* grad, void* dx, int dx_dtype, hipStream_t s);
+// adv and loss nullptr: log-probabilities only
+hipError_t launch_policy_loss(int64_t rows, int V, const void* x, int x_dtype, const int32_t* tok,
+                              const float* old_logp, const float* adv, const float* ref, double lo, double hi,
+                              double kl, double tau, const float* weight, const float* grad, float* loss,
+                              float* row_loss, float* logp, float* stats, void* dx, int dx_dtype, hipStream_t s);
+hipError_t launch_policy_loss_bwd(int64_t rows, int V, const void* x, int x_dtype, const float* stats,
+                                  const int32_t* tok, const float* old_logp, const float* adv, const float* ref,
+                                  double lo, double hi, double kl, double tau, const float* weight, const float* grad,
+                                  void* dx, int dx_dtype, hipStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,159 @@
+// The clipped policy loss with a KL term.  For a row's token with
+// logp = log softmax(x / tau)[token], r = exp(logp - old), d = ref - logp:
+//     l = -min(r A, clamp(r, 1 - lo, 1 + hi) A) + kl (exp(d) - d - 1)
+//     dl/dlogp = -[r A <= clamp(r) A] r A + kl (1 - exp(d))
+//     dx[v] = dl/dlogp / tau ([v = token] - q[v])
+// A row with weight 0 or a token outside the vocabulary adds nothing.
+#include "vocab_loss.h"
+
+namespace moe {
+namespace {
+
+using vocab::exp2_of;
+using vocab::Logits;
+
+struct Policy {
+  struct Args {
+    const int* tok;
+    const float* old_logp;
+    const float* adv;  // nullptr: log-probabilities only
+    const float* ref;  // nullptr: no KL term
+    float* logp;
+    float least, most, kl;  // the ratio's bounds, the KL term's weight
+  };
+  template <int NT>
+  struct Shared {
+    int tok;
+    float x, old_logp, adv, ref, k;
+  };
+  static constexpr bool kLateFactor = true;
+
+  template <typename S>
+  static __device__ __forceinline__ void init(S&, int) {}
+  static __device__ __forceinline__ bool live(const Args& k, int64_t row, int V) {
+    return static_cast<unsigned>(k.tok[row]) < static_cast<unsigned>(V);
+  }
+
+  template <typename TX, int E, typename S>
+  static __device__ __forceinline__ void begin(const Logits&, const Args& k, int64_t row, const TX* x, bool, int lane,
+                                               S& sh) {
+    if (lane != 0) return;
+    const int tok = k.tok[row];
+    sh.tok = tok;
+    sh.x = one_f32(x[tok]);
+    if (k.adv == nullptr) return;
+    sh.adv = k.adv[row];
+    sh.old_logp = k.old_logp[row];
+    if (k.ref != nullptr) sh.ref = k.ref[row];
+  }
+
+  // The differences of log-probabilities in fp64 (their absolute error is the
+  // ratio's relative one), exponentials in fp32 with the exponent's rounding error
+  // carried.
+  template <typename S>
+  static __device__ __forceinline__ void finish(const Logits& p, const Args& k, int64_t row, float gw, float m,
+                                                float sum, int lane, S& sh, bool outputs) {
+    if (lane != 0) return;
+    const double logp = (static_cast<double>(sh.x) - static_cast<double>(m)) * p.inv_tau - vocab::ln_of(sum);
+    if (outputs) {
+      k.logp[row] = static_cast<float>(logp);
+      p.stats[2 * row] = m;
+      p.stats[2 * row + 1] = sum;
+    }
+    if (k.adv == nullptr) return;
+    const float a = sh.adv, r = exp_of(static_cast<float>(logp - static_cast<double>(sh.old_logp)));
+    const float free = r * a, cut = fminf(fmaxf(r, k.least), k.most) * a;
+    float l = free > cut ? -cut : -free, slope = free > cut ? 0.0f : -free;
+    if (k.ref != nullptr) {
+      const float d = static_cast<float>(static_cast<double>(sh.ref) - logp), g = gap_of(d);
+      l += k.kl * g;
+      slope -= k.kl * (fabsf(d) < 0.5f ? d + g : exp_of(d) - 1.0f);
+    }
+    if (outputs) p.row_loss[row] = l;
+    sh.k = -slope * p.inv_tau_f * gw;
+  }
+  static __device__ __forceinline__ float exp_of(float v) {
+    const float t = v * 1.44269504f, lo = __builtin_fmaf(v, 1.44269504f, -t) + v * 1.92596299e-8f;
+    const float e = exp2_of(t);
+    return fabsf(t) < 150.0f ? __builtin_fmaf(e, lo * 0.693147181f, e) : e;  // (infinities and NaN as they are)
+  }
+  // exp(d) - d - 1; near 0, where that would cancel, as its series to d^10
+  static __device__ __forceinline__ float gap_of(float d) {
+    if (!(fabsf(d) < 0.5f)) return exp_of(d) - d - 1.0f;
+    float s = 1.0f / 3628800;
+    constexpr float kInv[] = {1.0f / 362880, 1.0f / 40320, 1.0f / 5040, 1.0f / 720, 1.0f / 120, 1.0f / 24, 1.0f / 6, 0.5f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(s, d, kInv[i]);
+    return s * d * d;
+  }
+
+  template <typename S>
+  static __device__ __forceinline__ float factor(const Logits&, float, const S& sh) {
+    return sh.k;
+  }
+
+  template <int E, int NT, typename TD, typename S>
+  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, int lo, int hi, int tid, float m, float ks,
+                                               float kr, S& sh) {
+    const int v = sh.tok, piece = v / E, pieces = p.V / E;
+    const int owner = piece < pieces ? piece & (NT - 1) : v - pieces * E;
+    if (tid != owner || v < lo || v >= hi || kr == 0.0f) return;
+    put_one(dx + v, ks * exp2_of((sh.x - m) * p.c) - kr);
+  }
+
+  static __device__ __forceinline__ void none(const Logits& p, const Args& k, int64_t row) {
+    p.stats[2 * row] = p.stats[2 * row + 1] = k.logp[row] = 0.0f;
+    if (k.adv != nullptr) p.row_loss[row] = 0.0f;
+  }
+};
+
+Logits policy_logits(int64_t rows, int V, double tau, const float* weight, const float* grad) {
+  Logits p{};
+  p.rows = rows;
+  p.V = V;
+  p.weight = weight;
+  p.grad = grad;
+  p.even = static_cast<float>(1.0 / static_cast<double>(rows));
+  p.tau = tau;
+  p.inv_tau = 1.0 / tau;
+  p.inv_tau_f = static_cast<float>(1.0 / tau);
+  p.c = static_cast<float>(1.4426950408889634 / tau);
+  return p;
+}
+
+}  // namespace
+
+hipError_t launch_policy_loss(int64_t rows, int V, const void* x, int x_dtype, const int32_t* tok,
+                              const float* old_logp, const float* adv, const float* ref, double lo, double hi,
+                              double kl, double tau, const float* weight, const float* grad, float* loss,
+                              float* row_loss, float* logp, float* stats, void* dx, int dx_dtype, hipStream_t s) {
+  if (rows > 0) {
+    Logits p = policy_logits(rows, V, tau, weight, grad);
+    p.x = x;
+    p.dx = dx;
+    p.stats = stats;
+    p.row_loss = row_loss;
+    const Policy::Args k{tok, old_logp, adv, ref, logp, static_cast<float>(1.0 - lo),
+                         static_cast<float>(1.0 + hi), static_cast<float>(kl)};
+    const hipError_t e = vocab::loss_dtypes<Policy>(p, k, x_dtype, dx_dtype, s);
+    if (e != hipSuccess || loss == nullptr) return e;
+  }
+  if (loss == nullptr) return hipSuccess;
+  return launch_loss_sum(rows, row_loss, weight, rows > 0 ? static_cast<float>(1.0 / static_cast<double>(rows)) : 0.0f,
+                         loss, s);
+}
+
+hipError_t launch_policy_loss_bwd(int64_t rows, int V, const void* x, int x_dtype, const float* stats,
+                                  const int32_t* tok, const float* old_logp, const float* adv, const float* ref,
+                                  double lo, double hi, double kl, double tau, const float* weight, const float* grad,
+                                  void* dx, int dx_dtype, hipStream_t s) {
+  Logits p = policy_logits(rows, V, tau, weight, grad);
+  p.x = x;
+  p.dx = dx;
+  p.stats = const_cast<float*>(stats);  // read only
+  const Policy::Args k{tok, old_logp, adv, ref, nullptr, static_cast<float>(1.0 - lo),
+                       static_cast<float>(1.0 + hi), static_cast<float>(kl)};
+  return vocab::grad_dtypes<Policy>(p, k, x_dtype, dx_dtype, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,434 @@
+// Losses on rows of logits over a vocabulary and their gradients, as one kernel
+// each: what the distillation loss and the policy loss share.
+//
+// Both take a softmax q over the V logits x of a row at temperature tau, need
+// q at a few entries, and have the gradient
+//     dx[v] = k (q[v] - sum_{j: i_j = v} p_j)
+// with a factor k of the row and weights p_j of its entries (distillation: the
+// teacher's probabilities; policy: 1 at the token).  KIND says what a row's few
+// entries are and how its loss and k come from them:
+//
+//   Shared<NT>   what the row's threads share
+//   live         whether the row may count (the same in all its threads)
+//   begin        wave 0 of the row, before the sums: its entries into Shared
+//   finish       wave 0, with the row's maximum and sum: statistics, loss, k
+//   factor       k, every thread (after finish where kLateFactor, else after begin)
+//   patch        every thread: the entries among the logits it stored, again
+//   none         one thread: the outputs of a row that does not count
+//
+// exp is 2^((x - max) log2(e)/tau): the difference first, so that its relative
+// error does not grow with the logits.  Sums are fp32, a thread's in order, then
+// a fixed tree.  A row without a finite logit gives NaN; a NaN spreads over its
+// row.  -inf is a logit of probability 0.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "launch.h"
+#include "rowvec.h"
+
+namespace moe {
+namespace vocab {
+
+struct Logits {
+  int64_t rows;
+  int V;
+  const void* x;
+  void* dx;             // or nullptr
+  float* stats;         // [rows][2]: maximum, sum of exp((x - max)/tau); the gradient alone reads it
+  const float* weight;  // [rows] or nullptr: 1 / rows
+  const float* grad;    // [1] or nullptr: 1
+  float* row_loss;
+  float even;           // 1 / rows
+  float c;              // log2(e) / tau
+  float inv_tau_f;
+  double inv_tau, tau;
+};
+
+__device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+__device__ __forceinline__ float weight_of(const Logits& p, int64_t row) {
+  return p.weight != nullptr ? p.weight[row] : p.even;
+}
+
+// ln(v) of a normal fp32 v > 0 to 6e-8 absolute: fp32 for the mantissa, the
+// exponent's share in fp64.  (libm's fp64 log would take 40 registers of
+// constants out of the rows' loop.)  0, infinities and NaN as log's.
+__device__ __forceinline__ double ln_of(float v) {
+  if (!(v > 0.0f && v < INFINITY)) return static_cast<double>(__builtin_logf(v));
+  const uint32_t u = __float_as_uint(v) - 0x3F3504F3u;  // mantissa in [0.707, 1.414)
+  const int e = static_cast<int>(u) >> 23;
+  const float f = __uint_as_float((u & 0x7FFFFFu) + 0x3F3504F3u);
+  return static_cast<double>(e) * 0.6931471805599453 +
+         static_cast<double>(__builtin_amdgcn_logf(f) * 0.6931471805599453f);
+}
+
+// Keeps the compiler from holding on to what it made of a piece: three passes
+// unpack the same registers, and their fp32 values would be twice the registers.
+template <typename T, int E>
+__device__ __forceinline__ void pin(Vec<T, E>& v) {
+#pragma unroll
+  for (int i = 0; i < Vec<T, E>::kWords; ++i) asm volatile("" : "+v"(v.w[i]));
+}
+
+// Pieces by their number, as a byte offset from the row's (scalar) address.
+template <bool STREAM, typename T, int E>
+__device__ __forceinline__ void load_at(Vec<T, E>& v, const T* row, int piece) {
+  const uint32_t at = static_cast<uint32_t>(piece) * static_cast<uint32_t>(E * sizeof(T));
+  load_vec<STREAM>(v, reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + at));
+}
+template <typename T, int E>
+__device__ __forceinline__ void store_at(T* row, const Vec<T, E>& v, int piece) {
+  const uint32_t at = static_cast<uint32_t>(piece) * static_cast<uint32_t>(E * sizeof(T));
+  store_vec<true>(reinterpret_cast<T*>(reinterpret_cast<char*>(row) + at), v);
+}
+__device__ __forceinline__ float uniform(float v) {  // the same in every lane
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+// the same number, but not one whose derived values are kept over the rows' loop
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Barrier of a row's threads (NT = 64: the wave, whose LDS accesses keep their
+// order).
+template <int NT>
+__device__ __forceinline__ void team_sync() {
+  if constexpr (NT > kWave) {
+    __syncthreads();
+  } else {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// a piece of logits: 16 bytes
+template <typename TX>
+constexpr int kPiece = 16 / static_cast<int>(sizeof(TX));
+
+constexpr int kBlock = 256;  // threads of a work-group whose rows are narrower
+template <int NT>
+constexpr int kTeams = NT < kBlock ? kBlock / NT : 1;  // rows a work-group has at once
+template <int NT>
+constexpr int kGroup = NT < kBlock ? kBlock : NT;
+
+// Loss, statistics and with GRAD the gradient, from one reading of the logits: a
+// row lives in the registers of its NT threads (NC pieces each).  A longer
+// row's other pieces are read twice, the second time as they lie in the caches.
+//
+// A work-group walks rows gridDim.x * kTeams apart.  The next row's piece is
+// loaded into each register as this row's last use of it is over, so that memory
+// is busy while a row is reduced.
+// waves a SIMD holds, by the registers a piece takes
+template <int NT, int NC>
+constexpr int kWaves = NC > 8 ? 4 : NC > 4 && NT < 1024 ? 5 : 8;
+template <typename KIND, typename TX, typename TD, int NT, int NC, bool GRAD>
+__global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(const Logits p, const typename KIND::Args k) {
+  constexpr int E = kPiece<TX>, WAVES = NT / kWave;
+  // two copies by turns where a wave may be a row ahead of another
+  constexpr int COPIES = WAVES > 1 ? 2 : 1;
+  __shared__ typename KIND::template Shared<NT> s_kind[kTeams<NT>][COPIES];
+  __shared__ float s_red[COPIES][2][16];  // the waves' maxima and sums
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int V = p.V, pieces = V / E, tail = V % E;  // the last V % E logits: one a thread
+  const int64_t step = (int64_t)gridDim.x * kTeams<NT>;
+  int64_t row = (int64_t)blockIdx.x * kTeams<NT> + team;
+  if (row >= p.rows) return;  // whole teams; no barrier where a work-group has several
+  for (int b = 0; b < COPIES; ++b) KIND::init(s_kind[team][b], tid);
+  if (WAVES > 1 && tid < COPIES * 32) (&s_red[0][0][0])[tid] = tid % 32 < 16 ? -FLT_MAX : 0.0f;
+  team_sync<NT>();
+  const float g = p.grad != nullptr ? *p.grad : 1.0f;
+
+  const float c = p.c;
+  const TX* const x0 = static_cast<const TX*>(p.x);
+  Vec<TX, E> h[NC > 0 ? NC : 1];
+  float t = -INFINITY;
+  int ft = tid;  // tid, as `fresh` gives it
+  // Without a branch (registers that a branch may or may not load are copied where
+  // it ends): what a row has no piece for, and every piece of a row that is not
+  // read, loads one that is there.
+  auto fetch = [&](int i, const TX* x, bool read) __attribute__((always_inline)) {
+    load_at<false>(h[i], x, min(i * NT + ft, read ? pieces - 1 : 0));
+  };
+  auto fetch_tail = [&](const TX* x) __attribute__((always_inline)) {
+    if (tail != 0) t = one_f32(x[(int64_t)pieces * E + min(tid, tail - 1)]);
+  };
+  float w = weight_of(p, row);
+  bool live = w != 0.0f && KIND::live(k, row, V);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) fetch(i, x0 + row * V, live);
+  fetch_tail(x0 + row * V);
+  int turn = 0;
+  for (; row < p.rows;) {
+    const int64_t next = row + step;
+    float w_next = 0.0f;
+    bool live_next = false;
+    if (next < p.rows) {
+      w_next = weight_of(p, next);
+      live_next = w_next != 0.0f && KIND::live(k, next, V);
+    }
+    ft = fresh(tid);
+    const TX* const x = x0 + row * V;
+    const TX* const xn = x0 + (next < p.rows ? next : row) * V;
+    TD* const dx = static_cast<TD*>(p.dx) + row * V;
+    auto zero_row = [&]() __attribute__((always_inline)) {
+      Vec<TD, E> z;
+#pragma unroll
+      for (int i = 0; i < Vec<TD, E>::kWords; ++i) z.w[i] = 0;
+      for (int i = tid; i < pieces; i += NT) store_at(dx, z, i);
+      if (tid < tail) put_one(dx + (int64_t)pieces * E + tid, 0.0f);
+    };
+    if (!live) {
+      if (tid == 0) {
+        p.stats[2 * row] = p.stats[2 * row + 1] = 0.0f;
+        KIND::none(p, k, row);
+      }
+      if constexpr (GRAD) zero_row();
+#pragma unroll
+      for (int i = 0; i < NC; ++i) fetch(i, xn, live_next);
+      fetch_tail(xn);
+    } else {
+      auto& sh = s_kind[team][turn];
+      if (wave == 0) KIND::template begin<TX, E>(p, k, row, x, GRAD, lane, sh);
+
+      // this thread's maximum and sum
+      float m = -FLT_MAX;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        float f[E];
+        vec_f32(h[i], f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) m = fmaxf(m, f[j]);  // (a repeated last piece changes nothing)
+        pin(h[i]);
+      }
+      const float tv = tid < tail ? t : -INFINITY;
+      m = fmaxf(m, tv);
+      float sum = exp2_of((tv - m) * c);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if (i * NT < pieces) {
+          float f[E], s1 = 0.0f;
+          vec_f32(h[i], f);
+#pragma unroll
+          for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m) * c);
+          sum += i * NT + ft < pieces ? s1 : 0.0f;
+        }
+        if constexpr (GRAD) pin(h[i]);
+        else fetch(i, xn, live_next);
+      }
+      if constexpr (!GRAD) fetch_tail(xn);
+      constexpr int U = 4;
+      for (int i0 = NC * NT + tid; i0 < pieces; i0 += U * NT) {  // what the registers do not hold
+        Vec<TX, E> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) load_at<false>(v[u], x, min(i0 + u * NT, pieces - 1));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[E], s1 = 0.0f, m1 = m;
+          vec_f32(v[u], f);
+#pragma unroll
+          for (int j = 0; j < E; ++j) m1 = fmaxf(m1, f[j]);
+#pragma unroll
+          for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m1) * c);
+          sum = sum * exp2_of((m - m1) * c) + (i0 + u * NT < pieces ? s1 : 0.0f);
+          m = m1;
+        }
+      }
+      // the row's
+      const float mw = wave_max(m);
+      sum = wave_sum(sum * exp2_of((m - mw) * c));
+      m = mw;
+      if constexpr (WAVES > 1) {
+        if (lane == 0) {
+          s_red[turn][0][wave] = m;
+          s_red[turn][1][wave] = sum;
+        }
+      }
+      team_sync<NT>();
+      if constexpr (WAVES > 1) {
+        const float m1 = s_red[turn][0][tid & 15];
+        sum = s_red[turn][1][tid & 15];
+        m = row16_max(m1);
+        sum = row16_sum(sum * exp2_of((m1 - m) * c));
+      }
+      if (wave == 0) KIND::finish(p, k, row, g * w, m, sum, lane, sh, true);
+      if constexpr (GRAD && KIND::kLateFactor) team_sync<NT>();
+      const float kr = GRAD ? uniform(KIND::factor(p, g * w, sh)) : 0.0f, ks = kr / sum;
+      if constexpr (GRAD) {
+        // k = 0: zeros, also where the logits hold anything
+        if (kr == 0.0f) zero_row();
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          if (i * NT < pieces && kr != 0.0f) {
+            float f[E];
+            vec_f32(h[i], f);
+#pragma unroll
+            for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+            Vec<TD, E> o;
+            f32_vec(o, f);
+            if (i * NT + ft < pieces) store_at(dx, o, i * NT + ft);
+          }
+          fetch(i, xn, live_next);
+        }
+        if (tid < tail && kr != 0.0f) put_one(dx + (int64_t)pieces * E + tid, ks * exp2_of((tv - m) * c));
+        fetch_tail(xn);
+        for (int i0 = kr != 0.0f ? NC * NT + tid : pieces; i0 < pieces; i0 += U * NT) {
+          Vec<TX, E> v[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) load_at<false>(v[u], x, min(i0 + u * NT, pieces - 1));
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float f[E];
+            vec_f32(v[u], f);
+#pragma unroll
+            for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+            Vec<TD, E> o;
+            f32_vec(o, f);
+            if (i0 + u * NT < pieces) store_at(dx, o, i0 + u * NT);
+          }
+        }
+      }
+      // (a thread's stores to one place keep their order)
+      if constexpr (GRAD) KIND::template patch<E, NT>(p, dx, 0, V, tid, m, ks, kr, sh);
+      if constexpr (COPIES > 1) turn ^= 1;
+      else team_sync<NT>();
+    }
+    row = next;
+    w = w_next;
+    live = live_next;
+  }
+}
+
+// The gradient from the logits and the forward's statistics: a work-group has
+// `span` pieces of a row, a multiple of NT (NT = 64: a wave has them).
+constexpr int kGradAhead = 4;
+template <typename KIND, typename TX, typename TD, int NT>
+__global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, const typename KIND::Args k, int splits,
+                                                             int span, int64_t units) {
+  constexpr int E = kPiece<TX>, U = kGradAhead;
+  __shared__ typename KIND::template Shared<NT> s_kind[kTeams<NT>];
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int V = p.V, pieces = V / E, tail = V % E;
+  const float g = p.grad != nullptr ? *p.grad : 1.0f, c = p.c;
+  auto& sh = s_kind[team];
+  for (int64_t unit = (int64_t)blockIdx.x * kTeams<NT> + team; unit < units; unit += (int64_t)gridDim.x * kTeams<NT>) {
+    const int64_t row = unit / splits;
+    const int part = static_cast<int>(unit % splits), first = part * span, last = min(pieces, first + span);
+    const TX* const x = static_cast<const TX*>(p.x) + row * V;
+    TD* const dx = static_cast<TD*>(p.dx) + row * V;
+    const bool ends = part == splits - 1, one = ends && tid < tail;
+    const float w = weight_of(p, row);
+    float kr = 0.0f, m = 0.0f, ks = 0.0f;
+    if (w != 0.0f && KIND::live(k, row, V)) {
+      KIND::init(sh, tid);
+      team_sync<NT>();
+      m = p.stats[2 * row];
+      const float sum = p.stats[2 * row + 1];
+      if (wave == 0) {
+        KIND::template begin<TX, E>(p, k, row, x, true, lane, sh);
+        if constexpr (KIND::kLateFactor) KIND::finish(p, k, row, g * w, m, sum, lane, sh, false);
+      }
+      team_sync<NT>();
+      kr = uniform(KIND::factor(p, g * w, sh));
+      ks = kr / sum;
+    }
+    if (kr == 0.0f) {  // nothing to read
+      Vec<TD, E> z;
+#pragma unroll
+      for (int i = 0; i < Vec<TD, E>::kWords; ++i) z.w[i] = 0;
+      for (int i = first + tid; i < last; i += NT) store_at(dx, z, i);
+      if (one) put_one(dx + (int64_t)pieces * E + tid, 0.0f);
+    } else {
+      for (int i0 = first + tid; i0 < last; i0 += U * NT) {
+        Vec<TX, E> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) load_at<false>(v[u], x, min(i0 + u * NT, last - 1));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[E];
+          vec_f32(v[u], f);
+#pragma unroll
+          for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          Vec<TD, E> o;
+          f32_vec(o, f);
+          if (i0 + u * NT < last) store_at(dx, o, i0 + u * NT);
+        }
+      }
+      if (one) {
+        const int64_t at = (int64_t)pieces * E + tid;
+        put_one(dx + at, ks * exp2_of((one_f32(x[at]) - m) * c));
+      }
+      KIND::template patch<E, NT>(p, dx, first * E, ends ? V : last * E, tid, m, ks, kr, sh);
+    }
+    team_sync<NT>();  // Shared is free again
+  }
+}
+
+// ---------------------------------------------------------------- launches
+// Threads of a row and the pieces each holds: a wave for rows of up to 8 pieces a
+// lane, 4 waves up to 16, then 16 waves.
+template <typename KIND, typename TX, typename TD, int NT, int NC, bool GRAD>
+hipError_t run_loss(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
+  const int64_t need = (p.rows + kTeams<NT> - 1) / kTeams<NT>;
+  // the work-groups the chip holds at once: waves a SIMD by the kernel's registers
+  const int64_t held = (int64_t)stream_cu_count(s) * 4 * kWaves<NT, NC> * kWave / kGroup<NT>;
+  const dim3 grid(static_cast<unsigned>(need < held ? need : held)), block(kGroup<NT>);
+  hipLaunchKernelGGL((loss_kernel<KIND, TX, TD, NT, NC, GRAD>), grid, block, 0, s, p, k);
+  return hipGetLastError();
+}
+
+template <typename KIND, typename TX, typename TD, bool GRAD>
+hipError_t loss_rows(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
+  const int pieces = p.V / kPiece<TX>;
+  if (pieces == 0) return run_loss<KIND, TX, TD, 64, 0, GRAD>(p, k, s);
+  if (pieces <= 2 * kWave) return run_loss<KIND, TX, TD, 64, 2, GRAD>(p, k, s);
+  if (pieces <= 8 * kWave) return run_loss<KIND, TX, TD, 64, 8, GRAD>(p, k, s);
+  if (pieces <= 4 * 256) return run_loss<KIND, TX, TD, 256, 4, GRAD>(p, k, s);
+  if (pieces <= 16 * 256) return run_loss<KIND, TX, TD, 256, 16, GRAD>(p, k, s);
+  if (pieces <= 8 * 1024) return run_loss<KIND, TX, TD, 1024, 8, GRAD>(p, k, s);
+  return run_loss<KIND, TX, TD, 1024, 16, GRAD>(p, k, s);
+}
+
+template <typename KIND, typename TX, typename TD, int NT>
+hipError_t run_grad(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
+  // 8 pieces a thread
+  const int pieces = p.V / kPiece<TX>, span = 8 * NT, splits = pieces <= span ? 1 : (pieces + span - 1) / span;
+  const int64_t units = p.rows * splits, groups = (units + kTeams<NT> - 1) / kTeams<NT>;
+  const dim3 grid(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20)), block(kGroup<NT>);
+  hipLaunchKernelGGL((grad_kernel<KIND, TX, TD, NT>), grid, block, 0, s, p, k, splits, span, units);
+  return hipGetLastError();
+}
+
+template <typename KIND, typename TX, typename TD>
+hipError_t grad_rows(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
+  if (p.V / kPiece<TX> <= 8 * kWave) return run_grad<KIND, TX, TD, 64>(p, k, s);
+  return run_grad<KIND, TX, TD, 256>(p, k, s);
+}
+
+// x_dtype, dx_dtype: MOE_F32 or MOE_BF16
+template <typename KIND>
+hipError_t loss_dtypes(const Logits& p, const typename KIND::Args& k, int x_dtype, int dx_dtype, hipStream_t s) {
+  using B = uint16_t;
+  const bool xb = x_dtype == MOE_BF16, db = dx_dtype == MOE_BF16;
+  if (p.dx == nullptr) return xb ? loss_rows<KIND, B, float, false>(p, k, s) : loss_rows<KIND, float, float, false>(p, k, s);
+  if (xb) return db ? loss_rows<KIND, B, B, true>(p, k, s) : loss_rows<KIND, B, float, true>(p, k, s);
+  return db ? loss_rows<KIND, float, B, true>(p, k, s) : loss_rows<KIND, float, float, true>(p, k, s);
+}
+template <typename KIND>
+hipError_t grad_dtypes(const Logits& p, const typename KIND::Args& k, int x_dtype, int dx_dtype, hipStream_t s) {
+  using B = uint16_t;
+  const bool xb = x_dtype == MOE_BF16, db = dx_dtype == MOE_BF16;
+  if (xb) return db ? grad_rows<KIND, B, B>(p, k, s) : grad_rows<KIND, B, float>(p, k, s);
+  return db ? grad_rows<KIND, float, B>(p, k, s) : grad_rows<KIND, float, float>(p, k, s);
+}
+
+}  // namespace vocab
+
+// loss[0] = sum_t weight[t] row_loss[t] (weight nullptr: even), in a fixed order
+hipError_t launch_loss_sum(int64_t rows, const float* row_loss, const float* weight, float even, float* loss,
+                           hipStream_t s);
+
+}  // namespace moe

@@ -28,6 +28,9 @@ Stages (pages cited by title and section):
   norm      - layer norm with the residual add, and its backward
   balance_loss - the router's balance loss, counts and gradient
   adamw     - the optimizer step with fp32 or 8-bit states
+  embedding - the embedding lookup with scaling and its gradient
+  vocab_loss - the losses on logits over a vocabulary and their gradients:
+              distillation from a teacher's top logits, the clipped policy loss
 
 Parity pinned by tests/test_oracle_*.py; see each module's header for the pins
 and for the functions whose parity the pages leave unpinned.
