@@ -12,8 +12,6 @@ namespace {
 using vocab::exp2_of;
 using vocab::Logits;
 
-constexpr int kSlots = kMaxTeacher / kWave;  // entries a lane
-
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o, kWave);
@@ -29,7 +27,7 @@ struct Distill {
   // The entries, and for each thread a list of those among the logits it stores.
   template <int NT>
   struct Shared {
-    int counted, K;
+    int counted;
     float sum;              // of the teacher's exponentials
     float p[kMaxTeacher];   // probability (0: no entry)
     float u[kMaxTeacher];   // teacher's logit less the largest
@@ -47,58 +45,75 @@ struct Distill {
   }
   static __device__ __forceinline__ bool live(const Args&, int64_t, int) { return true; }
 
+  // a lane's first entry
+  struct Ahead {
+    int id;
+    float t;
+  };
+  static __device__ __forceinline__ Ahead entry(const Args& k, int64_t row, int j) {
+    const int64_t from = row * k.K + min(j, k.K - 1);
+    return {k.idx[from], k.wide ? static_cast<const float*>(k.teacher)[from]
+                                : bf16_to_f32(static_cast<const uint16_t*>(k.teacher)[from])};
+  }
+  static __device__ __forceinline__ bool is_entry(const Logits& p, const Args& k, const Ahead& a, int j) {
+    return j < k.K && static_cast<unsigned>(a.id) < static_cast<unsigned>(p.V) && a.t != -INFINITY;
+  }
+  static __device__ __forceinline__ Ahead ahead(const Args& k, int64_t row, int tid) {
+    if (tid >= kWave) return {};
+    return entry(k, row, tid);
+  }
+  // and the student's logit there
+  template <typename TX>
+  struct Few {
+    Ahead a;
+    TX x;
+  };
+  template <typename TX>
+  static __device__ __forceinline__ Few<TX> begin(const Logits& p, const Args& k, int64_t, const TX* x, int tid,
+                                                  const Ahead& a) {
+    if (tid >= kWave) return {};
+    return {a, x[is_entry(p, k, a, tid) ? a.id : 0]};
+  }
+
   template <typename TX, int E, typename S>
-  static __device__ __forceinline__ void begin(const Logits& p, const Args& k, int64_t row, const TX* x, bool grad,
-                                               int lane, S& sh) {
-    int id[kSlots];
-    float t[kSlots];
-    bool ok[kSlots];
+  static __device__ __forceinline__ void share(const Logits& p, const Args& k, int64_t row, const TX* x, bool grad,
+                                               int lane, const Few<TX>& few, S& sh) {
     float top = -FLT_MAX;
-#pragma unroll
-    for (int e = 0; e < kSlots; ++e) {
-      ok[e] = false;
-      if (e * kWave >= k.K) continue;
-      const int j = e * kWave + lane;
-      const int64_t from = row * k.K + min(j, k.K - 1);
-      id[e] = k.idx[from];
-      t[e] = k.wide ? static_cast<const float*>(k.teacher)[from] : bf16_to_f32(static_cast<const uint16_t*>(k.teacher)[from]);
-      ok[e] = j < k.K && static_cast<unsigned>(id[e]) < static_cast<unsigned>(p.V) && t[e] != -INFINITY;
-      if (ok[e]) top = fmaxf(top, t[e]);
-    }
-    float xs[kSlots];
-#pragma unroll
-    for (int e = 0; e < kSlots; ++e) {
-      if (e * kWave >= k.K) continue;
-      xs[e] = one_f32(x[ok[e] ? id[e] : 0]);
+    uint64_t any = 0;
+    auto note = [&](int j, const Ahead& a, TX xs) __attribute__((always_inline)) {
+      const bool ok = is_entry(p, k, a, j);
+      any |= __ballot(ok);
+      if (ok) top = fmaxf(top, a.t);
+      if (j >= k.K) return;
+      sh.at[j] = ok ? a.id : -1;
+      sh.u[j] = a.t;
+      sh.x[j] = one_f32(xs);
+    };
+    note(lane, few.a, few.x);
+    for (int j0 = kWave; j0 < k.K; j0 += kWave) {
+      const Ahead a = entry(k, row, j0 + lane);
+      note(j0 + lane, a, x[is_entry(p, k, a, j0 + lane) ? a.id : 0]);
     }
     top = wave_max(top);
     float sum = 0.0f;
-    uint64_t any = 0;
-#pragma unroll
-    for (int e = 0; e < kSlots; ++e) {
-      if (e * kWave >= k.K) continue;
-      t[e] -= top;
-      sum += ok[e] ? exp2_of(t[e] * p.c) : 0.0f;
-      any |= __ballot(ok[e]);
+    for (int j = lane; j < k.K; j += kWave) {
+      const float u = sh.u[j] - top, e = sh.at[j] >= 0 ? exp2_of(u * p.c) : 0.0f;
+      sh.u[j] = u;
+      sh.p[j] = e;
+      sum += e;
     }
     sum = wave_sum(sum);
-#pragma unroll
-    for (int e = 0; e < kSlots; ++e) {
-      const int j = e * kWave + lane;
-      if (j >= k.K) continue;
-      sh.p[j] = ok[e] ? exp2_of(t[e] * p.c) / sum : 0.0f;
-      sh.u[j] = t[e];
-      sh.x[j] = xs[e];
-      sh.at[j] = ok[e] ? id[e] : -1;
-      if (grad && ok[e]) {
-        const int piece = id[e] / E, pieces = p.V / E;
-        const int owner = piece < pieces ? piece & (S::kThreads - 1) : id[e] - pieces * E;
+    for (int j = lane; j < k.K; j += kWave) {
+      sh.p[j] /= sum;
+      const int v = sh.at[j];
+      if (grad && v >= 0) {
+        const int piece = v / E, pieces = p.V / E;
+        const int owner = piece < pieces ? piece & (S::kThreads - 1) : v - pieces * E;
         sh.next[j] = static_cast<int16_t>(atomicExch(&sh.head[owner], j));
       }
     }
     if (lane == 0) {
       sh.counted = any != 0;
-      sh.K = k.K;
       sh.sum = sum;
     }
   }

@@ -24,27 +24,33 @@ struct Policy {
   template <int NT>
   struct Shared {
     int tok;
-    float x, old_logp, adv, ref, k;
+    float x, k;
   };
   static constexpr bool kLateFactor = true;
 
   template <typename S>
   static __device__ __forceinline__ void init(S&, int) {}
   static __device__ __forceinline__ bool live(const Args& k, int64_t row, int V) {
-    return static_cast<unsigned>(k.tok[row]) < static_cast<unsigned>(V);
+    return static_cast<unsigned>(vocab::scalar_of(k.tok + row)) < static_cast<unsigned>(V);
   }
-
+  struct Ahead {};
+  static __device__ __forceinline__ Ahead ahead(const Args&, int64_t, int) { return {}; }
+  template <typename TX>
+  struct Few {
+    int tok;
+    float x;
+  };
+  template <typename TX>
+  static __device__ __forceinline__ Few<TX> begin(const Logits&, const Args& k, int64_t row, const TX* x, int, Ahead) {
+    const int tok = vocab::scalar_of(k.tok + row);
+    return {tok, vocab::scalar_logit(x, tok)};
+  }
   template <typename TX, int E, typename S>
-  static __device__ __forceinline__ void begin(const Logits&, const Args& k, int64_t row, const TX* x, bool, int lane,
-                                               S& sh) {
+  static __device__ __forceinline__ void share(const Logits&, const Args&, int64_t, const TX*, bool, int lane,
+                                               const Few<TX>& few, S& sh) {
     if (lane != 0) return;
-    const int tok = k.tok[row];
-    sh.tok = tok;
-    sh.x = one_f32(x[tok]);
-    if (k.adv == nullptr) return;
-    sh.adv = k.adv[row];
-    sh.old_logp = k.old_logp[row];
-    if (k.ref != nullptr) sh.ref = k.ref[row];
+    sh.tok = few.tok;
+    sh.x = few.x;
   }
 
   // The differences of log-probabilities in fp64 (their absolute error is the
@@ -61,11 +67,12 @@ struct Policy {
       p.stats[2 * row + 1] = sum;
     }
     if (k.adv == nullptr) return;
-    const float a = sh.adv, r = exp_of(static_cast<float>(logp - static_cast<double>(sh.old_logp)));
+    const float a = vocab::scalar_of(k.adv + row);
+    const float r = exp_of(static_cast<float>(logp - static_cast<double>(vocab::scalar_of(k.old_logp + row))));
     const float free = r * a, cut = fminf(fmaxf(r, k.least), k.most) * a;
     float l = free > cut ? -cut : -free, slope = free > cut ? 0.0f : -free;
     if (k.ref != nullptr) {
-      const float d = static_cast<float>(static_cast<double>(sh.ref) - logp), g = gap_of(d);
+      const float d = static_cast<float>(static_cast<double>(vocab::scalar_of(k.ref + row)) - logp), g = gap_of(d);
       l += k.kl * g;
       slope -= k.kl * (fabsf(d) < 0.5f ? d + g : exp_of(d) - 1.0f);
     }

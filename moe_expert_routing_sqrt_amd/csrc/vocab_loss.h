@@ -10,9 +10,11 @@
 //
 //   Shared<NT>   what the row's threads share
 //   live         whether the row may count (the same in all its threads)
-//   begin        wave 0 of the row, before the sums: its entries into Shared
+//   ahead        what of a row is loaded while the row before it is at work
+//   begin        before the sums: with that, loads whose results are wanted after them
+//   share        wave 0 of the row, after its sums: the row's entries into Shared
 //   finish       wave 0, with the row's maximum and sum: statistics, loss, k
-//   factor       k, every thread (after finish where kLateFactor, else after begin)
+//   factor       k, every thread (after finish where kLateFactor, else after share)
 //   patch        every thread: the entries among the logits it stored, again
 //   none         one thread: the outputs of a row that does not count
 //
@@ -47,8 +49,25 @@ struct Logits {
 
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
 
+// A value of an input that the kernel does not write, at an address that is the
+// same in all lanes, through the scalar cache: it does not wait for the vector
+// loads in flight, which return in order.
+template <typename T>
+__device__ __forceinline__ T scalar_of(const T* p) {
+  static_assert(sizeof(T) == 4, "dwords");
+  return *reinterpret_cast<const __attribute__((address_space(4))) T*>(reinterpret_cast<uintptr_t>(p));
+}
+// a logit likewise (of a gradient written over the logits, the kernel writes it
+// only after this reading of it)
+__device__ __forceinline__ float scalar_logit(const float* x, int v) { return scalar_of(x + v); }
+__device__ __forceinline__ float scalar_logit(const uint16_t* x, int v) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(x + v);
+  const uint32_t w = scalar_of(reinterpret_cast<const uint32_t*>(at & ~uintptr_t{3}));
+  return __uint_as_float(at & 2 ? w & 0xFFFF0000u : w << 16);
+}
+
 __device__ __forceinline__ float weight_of(const Logits& p, int64_t row) {
-  return p.weight != nullptr ? p.weight[row] : p.even;
+  return p.weight != nullptr ? scalar_of(p.weight + row) : p.even;
 }
 
 // ln(v) of a normal fp32 v > 0 to 6e-8 absolute: fp32 for the mantissa, the
@@ -71,16 +90,22 @@ __device__ __forceinline__ void pin(Vec<T, E>& v) {
   for (int i = 0; i < Vec<T, E>::kWords; ++i) asm volatile("" : "+v"(v.w[i]));
 }
 
-// Pieces by their number, as a byte offset from the row's (scalar) address.
+// What lies `at` bytes from a row's (scalar) address, and pieces by their number.
+template <typename T>
+__device__ __forceinline__ const T* at_byte(const T* row, uint32_t at) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + at);
+}
+template <typename T>
+__device__ __forceinline__ T* at_byte(T* row, uint32_t at) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(row) + at);
+}
 template <bool STREAM, typename T, int E>
 __device__ __forceinline__ void load_at(Vec<T, E>& v, const T* row, int piece) {
-  const uint32_t at = static_cast<uint32_t>(piece) * static_cast<uint32_t>(E * sizeof(T));
-  load_vec<STREAM>(v, reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + at));
+  load_vec<STREAM>(v, at_byte(row, static_cast<uint32_t>(piece) * static_cast<uint32_t>(E * sizeof(T))));
 }
 template <typename T, int E>
 __device__ __forceinline__ void store_at(T* row, const Vec<T, E>& v, int piece) {
-  const uint32_t at = static_cast<uint32_t>(piece) * static_cast<uint32_t>(E * sizeof(T));
-  store_vec<true>(reinterpret_cast<T*>(reinterpret_cast<char*>(row) + at), v);
+  store_vec<true>(at_byte(row, static_cast<uint32_t>(piece) * static_cast<uint32_t>(E * sizeof(T))), v);
 }
 __device__ __forceinline__ float uniform(float v) {  // the same in every lane
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
@@ -88,6 +113,12 @@ __device__ __forceinline__ float uniform(float v) {  // the same in every lane
 // the same number, but not one whose derived values are kept over the rows' loop
 __device__ __forceinline__ int fresh(int v) {
   asm volatile("" : "+v"(v));
+  return v;
+}
+// a row's number likewise, in scalar registers: addresses are formed from it where
+// they are used instead of being carried along, a register pair each
+__device__ __forceinline__ int64_t fresh(int64_t v) {
+  asm volatile("" : "+s"(v));
   return v;
 }
 
@@ -107,6 +138,7 @@ __device__ __forceinline__ void team_sync() {
 template <typename TX>
 constexpr int kPiece = 16 / static_cast<int>(sizeof(TX));
 
+constexpr int kTogether = 4;  // pieces whose maximum is taken before their exponentials
 constexpr int kBlock = 256;  // threads of a work-group whose rows are narrower
 template <int NT>
 constexpr int kTeams = NT < kBlock ? kBlock / NT : 1;  // rows a work-group has at once
@@ -115,22 +147,24 @@ constexpr int kGroup = NT < kBlock ? kBlock : NT;
 
 // Loss, statistics and with GRAD the gradient, from one reading of the logits: a
 // row lives in the registers of its NT threads (NC pieces each).  A longer
-// row's other pieces are read twice, the second time as they lie in the caches.
+// row's other pieces (MORE) are read twice, the second time as they lie in the
+// caches.
 //
 // A work-group walks rows gridDim.x * kTeams apart.  The next row's piece is
 // loaded into each register as this row's last use of it is over, so that memory
-// is busy while a row is reduced.
+// is busy while a row is reduced; nothing between that and the next row's first
+// use waits for a vector load.
 // waves a SIMD holds, by the registers a piece takes
 template <int NT, int NC>
 constexpr int kWaves = NC > 8 ? 4 : NC > 4 && NT < 1024 ? 5 : 8;
-template <typename KIND, typename TX, typename TD, int NT, int NC, bool GRAD>
+template <typename KIND, typename TX, typename TD, int NT, int NC, bool MORE, bool GRAD>
 __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(const Logits p, const typename KIND::Args k) {
   constexpr int E = kPiece<TX>, WAVES = NT / kWave;
   // two copies by turns where a wave may be a row ahead of another
   constexpr int COPIES = WAVES > 1 ? 2 : 1;
   __shared__ typename KIND::template Shared<NT> s_kind[kTeams<NT>][COPIES];
   __shared__ float s_red[COPIES][2][16];  // the waves' maxima and sums
-  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT, lane = threadIdx.x & 63;
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int V = p.V, pieces = V / E, tail = V % E;  // the last V % E logits: one a thread
   const int64_t step = (int64_t)gridDim.x * kTeams<NT>;
@@ -139,88 +173,91 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
   for (int b = 0; b < COPIES; ++b) KIND::init(s_kind[team][b], tid);
   if (WAVES > 1 && tid < COPIES * 32) (&s_red[0][0][0])[tid] = tid % 32 < 16 ? -FLT_MAX : 0.0f;
   team_sync<NT>();
-  const float g = p.grad != nullptr ? *p.grad : 1.0f;
+  const float g = p.grad != nullptr ? scalar_of(p.grad) : 1.0f;
 
   const float c = p.c;
   const TX* const x0 = static_cast<const TX*>(p.x);
   Vec<TX, E> h[NC > 0 ? NC : 1];
-  float t = -INFINITY;
+  TX t{};
   int ft = tid;  // tid, as `fresh` gives it
   // Without a branch (registers that a branch may or may not load are copied where
   // it ends): what a row has no piece for, and every piece of a row that is not
   // read, loads one that is there.
   auto fetch = [&](int i, const TX* x, bool read) __attribute__((always_inline)) {
-    load_at<false>(h[i], x, min(i * NT + ft, read ? pieces - 1 : 0));
+    load_at<true>(h[i], x, min(i * NT + ft, read ? pieces - 1 : 0));
   };
   auto fetch_tail = [&](const TX* x) __attribute__((always_inline)) {
-    if (tail != 0) t = one_f32(x[(int64_t)pieces * E + min(tid, tail - 1)]);
+    t = *at_byte(x, static_cast<uint32_t>(min(pieces * E + ft, V - 1)) * static_cast<uint32_t>(sizeof(TX)));
   };
   float w = weight_of(p, row);
   bool live = w != 0.0f && KIND::live(k, row, V);
+  typename KIND::Ahead ahead = KIND::ahead(k, row, ft);
 #pragma unroll
   for (int i = 0; i < NC; ++i) fetch(i, x0 + row * V, live);
   fetch_tail(x0 + row * V);
   int turn = 0;
-  for (; row < p.rows;) {
-    const int64_t next = row + step;
-    float w_next = 0.0f;
-    bool live_next = false;
-    if (next < p.rows) {
-      w_next = weight_of(p, next);
-      live_next = w_next != 0.0f && KIND::live(k, next, V);
-    }
+  while (row < p.rows) {
+    row = fresh(row);
     ft = fresh(tid);
+    const int64_t next = row + step, after = next < p.rows ? next : row;
+    const float w_next = weight_of(p, after);
+    const bool live_next = next < p.rows && w_next != 0.0f && KIND::live(k, after, V);
     const TX* const x = x0 + row * V;
-    const TX* const xn = x0 + (next < p.rows ? next : row) * V;
+    const TX* const xn = x0 + after * V;
     TD* const dx = static_cast<TD*>(p.dx) + row * V;
+    auto tail_out = [&](float v) __attribute__((always_inline)) {
+      if (ft < tail) put_one(at_byte(dx, static_cast<uint32_t>(pieces * E + ft) * static_cast<uint32_t>(sizeof(TD))), v);
+    };
     auto zero_row = [&]() __attribute__((always_inline)) {
       Vec<TD, E> z;
 #pragma unroll
-      for (int i = 0; i < Vec<TD, E>::kWords; ++i) z.w[i] = 0;
-      for (int i = tid; i < pieces; i += NT) store_at(dx, z, i);
-      if (tid < tail) put_one(dx + (int64_t)pieces * E + tid, 0.0f);
+      for (int i = 0; i < Vec<TD, E>::kWords; ++i) z.w[i] = static_cast<uint32_t>(fresh(0));
+      for (int i = ft; i < pieces; i += NT) store_at(dx, z, i);
+      tail_out(0.0f);
     };
-    if (!live) {
-      if (tid == 0) {
-        p.stats[2 * row] = p.stats[2 * row + 1] = 0.0f;
-        KIND::none(p, k, row);
-      }
-      if constexpr (GRAD) zero_row();
-#pragma unroll
-      for (int i = 0; i < NC; ++i) fetch(i, xn, live_next);
-      fetch_tail(xn);
-    } else {
-      auto& sh = s_kind[team][turn];
-      if (wave == 0) KIND::template begin<TX, E>(p, k, row, x, GRAD, lane, sh);
+    auto& sh = s_kind[team][turn];
+    typename KIND::template Few<TX> few{};
+    if (live) few = KIND::template begin<TX>(p, k, row, x, ft, ahead);
+    ahead = KIND::ahead(k, after, ft);
 
-      // this thread's maximum and sum
-      float m = -FLT_MAX;
+    // This thread's maximum and sum, a few pieces at a time as they arrive.  (There
+    // is one place that loads a piece, taken by every row: with two, the registers
+    // would be copied where they meet, and the copies wait for all loads.)
+    const float tv = ft < tail ? one_f32(t) : -INFINITY;
+    float m = fmaxf(tv, -FLT_MAX), sum = exp2_of((tv - m) * c);
+    constexpr int G = NC < kTogether ? (NC > 0 ? NC : 1) : kTogether;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        float f[E];
-        vec_f32(h[i], f);
+    for (int i0 = 0; i0 < NC; i0 += G) {
+      if (live && i0 * NT < pieces) {
+        float m1 = m, s2 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) m = fmaxf(m, f[j]);  // (a repeated last piece changes nothing)
-        pin(h[i]);
-      }
-      const float tv = tid < tail ? t : -INFINITY;
-      m = fmaxf(m, tv);
-      float sum = exp2_of((tv - m) * c);
+        for (int i = i0; i < i0 + G; ++i) {
+          float f[E];
+          vec_f32(h[i], f);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (i * NT < pieces) {
+          for (int j = 0; j < E; ++j) m1 = fmaxf(m1, f[j]);  // (a repeated last piece changes nothing)
+        }
+#pragma unroll
+        for (int i = i0; i < i0 + G; ++i) {
           float f[E], s1 = 0.0f;
           vec_f32(h[i], f);
 #pragma unroll
-          for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m) * c);
-          sum += i * NT + ft < pieces ? s1 : 0.0f;
+          for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m1) * c);
+          s2 += i * NT + ft < pieces ? s1 : 0.0f;
         }
-        if constexpr (GRAD) pin(h[i]);
-        else fetch(i, xn, live_next);
+        sum = sum * exp2_of((m - m1) * c) + s2;
+        m = m1;
       }
-      if constexpr (!GRAD) fetch_tail(xn);
-      constexpr int U = 4;
-      for (int i0 = NC * NT + tid; i0 < pieces; i0 += U * NT) {  // what the registers do not hold
+      if constexpr (!GRAD) {
+#pragma unroll
+        for (int i = i0; i < i0 + G; ++i) fetch(i, xn, live_next);
+      }
+    }
+    if constexpr (!GRAD) fetch_tail(xn);
+    constexpr int U = 4;
+    float kr = 0.0f, ks = 0.0f;
+    if (live) {
+      for (int i0 = MORE ? NC * NT + ft : pieces; i0 < pieces; i0 += U * NT) {  // what the registers do not hold
         Vec<TX, E> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) load_at<false>(v[u], x, min(i0 + u * NT, pieces - 1));
@@ -241,57 +278,66 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
       sum = wave_sum(sum * exp2_of((m - mw) * c));
       m = mw;
       if constexpr (WAVES > 1) {
-        if (lane == 0) {
+        if ((ft & 63) == 0) {
           s_red[turn][0][wave] = m;
           s_red[turn][1][wave] = sum;
         }
       }
+      if (wave == 0) KIND::template share<TX, E>(p, k, row, x, GRAD, ft, few, sh);
       team_sync<NT>();
       if constexpr (WAVES > 1) {
-        const float m1 = s_red[turn][0][tid & 15];
-        sum = s_red[turn][1][tid & 15];
+        const float m1 = s_red[turn][0][ft & 15];
+        sum = s_red[turn][1][ft & 15];
         m = row16_max(m1);
         sum = row16_sum(sum * exp2_of((m1 - m) * c));
       }
-      if (wave == 0) KIND::finish(p, k, row, g * w, m, sum, lane, sh, true);
-      if constexpr (GRAD && KIND::kLateFactor) team_sync<NT>();
-      const float kr = GRAD ? uniform(KIND::factor(p, g * w, sh)) : 0.0f, ks = kr / sum;
+      if (wave == 0) KIND::finish(p, k, row, g * w, m, sum, ft, sh, true);
       if constexpr (GRAD) {
-        // k = 0: zeros, also where the logits hold anything
-        if (kr == 0.0f) zero_row();
+        if constexpr (KIND::kLateFactor) team_sync<NT>();
+        kr = uniform(KIND::factor(p, g * w, sh));
+        ks = kr / sum;
+      }
+    } else {
+      if (ft == 0) KIND::none(p, k, row);
+    }
+    if constexpr (GRAD) {
+      // k = 0: zeros, also where the logits hold anything
+      if (kr == 0.0f) zero_row();
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          if (i * NT < pieces && kr != 0.0f) {
-            float f[E];
-            vec_f32(h[i], f);
+      for (int i = 0; i < NC; ++i) {
+        pin(h[i]);
+        if (i * NT < pieces && kr != 0.0f) {
+          float f[E];
+          vec_f32(h[i], f);
 #pragma unroll
-            for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
-            Vec<TD, E> o;
-            f32_vec(o, f);
-            if (i * NT + ft < pieces) store_at(dx, o, i * NT + ft);
-          }
-          fetch(i, xn, live_next);
+          for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          Vec<TD, E> o;
+          f32_vec(o, f);
+          if (i * NT + ft < pieces) store_at(dx, o, i * NT + ft);
         }
-        if (tid < tail && kr != 0.0f) put_one(dx + (int64_t)pieces * E + tid, ks * exp2_of((tv - m) * c));
-        fetch_tail(xn);
-        for (int i0 = kr != 0.0f ? NC * NT + tid : pieces; i0 < pieces; i0 += U * NT) {
-          Vec<TX, E> v[U];
+        fetch(i, xn, live_next);
+      }
+      if (kr != 0.0f) tail_out(ks * exp2_of((tv - m) * c));
+      fetch_tail(xn);
+      for (int i0 = MORE && kr != 0.0f ? NC * NT + ft : pieces; i0 < pieces; i0 += U * NT) {
+        Vec<TX, E> v[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u) load_at<false>(v[u], x, min(i0 + u * NT, pieces - 1));
+        for (int u = 0; u < U; ++u) load_at<false>(v[u], x, min(i0 + u * NT, pieces - 1));
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            float f[E];
-            vec_f32(v[u], f);
+        for (int u = 0; u < U; ++u) {
+          float f[E];
+          vec_f32(v[u], f);
 #pragma unroll
-            for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
-            Vec<TD, E> o;
-            f32_vec(o, f);
-            if (i0 + u * NT < pieces) store_at(dx, o, i0 + u * NT);
-          }
+          for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          Vec<TD, E> o;
+          f32_vec(o, f);
+          if (i0 + u * NT < pieces) store_at(dx, o, i0 + u * NT);
         }
       }
       // (a thread's stores to one place keep their order)
-      if constexpr (GRAD) KIND::template patch<E, NT>(p, dx, 0, V, tid, m, ks, kr, sh);
+      if (live) KIND::template patch<E, NT>(p, dx, 0, V, ft, m, ks, kr, sh);
+    }
+    if (live) {
       if constexpr (COPIES > 1) turn ^= 1;
       else team_sync<NT>();
     }
@@ -312,7 +358,7 @@ __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, con
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int V = p.V, pieces = V / E, tail = V % E;
-  const float g = p.grad != nullptr ? *p.grad : 1.0f, c = p.c;
+  const float g = p.grad != nullptr ? scalar_of(p.grad) : 1.0f, c = p.c;
   auto& sh = s_kind[team];
   for (int64_t unit = (int64_t)blockIdx.x * kTeams<NT> + team; unit < units; unit += (int64_t)gridDim.x * kTeams<NT>) {
     const int64_t row = unit / splits;
@@ -325,10 +371,10 @@ __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, con
     if (w != 0.0f && KIND::live(k, row, V)) {
       KIND::init(sh, tid);
       team_sync<NT>();
-      m = p.stats[2 * row];
-      const float sum = p.stats[2 * row + 1];
+      m = scalar_of(p.stats + 2 * row);
+      const float sum = scalar_of(p.stats + 2 * row + 1);
       if (wave == 0) {
-        KIND::template begin<TX, E>(p, k, row, x, true, lane, sh);
+        KIND::template share<TX, E>(p, k, row, x, true, lane, KIND::template begin<TX>(p, k, row, x, lane, KIND::ahead(k, row, lane)), sh);
         if constexpr (KIND::kLateFactor) KIND::finish(p, k, row, g * w, m, sum, lane, sh, false);
       }
       team_sync<NT>();
@@ -370,26 +416,27 @@ __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, con
 // ---------------------------------------------------------------- launches
 // Threads of a row and the pieces each holds: a wave for rows of up to 8 pieces a
 // lane, 4 waves up to 16, then 16 waves.
-template <typename KIND, typename TX, typename TD, int NT, int NC, bool GRAD>
+template <typename KIND, typename TX, typename TD, int NT, int NC, bool MORE, bool GRAD>
 hipError_t run_loss(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
   const int64_t need = (p.rows + kTeams<NT> - 1) / kTeams<NT>;
-  // the work-groups the chip holds at once: waves a SIMD by the kernel's registers
+  // the work-groups the chip holds at once
   const int64_t held = (int64_t)stream_cu_count(s) * 4 * kWaves<NT, NC> * kWave / kGroup<NT>;
   const dim3 grid(static_cast<unsigned>(need < held ? need : held)), block(kGroup<NT>);
-  hipLaunchKernelGGL((loss_kernel<KIND, TX, TD, NT, NC, GRAD>), grid, block, 0, s, p, k);
+  hipLaunchKernelGGL((loss_kernel<KIND, TX, TD, NT, NC, MORE, GRAD>), grid, block, 0, s, p, k);
   return hipGetLastError();
 }
 
 template <typename KIND, typename TX, typename TD, bool GRAD>
 hipError_t loss_rows(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
   const int pieces = p.V / kPiece<TX>;
-  if (pieces == 0) return run_loss<KIND, TX, TD, 64, 0, GRAD>(p, k, s);
-  if (pieces <= 2 * kWave) return run_loss<KIND, TX, TD, 64, 2, GRAD>(p, k, s);
-  if (pieces <= 8 * kWave) return run_loss<KIND, TX, TD, 64, 8, GRAD>(p, k, s);
-  if (pieces <= 4 * 256) return run_loss<KIND, TX, TD, 256, 4, GRAD>(p, k, s);
-  if (pieces <= 16 * 256) return run_loss<KIND, TX, TD, 256, 16, GRAD>(p, k, s);
-  if (pieces <= 8 * 1024) return run_loss<KIND, TX, TD, 1024, 8, GRAD>(p, k, s);
-  return run_loss<KIND, TX, TD, 1024, 16, GRAD>(p, k, s);
+  if (pieces == 0) return run_loss<KIND, TX, TD, 64, 0, false, GRAD>(p, k, s);
+  if (pieces <= 2 * 64) return run_loss<KIND, TX, TD, 64, 2, false, GRAD>(p, k, s);
+  if (pieces <= 8 * 64) return run_loss<KIND, TX, TD, 64, 8, false, GRAD>(p, k, s);
+  if (pieces <= 4 * 256) return run_loss<KIND, TX, TD, 256, 4, false, GRAD>(p, k, s);
+  if (pieces <= 16 * 256) return run_loss<KIND, TX, TD, 256, 16, false, GRAD>(p, k, s);
+  if (pieces <= 16 * 512) return run_loss<KIND, TX, TD, 512, 16, false, GRAD>(p, k, s);
+  if (pieces <= 16 * 1024) return run_loss<KIND, TX, TD, 1024, 16, false, GRAD>(p, k, s);
+  return run_loss<KIND, TX, TD, 1024, 12, true, GRAD>(p, k, s);
 }
 
 template <typename KIND, typename TX, typename TD, int NT>

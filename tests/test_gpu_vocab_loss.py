@@ -5,9 +5,12 @@ Tolerances, from the operations' roundings (U = 2^-24, z = (x - max)/tau):
   e = 2^((x - max) c): a difference, a product and the rounded c give 3 U |z|
       relative, the exponential itself 2 U; where a thread's sum is brought to
       the row's maximum that comes once more.
-  sum: at most 8 + 16 + 10 additions and, past what the registers hold, one more
-      per piece: A U relative with A = 34 + V / 4096; the e's errors average to
-      (6 Z + 4) U with Z = sum e |z| / sum.  Together S.
+  sum: at most 8 + 16 + 10 additions; a thread's maximum grows in at most 4 steps,
+      each with an exponential and a product (3 U; its own |z| is part of the 6 Z
+      below, as the steps add up to at most |z|); past what the registers hold one
+      addition and one such step per piece, V / 4096 of them: A U relative with
+      A = 34 + 12 + 4 V / 4096; the e's errors average to (6 Z + 4) U with
+      Z = sum e |z| / sum.  Together S.
   ln of a sum: S absolute, and 4 U its own.
   teacher's probabilities: (3 |z| + 2 + 12 + 6 Zt + 4) U relative, as above with
       at most 12 additions.
@@ -64,7 +67,7 @@ def _row_stats(x, tau):
     e = np.exp(z)
     s = e.sum(1, keepdims=True)
     zz = np.where(e > 0, np.abs(z), 0.0)
-    S = U * (34 + V / 4096 + 6 * (e * zz).sum(1, keepdims=True) / s + 4)
+    S = U * (46 + V / 1024 + 6 * (e * zz).sum(1, keepdims=True) / s + 4)
     return zz, e / s, S
 
 
