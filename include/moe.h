@@ -663,8 +663,8 @@ int moe_embedding(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, con
  *            batch's ids are touched
  *   ws       moe_embedding_backward_workspace_size(T, V, d) bytes; nothing in it
  *            needs to start at zero
- * The sums are fp32 over runs of the batch sorted by id, in token order
- * (deterministic).
+ * T ceil(d / 1024) < 2^25.  The sums are fp32 over runs of the batch sorted by id,
+ * in token order (deterministic).
  */
 size_t moe_embedding_backward_workspace_size(int64_t T, int64_t V, int32_t d);
 int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* d_out,

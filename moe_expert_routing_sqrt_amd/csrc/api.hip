@@ -709,6 +709,7 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
     return MOE_ERR_INVALID_ARG;
   const int st = vocab_check(T, V);
   if (st != MOE_OK) return st;
+  if (T * ((d + 1023) / 1024) >= (int64_t{1} << 25)) return MOE_ERR_UNSUPPORTED;  // the launch's work-groups
   if (T > 0 && (token_ids == nullptr || d_out == nullptr)) return MOE_ERR_INVALID_ARG;
   if (d_table == nullptr || d_table == d_out) return MOE_ERR_INVALID_ARG;
   if (ws == nullptr || ws_bytes < embedding_bwd_workspace_bytes(T, V, d) || !aligned256(ws)) return MOE_ERR_WORKSPACE;

@@ -15,6 +15,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kMaxGroups = UINT32_MAX / kThreads;  // a launch holds fewer than 2^32 threads
 
 // A thread's piece of a row of d elements: E of them from c.  The row's last
 // piece is moved back to end with the row and owns only what the piece before
@@ -47,10 +48,10 @@ __device__ __forceinline__ void load_piece(Vec<T, E>& v, const T* row, int c, in
 }
 
 // stores elements [lo, min(E, d))
-template <typename T, int E>
+template <bool STREAM, typename T, int E>
 __device__ __forceinline__ void store_piece(T* row, const Vec<T, E>& v, int c, int lo, int d) {
   if (d >= E && lo == 0) {
-    store_vec<true>(row + c, v);
+    store_vec<STREAM>(row + c, v);
     return;
   }
 #pragma unroll
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const LookupArgs p)
         for (int j = 0; j < E; ++j) f[j] = in ? f[j] * p.scale : 0.0f;
         Vec<TO, E> o;
         f32_vec(o, f);
-        store_piece(dst, o, q.c, 0, p.d);  // what two pieces share is the same in both
+        store_piece<true>(dst, o, q.c, 0, p.d);  // what two pieces share is the same in both
       }
     }
   }
@@ -112,7 +113,6 @@ hipError_t lookup(const LookupArgs& a, hipStream_t s) {
   const int pieces = (a.d + E - 1) / E;
   const bool narrow = pieces <= kWave * kAhead;  // a wave per row
   const int64_t rows = narrow ? kThreads / kWave : 1, groups = (a.T + rows - 1) / rows;
-  // (a launch holds fewer than 2^32 threads)
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(groups, 1 << 22))), block(kThreads);
   if (narrow) hipLaunchKernelGGL((embedding_kernel<TX, TO, E, kWave>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((embedding_kernel<TX, TO, E, kThreads>), grid, block, 0, s, a);
@@ -121,13 +121,15 @@ hipError_t lookup(const LookupArgs& a, hipStream_t s) {
 
 // ---------------------------------------------------------------- sort
 // One launch.  Work-group r takes the table rows [r * span, (r + 1) * span): it
-// reads every id twice (they stay in the XCD's L2), each of its 16 waves one
-// sixteenth of the batch, and counts those of its rows and those below them.
-// The counts per wave and row give every wave its first position for every row,
-// so that the second reading places its tokens in token order.
+// goes through every id twice (they stay in the XCD's L2, or in registers), each
+// of its 16 waves one sixteenth of the batch, and counts those of its rows and
+// those below them.  The counts per wave and row give every wave its first
+// position for every row, so that the second time it places its tokens in token
+// order.
 constexpr int kSortWaves = 16;
 constexpr int kMaxSpan = 1024;
-constexpr int kIdsAhead = 8;
+constexpr int kHeldIds = 16;  // ids of a thread that stay in registers: batches of up to 16384
+constexpr int kFewLanes = 8;
 
 struct SortArgs {
   const int* ids;
@@ -136,45 +138,50 @@ struct SortArgs {
   int* start;            // [V + 1] each id's first position; start[V]: tokens with an id inside
 };
 
+template <bool HELD>
 __global__ __launch_bounds__(kSortWaves* kWave) void embedding_sort_kernel(const SortArgs p) {
+  constexpr int B = HELD ? kHeldIds : 8;
   extern __shared__ int s_count[];  // [kSortWaves][span]
   __shared__ int s_below, s_total[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int first = blockIdx.x * p.span, n = min(p.span, p.V - first);
-  for (int i = tid; i < kSortWaves * p.span; i += blockDim.x) s_count[i] = 0;
-  if (tid == 0) s_below = 0;
-  __syncthreads();
   int* const mine = s_count + wave * p.span;
   const int per = ((p.T + kSortWaves - 1) / kSortWaves + kWave - 1) / kWave * kWave;
   const int t0 = min(p.T, wave * per), t1 = min(p.T, t0 + per);
-  auto batch = [&](int t, int (&id)[kIdsAhead]) __attribute__((always_inline)) {
+  int id[B];
+  auto batch = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int b = 0; b < kIdsAhead; ++b) {
-      const int at = t + b * kWave + lane;
-      id[b] = p.ids[min(at, p.T - 1)];
-      if (at >= t1) id[b] = -1;
-    }
+    for (int b = 0; b < B; ++b) id[b] = p.ids[max(0, min(t + b * kWave + lane, t1 - 1))];
+#pragma unroll
+    for (int b = 0; b < B; ++b) id[b] = t + b * kWave + lane < t1 ? id[b] : -1;
   };
+  if (HELD && p.T > 0) batch(t0);
+  for (int i = tid; i < kSortWaves * p.span; i += blockDim.x) s_count[i] = 0;
+  if (tid == 0) s_below = 0;
+  __syncthreads();
   int below = 0;
-  for (int t = t0; t < t1; t += kIdsAhead * kWave) {
-    int id[kIdsAhead];
-    batch(t, id);
+  for (int t = t0; t < t1; t += B * kWave) {
+    if (!HELD) batch(t);
 #pragma unroll
-    for (int b = 0; b < kIdsAhead; ++b) {
-      below += id[b] >= 0 && id[b] < first;
+    for (int b = 0; b < B; ++b) {
+      if (HELD && t + b * kWave >= t1) break;
+      below += __popcll(__ballot(id[b] >= 0 && id[b] < first));
       const int r = id[b] - first;
       if (id[b] >= 0 && static_cast<unsigned>(r) < static_cast<unsigned>(n)) atomicAdd(&mine[r], 1);
     }
   }
-  if (below > 0) atomicAdd(&s_below, below);
+  if (lane == 0 && below > 0) atomicAdd(&s_below, below);
   __syncthreads();
   // counts to first positions: over the waves of each row, then over the rows
-  int total = 0;
+  int total = 0, c[kSortWaves];
   if (tid < n) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = s_count[w * p.span + tid];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const int c = s_count[w * p.span + tid];
-      s_count[w * p.span + tid] = total;
-      total += c;
+      const int v = c[w];
+      c[w] = total;
+      total += v;
     }
   }
   int upto = total;
@@ -188,49 +195,65 @@ __global__ __launch_bounds__(kSortWaves* kWave) void embedding_sort_kernel(const
   int base = s_below + upto - total;
   for (int w = 0; w < wave; ++w) base += s_total[w];
   if (tid < n) {
-    for (int w = 0; w < kSortWaves; ++w) s_count[w * p.span + tid] += base;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) s_count[w * p.span + tid] = c[w] + base;
     p.start[first + tid] = base;
     if (first + tid == p.V - 1) p.start[p.V] = base + total;
   }
   __syncthreads();
-  for (int t = t0; t < t1; t += kIdsAhead * kWave) {
-    int id[kIdsAhead];
-    batch(t, id);
+  for (int t = t0; t < t1; t += B * kWave) {
+    if (!HELD) batch(t);
 #pragma unroll
-    for (int b = 0; b < kIdsAhead; ++b) {
+    for (int b = 0; b < B; ++b) {
+      if (HELD && t + b * kWave >= t1) break;
       const int r = id[b] - first;
       const bool in = id[b] >= 0 && static_cast<unsigned>(r) < static_cast<unsigned>(n);
-      uint64_t same = __ballot(in);
-      if (same == 0) continue;
-      for (int k = 0; k < p.bits; ++k) {  // the lanes with this lane's row
-        const bool bit = (r >> k) & 1;
-        const uint64_t set = __ballot(bit);
-        same &= bit ? set : ~set;
-      }
-      const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
-      asm volatile("" ::: "memory");  // the wave's positions as its own last batch left them
+      uint64_t left = __ballot(in);
+      if (left == 0) continue;
       int pos = 0;
-      if (in) pos = mine[r] + rank;
-      asm volatile("" ::: "memory");
-      if (in && rank == 0) mine[r] = pos + __popcll(same);
+      if (__popcll(left) <= kFewLanes) {  // one row after the other
+        while (left != 0) {
+          const int at = __builtin_amdgcn_readlane(r, __builtin_ctzll(left));
+          const uint64_t same = __ballot(in && r == at);
+          const int from = mine[at];
+          if (in && r == at) pos = from + __popcll(same & ((uint64_t{1} << lane) - 1));
+          asm volatile("" ::: "memory");  // the wave's positions as it left them itself
+          if (lane == 0) mine[at] = from + __popcll(same);
+          asm volatile("" ::: "memory");
+          left &= ~same;
+        }
+      } else {  // all at once: the lanes with this lane's row, by the bits of its number
+        uint64_t same = left;
+        for (int k = 0; k < p.bits; ++k) {
+          const bool bit = (r >> k) & 1;
+          const uint64_t set = __ballot(bit);
+          same &= bit ? set : ~set;
+        }
+        const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
+        asm volatile("" ::: "memory");
+        if (in) pos = mine[r] + rank;
+        asm volatile("" ::: "memory");
+        if (in && rank == 0) mine[r] = pos + __popcll(same);
+        asm volatile("" ::: "memory");
+      }
       if (in) p.sorted[pos] = make_int2(t + b * kWave + lane, id[b]);
     }
   }
 }
 
 // ---------------------------------------------------------------- gradient
-// Work-groups of three kinds in one launch, by columns in y:
-//   runs   kRunChunk sorted positions each: the rows whose run starts there and
-//          has at most kLong tokens, summed and stored;
-//   long   kLong positions each: the part of a longer run that lies there (at
-//          most two, the end of one and the start of another), to `part`;
-//   zeros  kZeroRows table rows each: those without a token (not when adding).
+// Work-groups of three kinds in one launch:
+//   runs   kRunChunk sorted positions and a block of columns each: the rows whose
+//          run starts there and has at most kLong tokens, summed and stored;
+//   long   kLong positions and a block of columns each: the part of a longer run
+//          that lies there (at most two, the end of one and the start of another),
+//          to `part`; and whether a join starts there, to `job`;
+//   zeros  some table rows each: those without a token (not when adding).
 // A second launch joins the parts of every long run in order.  Every lane
 // of a wave holds one sorted position (two for runs), boundaries are ballots,
 // and a token's number reaches the scalar unit by a lane read.
 constexpr int kLong = 64;
 constexpr int kRunChunk = 8;
-constexpr int kZeroRows = 8;
 static_assert(kRunChunk + kLong < 2 * kWave && kLong == kWave, "positions a wave holds");
 
 struct GradArgs {
@@ -238,99 +261,77 @@ struct GradArgs {
   const int* start;
   const void* dy;
   void* table;
-  float* part;  // [ceil(T / kLong)][2][d]
-  int T, V, d, runs, longs;
+  float* part;  // [longs][2][d]
+  int* job;     // [longs] the row whose parts are joined from this chunk on, or -1
+  int T, V, d, runs, longs, blocks, zero_rows;
   float scale;
 };
 
 __device__ __forceinline__ int lane_of(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
 
-// Sum of the rows [i, e) of `tok` (lane numbers below 128: lanes of tok0, then
-// tok1), in order, TB rows in flight.
-template <typename TX, int E, int U, int TB>
-__device__ __forceinline__ void sum_tokens(const TX* dy, int d, const int (&c)[U], int tok0, int tok1, int i, int e,
-                                           float (&acc)[U][E]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-#pragma unroll
-    for (int j = 0; j < E; ++j) acc[u][j] = 0.0f;
-  }
-  for (; i < e; i += TB) {
-    Vec<TX, E> v[TB][U];
-#pragma unroll
-    for (int k = 0; k < TB; ++k) {
-      if (i + k >= e) break;
-      const int at = i + k;
-      const int tok = at < kWave ? lane_of(tok0, at) : lane_of(tok1, at - kWave);
-      const TX* row = dy + (int64_t)tok * d;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (c[u] >= 0) load_piece(v[k][u], row, c[u], d);
-    }
-#pragma unroll
-    for (int k = 0; k < TB; ++k) {
-      if (i + k >= e) break;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[E];
-        vec_f32(v[k][u], f);
-#pragma unroll
-        for (int j = 0; j < E; ++j) acc[u][j] += f[j];
-      }
-    }
-  }
-}
+constexpr int kRowsAhead = 8;  // rows in flight
 
+// scale * acc (+ old) to the row
 template <typename TO, int E, bool ADD>
-__device__ __forceinline__ void put_row(TO* row, int d, const RowPiece<E>& q, float (&f)[E], float scale) {
+__device__ __forceinline__ void put_row(TO* row, int d, const RowPiece<E>& q, const float (&acc)[E],
+                                        const Vec<TO, E>& old, float scale) {
   if (q.c < 0) return;
+  float f[E];
 #pragma unroll
-  for (int j = 0; j < E; ++j) f[j] *= scale;
+  for (int j = 0; j < E; ++j) f[j] = acc[j] * scale;
   if constexpr (ADD) {
-    Vec<TO, E> old;
     float g[E];
-    load_piece(old, row, q.c, d);
     vec_f32(old, g);
 #pragma unroll
     for (int j = 0; j < E; ++j) f[j] += g[j];
   }
   Vec<TO, E> o;
   f32_vec(o, f);
-  store_piece(row, o, q.c, ADD ? q.lo : 0, d);
+  store_piece<false>(row, o, q.c, ADD ? q.lo : 0, d);
 }
 
-template <typename TX, typename TO, int E, int U, bool ADD>
+template <typename TX, typename TO, int E, bool ADD>
 __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const GradArgs p) {
-  constexpr int TB = U == 1 ? 8 : 4;
+  constexpr int TB = kRowsAhead;
   const int lane = threadIdx.x & 63;
   const TX* const dy = static_cast<const TX*>(p.dy);
   TO* const table = static_cast<TO*>(p.table);
-  const int i0 = blockIdx.y * U * kThreads + threadIdx.x;
-  int c[U];
+  const int work = blockIdx.x;
+  if (work >= (p.runs + p.longs) * p.blocks) {  // zeros
+    const int v0 = (work - (p.runs + p.longs) * p.blocks) * p.zero_rows, rows = min(p.zero_rows, p.V - v0);
+    const int at = p.start[min(v0 + lane, p.V)], next = __shfl_down(at, 1, kWave);
+    const uint64_t empty = __ballot(lane < rows && at == next);
+    const int pieces = (p.d + E - 1) / E;
+    Vec<TO, E> z;
 #pragma unroll
-  for (int u = 0; u < U; ++u) c[u] = RowPiece<E>(i0 + u * kThreads, p.d).c;
-  int g = blockIdx.x;
-  if (g >= p.runs + p.longs) {  // zeros
-    const int v0 = (g - p.runs - p.longs) * kZeroRows, v = min(v0 + (lane & 15), p.V);
-    const int at = p.start[v], next = __shfl_down(at, 1, kWave);
-    const uint64_t empty = __ballot(at == next && lane < kZeroRows && v < p.V);
-#pragma unroll
-    for (int r = 0; r < kZeroRows; ++r) {
-      if (!(empty >> r & 1)) continue;
-      TO* row = table + (int64_t)(v0 + r) * p.d;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        Vec<TO, E> z;
-#pragma unroll
-        for (int w = 0; w < Vec<TO, E>::kWords; ++w) z.w[w] = 0;
-        if (c[u] >= 0) store_piece(row, z, c[u], 0, p.d);
-      }
+    for (int w = 0; w < Vec<TO, E>::kWords; ++w) z.w[w] = 0;
+    int r = threadIdx.x / pieces, i = threadIdx.x - r * pieces;
+    while (r < rows) {
+      if (empty >> r & 1) store_piece<false>(table + (int64_t)(v0 + r) * p.d, z, RowPiece<E>(i, p.d).c, 0, p.d);
+      for (i += kThreads; i >= pieces; i -= pieces) ++r;
     }
     return;
   }
+  const bool is_long = work >= p.runs * p.blocks;
+  const int g = (is_long ? work - p.runs * p.blocks : work) / p.blocks, y = work % p.blocks;
+  const RowPiece<E> q(y * kThreads + threadIdx.x, p.d);
   const int n = p.start[p.V];  // tokens with an id inside
-  float acc[U][E];
-  if (g < p.runs) {
+  float acc[E];
+  Vec<TX, E> v[TB];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) acc[j] = 0.0f;
+  };
+  auto load = [&](int k, int tok) __attribute__((always_inline)) {
+    if (q.c >= 0) load_piece(v[k], dy + (int64_t)tok * p.d, q.c, p.d);
+  };
+  auto add = [&](int k) __attribute__((always_inline)) {
+    float f[E];
+    vec_f32(v[k], f);
+#pragma unroll
+    for (int j = 0; j < E; ++j) acc[j] += f[j];
+  };
+  if (!is_long) {
     const int p0 = g * kRunChunk;
     if (p0 >= n) return;
     const int2 a = p.sorted[min(p0 + lane, n - 1)], b = p.sorted[min(p0 + kWave + lane, n - 1)];
@@ -343,56 +344,86 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const GradArgs
     // bit: a run starts here, or the batch has ended
     const uint64_t sa = __ballot(p0 + lane >= n || a.y != up_a);
     const uint64_t sb = __ballot(p0 + kWave + lane >= n || b.y != up_b);
-    uint64_t here = sa & ((uint64_t{1} << kRunChunk) - 1);
-    while (here != 0) {
-      const int s = __builtin_ctzll(here);
-      if (p0 + s >= n) break;
-      here &= here - 1;
-      const uint64_t later = sa & ~((uint64_t{2} << s) - 1);
-      const int e = later != 0 ? __builtin_ctzll(later) : sb != 0 ? kWave + __builtin_ctzll(sb) : 2 * kWave;
-      if (e - s > kLong) break;  // the positions of a long run reach past this chunk
-      sum_tokens<TX, E, U, TB>(dy, p.d, c, a.x, b.x, s, e, acc);
-      TO* row = table + (int64_t)lane_of(a.y, s) * p.d;
+    const uint64_t here = sa & ((uint64_t{1} << min(kRunChunk, n - p0)) - 1);
+    if (here == 0) return;
+    const int last = 63 - __builtin_clzll(here);  // the last run that starts here, and its end
+    const uint64_t later = sa & ~((uint64_t{2} << last) - 1);
+    const int e = later != 0 ? __builtin_ctzll(later) : sb != 0 ? kWave + __builtin_ctzll(sb) : 2 * kWave;
+    const int end = e - last > kLong ? last : e;  // a long run is not this kind's
+    auto starts = [&](int i) __attribute__((always_inline)) { return (i < kWave ? sa >> i : sb >> (i - kWave)) & 1; };
+    TO* row = table;
+    Vec<TO, E> old, olds[ADD ? TB : 1];
+    for (int i = __builtin_ctzll(here); i < end; i += TB) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) put_row<TO, E, ADD>(row, p.d, RowPiece<E>(i0 + u * kThreads, p.d), acc[u], p.scale);
+      for (int k = 0; k < TB; ++k) {
+        const int at = i + k;
+        if (at >= end) break;
+        load(k, at < kWave ? lane_of(a.x, at) : lane_of(b.x, at - kWave));
+        if constexpr (ADD) {
+          if (at < kRunChunk && starts(at) && q.c >= 0)
+            load_piece(olds[k], table + (int64_t)lane_of(a.y, at) * p.d, q.c, p.d);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < TB; ++k) {
+        const int at = i + k;
+        if (at >= end) break;
+        if (at < kRunChunk && starts(at)) {
+          clear();
+          row = table + (int64_t)lane_of(a.y, at) * p.d;
+          if constexpr (ADD) old = olds[k];
+        }
+        add(k);
+        if (starts(at + 1)) put_row<TO, E, ADD>(row, p.d, q, acc, old, p.scale);
+      }
     }
     return;
   }
-  g -= p.runs;
   const int p0 = g * kLong;
-  if (p0 >= n) return;
-  const int2 a = p.sorted[min(p0 + lane, n - 1)];
+  const int2 a = p.sorted[max(0, min(p0 + lane, n - 1))];
   const int used = min(kLong, n - p0);
+  int job = -1;
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    const int v = lane_of(a.y, side == 0 ? 0 : used - 1);
-    if (side == 1 && v == lane_of(a.y, 0)) return;
-    const int s = p.start[v], e = p.start[v + 1];
+    if (used <= 0) break;
+    const int id = lane_of(a.y, side == 0 ? 0 : used - 1);
+    if (side == 1 && id == lane_of(a.y, 0)) break;
+    const int s = p.start[id], e = p.start[id + 1];
     if (e - s <= kLong) continue;
-    sum_tokens<TX, E, U, TB>(dy, p.d, c, a.x, a.x, max(s - p0, 0), min(e - p0, used), acc);
-    float* part = p.part + ((int64_t)g * 2 + side) * p.d;
+    if (side == 0 && s > p0 - kLong) job = id;
+    clear();
+    const int to = min(e - p0, used);
+    for (int i = max(s - p0, 0); i < to; i += TB) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c[u] < 0) continue;
-      Vec<float, E> o;
-      f32_vec(o, acc[u]);
-      store_piece(part, o, c[u], 0, p.d);
+      for (int k = 0; k < TB; ++k) {
+        if (i + k >= to) break;
+        load(k, lane_of(a.x, i + k));
+      }
+#pragma unroll
+      for (int k = 0; k < TB; ++k) {
+        if (i + k >= to) break;
+        add(k);
+      }
     }
+    float* part = p.part + ((int64_t)g * 2 + side) * p.d;
+    Vec<float, E> o;
+    f32_vec(o, acc);
+    if (q.c >= 0) store_piece<false>(part, o, q.c, 0, p.d);
   }
+  if (y == 0 && threadIdx.x == 0) p.job[g] = job;
 }
 
-// The long run whose first whole-chunk position is this work-group's p0: its parts
+// The long run whose first position at a chunk's start is this chunk's: its parts
 // in order, a quarter of them by each of 4 waves, then the waves in order.
 template <typename TO, bool ADD>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const GradArgs p) {
   constexpr int E = 4, B = 8;
   __shared__ float s_sum[3][E][kWave];
-  const int p0 = blockIdx.x * kLong, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (p0 >= p.start[p.V]) return;
-  const int v = p.sorted[p0].y, s = p.start[v], e = p.start[v + 1];
-  if (e - s <= kLong || s <= p0 - kLong) return;
+  const int v = p.job[blockIdx.x], lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (v < 0) return;
+  const int c0 = blockIdx.x, s = p.start[v], e = p.start[v + 1];
   const RowPiece<E> q(blockIdx.y * kWave + lane, p.d);
-  const int c0 = blockIdx.x, lead = s < p0 ? 1 : 0;  // a part at the end of the chunk before
+  const int lead = s < c0 * kLong ? 1 : 0;  // a part at the end of the chunk before
   const int parts = (e - 1) / kLong - c0 + 1 + lead, per = (parts + 3) / 4;
   const int k1 = min(parts, (wave + 1) * per);
   float acc[E] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -422,25 +453,27 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const GradArgs
 #pragma unroll
     for (int j = 0; j < E; ++j) acc[j] += s_sum[w][j][lane];
   }
-  put_row<TO, E, ADD>(static_cast<TO*>(p.table) + (int64_t)v * p.d, p.d, q, acc, p.scale);
+  TO* row = static_cast<TO*>(p.table) + (int64_t)v * p.d;
+  Vec<TO, E> old;
+  if constexpr (ADD) {
+    if (q.c >= 0) load_piece(old, row, q.c, p.d);
+  }
+  put_row<TO, E, ADD>(row, p.d, q, acc, old, p.scale);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <typename TX, typename TO, int E, bool ADD>
 hipError_t grad(GradArgs a, hipStream_t s) {
-  const int pieces = (a.d + E - 1) / E;
-  const int64_t zeros = ADD ? 0 : ((int64_t)a.V + kZeroRows - 1) / kZeroRows;
-  const unsigned x = static_cast<unsigned>(a.runs + a.longs + zeros);
+  a.blocks = (a.d + E * kThreads - 1) / (E * kThreads);
+  // about 32 KB a work-group
+  a.zero_rows = static_cast<int>(std::min<int64_t>(kWave - 1, std::max<int64_t>(1, (int64_t{1} << 15) / ((int64_t)a.d * sizeof(TO)))));
+  const int64_t zeros = ADD ? 0 : ((int64_t)a.V + a.zero_rows - 1) / a.zero_rows;
+  const int64_t x = (int64_t)(a.runs + a.longs) * a.blocks + zeros;
   if (x == 0) return hipSuccess;
-  const dim3 block(kThreads);
-  auto y = [&](int u) { return static_cast<unsigned>((pieces + u * kThreads - 1) / (u * kThreads)); };
-  if (pieces <= kThreads)
-    hipLaunchKernelGGL((embedding_grad_kernel<TX, TO, E, 1, ADD>), dim3(x, y(1)), block, 0, s, a);
-  else if (pieces <= 2 * kThreads)
-    hipLaunchKernelGGL((embedding_grad_kernel<TX, TO, E, 2, ADD>), dim3(x, y(2)), block, 0, s, a);
-  else
-    hipLaunchKernelGGL((embedding_grad_kernel<TX, TO, E, 4, ADD>), dim3(x, y(4)), block, 0, s, a);
+  if (x > kMaxGroups) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(x)), block(kThreads);
+  hipLaunchKernelGGL((embedding_grad_kernel<TX, TO, E, ADD>), grid, block, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.longs == 0) return e;
   const int cols = kWave * 4;
@@ -467,7 +500,8 @@ hipError_t launch_embedding(int64_t T, int V, int d, const int32_t* ids, const v
 size_t embedding_bwd_workspace_bytes(int64_t T, int64_t V, int d) {
   if (T == 0) T = 1;
   const int64_t chunks = (T + kLong - 1) / kLong;
-  return up256(T * sizeof(int2)) + up256((V + 1) * sizeof(int)) + up256(chunks * 2 * d * sizeof(float));
+  return up256(T * sizeof(int2)) + up256((V + 1) * sizeof(int)) + up256(chunks * sizeof(int)) +
+         up256(chunks * 2 * d * sizeof(float));
 }
 
 hipError_t launch_embedding_bwd(int64_t T, int V, int d, const int32_t* ids, const void* dy, int dy_dtype, float scale,
@@ -484,12 +518,26 @@ hipError_t launch_embedding_bwd(int64_t T, int V, int d, const int32_t* ids, con
   w += up256(T * sizeof(int2));
   o.start = reinterpret_cast<int*>(w);
   w += up256((static_cast<size_t>(V) + 1) * sizeof(int));
-  hipLaunchKernelGGL(embedding_sort_kernel, dim3((V + o.span - 1) / o.span), dim3(kSortWaves * kWave),
-                     kSortWaves * o.span * sizeof(int), s, o);
+  const dim3 grid((V + o.span - 1) / o.span), block(kSortWaves * kWave);
+  const size_t lds = kSortWaves * o.span * sizeof(int);
+  if (T <= kHeldIds * kSortWaves * kWave) hipLaunchKernelGGL(embedding_sort_kernel<true>, grid, block, lds, s, o);
+  else hipLaunchKernelGGL(embedding_sort_kernel<false>, grid, block, lds, s, o);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const GradArgs a{o.sorted, o.start, dy, d_table, reinterpret_cast<float*>(w), o.T, V, d,
-                   (o.T + kRunChunk - 1) / kRunChunk, (o.T + kLong - 1) / kLong, scale};
+  GradArgs a{};
+  a.sorted = o.sorted;
+  a.start = o.start;
+  a.dy = dy;
+  a.table = d_table;
+  a.T = o.T;
+  a.V = V;
+  a.d = d;
+  a.runs = (o.T + kRunChunk - 1) / kRunChunk;
+  a.longs = (o.T + kLong - 1) / kLong;
+  a.scale = scale;
+  a.job = reinterpret_cast<int*>(w);
+  w += up256(std::max(1, a.longs) * sizeof(int));
+  a.part = reinterpret_cast<float*>(w);
   using B = uint16_t;
   const bool xb = dy_dtype == MOE_BF16, yb = d_table_dtype == MOE_BF16;
   if (xb) return yb ? grad<B, B, 8>(a, add, s) : grad<B, float, 4>(a, add, s);

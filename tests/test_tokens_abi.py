@@ -35,7 +35,7 @@ def _embed_bwd(T=4, V=8, d=8, ids=A, dy=B, yt=1, scale=1.0, table=C, tt=0, add=0
 @pytest.mark.parametrize("kw,want", SIZES + [
     (dict(d=0), INV), (dict(ids=None), INV), (dict(dy=None), INV), (dict(table=None), INV), (dict(table=B), INV),
     (dict(yt=2), INV), (dict(tt=9), INV), (dict(scale=NAN), INV), (dict(add=2), INV), (dict(ws=None), WS),
-    (dict(ws=D + 16), WS)])
+    (dict(ws=D + 16), WS), (dict(T=1 << 24, d=1025), UNS)])
 def test_embedding_backward_refusals(kw, want):
     assert _embed_bwd(**kw) == want
 
