@@ -35,9 +35,9 @@ struct Distill {
     int at[kMaxTeacher];
     int16_t next[kMaxTeacher];
     int head[NT];
-    static constexpr int kThreads = NT;
   };
   static constexpr bool kLateFactor = false;
+  static int grad_pieces(const Args& k) { return k.K <= 64 ? 2 : k.K <= 128 ? 4 : 8; }
 
   template <typename S>
   static __device__ __forceinline__ void init(S& sh, int tid) {
@@ -75,9 +75,9 @@ struct Distill {
     return {a, x[is_entry(p, k, a, tid) ? a.id : 0]};
   }
 
-  template <typename TX, int E, typename S>
+  template <typename TX, typename S>
   static __device__ __forceinline__ void share(const Logits& p, const Args& k, int64_t row, const TX* x, bool grad,
-                                               int lane, const Few<TX>& few, S& sh) {
+                                               const vocab::Owner& owner, int lane, const Few<TX>& few, S& sh) {
     float top = -FLT_MAX;
     uint64_t any = 0;
     auto note = [&](int j, const Ahead& a, TX xs) __attribute__((always_inline)) {
@@ -106,11 +106,7 @@ struct Distill {
     for (int j = lane; j < k.K; j += kWave) {
       sh.p[j] /= sum;
       const int v = sh.at[j];
-      if (grad && v >= 0) {
-        const int piece = v / E, pieces = p.V / E;
-        const int owner = piece < pieces ? piece & (S::kThreads - 1) : v - pieces * E;
-        sh.next[j] = static_cast<int16_t>(atomicExch(&sh.head[owner], j));
-      }
+      if (grad && v >= 0) sh.next[j] = static_cast<int16_t>(atomicExch(&sh.head[owner.of(v)], j));
     }
     if (lane == 0) {
       sh.counted = any != 0;
@@ -147,9 +143,9 @@ struct Distill {
 
   // An index that comes several times is stored once, with the probabilities'
   // sum in units of 2^-60, whose order does not matter.
-  template <int E, int NT, typename TD, typename S>
-  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, int lo, int hi, int tid, float m, float ks,
-                                               float kr, S& sh) {
+  template <typename TD, typename S>
+  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, const vocab::Owner&, int lo, int hi, int tid,
+                                               float m, float ks, float kr, S& sh) {
     int j = sh.head[tid];
     if (j < 0) return;
     sh.head[tid] = -1;

@@ -27,6 +27,7 @@ struct Policy {
     float x, k;
   };
   static constexpr bool kLateFactor = true;
+  static int grad_pieces(const Args&) { return 2; }
 
   template <typename S>
   static __device__ __forceinline__ void init(S&, int) {}
@@ -45,9 +46,9 @@ struct Policy {
     const int tok = vocab::scalar_of(k.tok + row);
     return {tok, vocab::scalar_logit(x, tok)};
   }
-  template <typename TX, int E, typename S>
-  static __device__ __forceinline__ void share(const Logits&, const Args&, int64_t, const TX*, bool, int lane,
-                                               const Few<TX>& few, S& sh) {
+  template <typename TX, typename S>
+  static __device__ __forceinline__ void share(const Logits&, const Args&, int64_t, const TX*, bool,
+                                               const vocab::Owner&, int lane, const Few<TX>& few, S& sh) {
     if (lane != 0) return;
     sh.tok = few.tok;
     sh.x = few.x;
@@ -99,12 +100,11 @@ struct Policy {
     return sh.k;
   }
 
-  template <int E, int NT, typename TD, typename S>
-  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, int lo, int hi, int tid, float m, float ks,
-                                               float kr, S& sh) {
-    const int v = sh.tok, piece = v / E, pieces = p.V / E;
-    const int owner = piece < pieces ? piece & (NT - 1) : v - pieces * E;
-    if (tid != owner || v < lo || v >= hi || kr == 0.0f) return;
+  template <typename TD, typename S>
+  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, const vocab::Owner& owner, int lo, int hi,
+                                               int tid, float m, float ks, float kr, S& sh) {
+    const int v = sh.tok;
+    if (tid != owner.of(v) || v < lo || v >= hi || kr == 0.0f) return;
     put_one(dx + v, ks * exp2_of((sh.x - m) * p.c) - kr);
   }
 

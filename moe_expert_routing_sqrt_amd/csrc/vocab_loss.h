@@ -122,6 +122,23 @@ __device__ __forceinline__ int64_t fresh(int64_t v) {
   return v;
 }
 
+// The thread that stores a logit's gradient.  Pieces below `held` lie in stretches
+// of `per` times 64, one a wave; the others, and with held = 0 all, go round the nt
+// threads; the logits behind the last piece are one a thread.
+struct Owner {
+  int pieces, e, nt, per, held;
+  static __host__ __device__ __forceinline__ int blocks(int pieces, int waves) {
+    const int b = (pieces + kWave * waves - 1) / (kWave * waves);
+    return b > 0 ? b : 1;
+  }
+  __device__ __forceinline__ int of(int v) const {
+    const int piece = v / e;
+    if (piece >= pieces) return v - pieces * e;
+    if (piece < held) return piece / kWave / per * kWave + piece % kWave;
+    return (piece - held) & (nt - 1);
+  }
+};
+
 // Barrier of a row's threads (NT = 64: the wave, whose LDS accesses keep their
 // order).
 template <int NT>
@@ -156,7 +173,7 @@ constexpr int kGroup = NT < kBlock ? kBlock : NT;
 // use waits for a vector load.
 // waves a SIMD holds, by the registers a piece takes
 template <int NT, int NC>
-constexpr int kWaves = NC > 8 ? 4 : NC > 4 && NT < 1024 ? 5 : 8;
+constexpr int kWaves = NC > 8 ? 4 : NC > 4 ? 5 : NC > 2 ? 6 : 8;
 template <typename KIND, typename TX, typename TD, int NT, int NC, bool MORE, bool GRAD>
 __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(const Logits p, const typename KIND::Args k) {
   constexpr int E = kPiece<TX>, WAVES = NT / kWave;
@@ -167,6 +184,9 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int V = p.V, pieces = V / E, tail = V % E;  // the last V % E logits: one a thread
+  // A wave holds `per` times 64 consecutive pieces: one stretch of memory (strided
+  // over the waves: 412 and 418 us where this takes 397 and 385).
+  const int per = MORE ? NC : Owner::blocks(pieces, WAVES);
   const int64_t step = (int64_t)gridDim.x * kTeams<NT>;
   int64_t row = (int64_t)blockIdx.x * kTeams<NT> + team;
   if (row >= p.rows) return;  // whole teams; no barrier where a work-group has several
@@ -175,6 +195,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
   team_sync<NT>();
   const float g = p.grad != nullptr ? scalar_of(p.grad) : 1.0f;
 
+  const Owner owner{pieces, E, NT, per, NC * NT};
   const float c = p.c;
   const TX* const x0 = static_cast<const TX*>(p.x);
   Vec<TX, E> h[NC > 0 ? NC : 1];
@@ -184,7 +205,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
   // it ends): what a row has no piece for, and every piece of a row that is not
   // read, loads one that is there.
   auto fetch = [&](int i, const TX* x, bool read) __attribute__((always_inline)) {
-    load_at<true>(h[i], x, min(i * NT + ft, read ? pieces - 1 : 0));
+    load_at<true>(h[i], x, min((wave * per + min(i, per - 1)) * kWave + (ft & 63), read ? pieces - 1 : 0));
   };
   auto fetch_tail = [&](const TX* x) __attribute__((always_inline)) {
     t = *at_byte(x, static_cast<uint32_t>(min(pieces * E + ft, V - 1)) * static_cast<uint32_t>(sizeof(TX)));
@@ -228,7 +249,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
     constexpr int G = NC < kTogether ? (NC > 0 ? NC : 1) : kTogether;
 #pragma unroll
     for (int i0 = 0; i0 < NC; i0 += G) {
-      if (live && i0 * NT < pieces) {
+      if (live && i0 < per) {
         float m1 = m, s2 = 0.0f;
 #pragma unroll
         for (int i = i0; i < i0 + G; ++i) {
@@ -243,7 +264,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
           vec_f32(h[i], f);
 #pragma unroll
           for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m1) * c);
-          s2 += i * NT + ft < pieces ? s1 : 0.0f;
+          s2 += i < per && (wave * per + i) * kWave + (ft & 63) < pieces ? s1 : 0.0f;
         }
         sum = sum * exp2_of((m - m1) * c) + s2;
         m = m1;
@@ -283,7 +304,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
           s_red[turn][1][wave] = sum;
         }
       }
-      if (wave == 0) KIND::template share<TX, E>(p, k, row, x, GRAD, ft, few, sh);
+      if (wave == 0) KIND::template share<TX>(p, k, row, x, GRAD, owner, ft, few, sh);
       team_sync<NT>();
       if constexpr (WAVES > 1) {
         const float m1 = s_red[turn][0][ft & 15];
@@ -306,14 +327,15 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         pin(h[i]);
-        if (i * NT < pieces && kr != 0.0f) {
+        if (i < per && kr != 0.0f) {
           float f[E];
           vec_f32(h[i], f);
 #pragma unroll
           for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
           Vec<TD, E> o;
           f32_vec(o, f);
-          if (i * NT + ft < pieces) store_at(dx, o, i * NT + ft);
+          const int at = (wave * per + i) * kWave + (ft & 63);
+          if (at < pieces) store_at(dx, o, at);
         }
         fetch(i, xn, live_next);
       }
@@ -335,7 +357,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
         }
       }
       // (a thread's stores to one place keep their order)
-      if (live) KIND::template patch<E, NT>(p, dx, 0, V, ft, m, ks, kr, sh);
+      if (live) KIND::patch(p, dx, owner, 0, V, ft, m, ks, kr, sh);
     }
     if (live) {
       if constexpr (COPIES > 1) turn ^= 1;
@@ -349,16 +371,18 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
 
 // The gradient from the logits and the forward's statistics: a work-group has
 // `span` pieces of a row, a multiple of NT (NT = 64: a wave has them).
-constexpr int kGradAhead = 4;
+template <int NT>
+constexpr int kGradAhead = NT > kWave ? 2 : 4;
 template <typename KIND, typename TX, typename TD, int NT>
 __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, const typename KIND::Args k, int splits,
                                                              int span, int64_t units) {
-  constexpr int E = kPiece<TX>, U = kGradAhead;
+  constexpr int E = kPiece<TX>, U = kGradAhead<NT>;
   __shared__ typename KIND::template Shared<NT> s_kind[kTeams<NT>];
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int V = p.V, pieces = V / E, tail = V % E;
   const float g = p.grad != nullptr ? scalar_of(p.grad) : 1.0f, c = p.c;
+  const Owner owner{pieces, E, NT, 1, 0};
   auto& sh = s_kind[team];
   for (int64_t unit = (int64_t)blockIdx.x * kTeams<NT> + team; unit < units; unit += (int64_t)gridDim.x * kTeams<NT>) {
     const int64_t row = unit / splits;
@@ -374,7 +398,8 @@ __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, con
       m = scalar_of(p.stats + 2 * row);
       const float sum = scalar_of(p.stats + 2 * row + 1);
       if (wave == 0) {
-        KIND::template share<TX, E>(p, k, row, x, true, lane, KIND::template begin<TX>(p, k, row, x, lane, KIND::ahead(k, row, lane)), sh);
+        KIND::template share<TX>(p, k, row, x, true, owner, lane,
+                                 KIND::template begin<TX>(p, k, row, x, lane, KIND::ahead(k, row, lane)), sh);
         if constexpr (KIND::kLateFactor) KIND::finish(p, k, row, g * w, m, sum, lane, sh, false);
       }
       team_sync<NT>();
@@ -391,7 +416,7 @@ __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, con
       for (int i0 = first + tid; i0 < last; i0 += U * NT) {
         Vec<TX, E> v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) load_at<false>(v[u], x, min(i0 + u * NT, last - 1));
+        for (int u = 0; u < U; ++u) load_at<true>(v[u], x, min(i0 + u * NT, last - 1));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           float f[E];
@@ -407,7 +432,7 @@ __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, con
         const int64_t at = (int64_t)pieces * E + tid;
         put_one(dx + at, ks * exp2_of((one_f32(x[at]) - m) * c));
       }
-      KIND::template patch<E, NT>(p, dx, first * E, ends ? V : last * E, tid, m, ks, kr, sh);
+      KIND::patch(p, dx, owner, first * E, ends ? V : last * E, tid, m, ks, kr, sh);
     }
     team_sync<NT>();  // Shared is free again
   }
@@ -441,8 +466,12 @@ hipError_t loss_rows(const Logits& p, const typename KIND::Args& k, hipStream_t 
 
 template <typename KIND, typename TX, typename TD, int NT>
 hipError_t run_grad(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
-  // 8 pieces a thread
-  const int pieces = p.V / kPiece<TX>, span = 8 * NT, splits = pieces <= span ? 1 : (pieces + span - 1) / span;
+  // A wave has its row.  4 waves have 2 pieces a thread, so that what runs at the
+  // same time lies side by side in memory (1500 x 50001 fp32: 98 us, 112 with 8
+  // pieces; 2048 x 100003: 191 and 236); more where every work-group has many entries
+  // to look up first.
+  const int pieces = p.V / kPiece<TX>, span = (NT > kWave ? KIND::grad_pieces(k) : 8) * NT;
+  const int splits = pieces <= span ? 1 : (pieces + span - 1) / span;
   const int64_t units = p.rows * splits, groups = (units + kTeams<NT> - 1) / kTeams<NT>;
   const dim3 grid(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20)), block(kGroup<NT>);
   hipLaunchKernelGGL((grad_kernel<KIND, TX, TD, NT>), grid, block, 0, s, p, k, splits, span, units);
