@@ -30,6 +30,7 @@ struct Distill {
     int counted;
     float sum;              // of the teacher's exponentials
     float p[kMaxTeacher];   // probability (0: no entry)
+    float w[kMaxTeacher];   // with that of the same index's other entries
     float u[kMaxTeacher];   // teacher's logit less the largest
     float x[kMaxTeacher];   // the student's logit
     int at[kMaxTeacher];
@@ -78,23 +79,41 @@ struct Distill {
   template <typename TX, typename S>
   static __device__ __forceinline__ void share(const Logits& p, const Args& k, int64_t row, const TX* x, bool grad,
                                                const vocab::Owner& owner, int lane, const Few<TX>& few, S& sh) {
-    float top = -FLT_MAX;
-    uint64_t any = 0;
-    auto note = [&](int j, const Ahead& a, TX xs) __attribute__((always_inline)) {
-      const bool ok = is_entry(p, k, a, j);
-      any |= __ballot(ok);
-      if (ok) top = fmaxf(top, a.t);
-      if (j >= k.K) return;
-      sh.at[j] = ok ? a.id : -1;
-      sh.u[j] = a.t;
-      sh.x[j] = one_f32(xs);
-    };
-    note(lane, few.a, few.x);
-    for (int j0 = kWave; j0 < k.K; j0 += kWave) {
-      const Ahead a = entry(k, row, j0 + lane);
-      note(j0 + lane, a, x[is_entry(p, k, a, j0 + lane) ? a.id : 0]);
+    const bool ok = is_entry(p, k, few.a, lane);
+    const int v = ok ? few.a.id : -1;
+    uint64_t any = __ballot(ok);
+    float top = ok ? few.a.t : -FLT_MAX, sum;
+    if (k.K <= kWave) {  // all in this lane's registers
+      top = wave_max(top);
+      const float u = few.a.t - top, e = ok ? exp2_of(u * p.c) : 0.0f;
+      sum = wave_sum(e);
+      if (lane < k.K) {
+        sh.u[lane] = u;
+        sh.x[lane] = one_f32(few.x);
+        enter(sh, owner, lane, v, e / sum, grad);
+      }
+    } else {
+      for (int j = lane; j < k.K; j += kWave) {
+        const Ahead a = j < kWave ? few.a : entry(k, row, j);
+        const bool in = is_entry(p, k, a, j);
+        sh.at[j] = in ? a.id : -1;
+        sh.u[j] = a.t;
+        sh.x[j] = one_f32(j < kWave ? few.x : x[in ? a.id : 0]);
+        if (in) top = fmaxf(top, a.t);
+        any |= __ballot(in);
+      }
+      top = wave_max(top);
+      sum = weigh(p, k, top, lane, sh);
+      for (int j = lane; j < k.K; j += kWave) enter(sh, owner, j, sh.at[j], sh.p[j] / sum, grad);
     }
-    top = wave_max(top);
+    if (lane == 0) {
+      sh.counted = any != 0;
+      sh.sum = sum;
+    }
+  }
+  // u and the exponentials' sum from the logits in u, by one wave
+  template <typename S>
+  static __device__ __forceinline__ float weigh(const Logits& p, const Args& k, float top, int lane, S& sh) {
     float sum = 0.0f;
     for (int j = lane; j < k.K; j += kWave) {
       const float u = sh.u[j] - top, e = sh.at[j] >= 0 ? exp2_of(u * p.c) : 0.0f;
@@ -102,16 +121,46 @@ struct Distill {
       sh.p[j] = e;
       sum += e;
     }
-    sum = wave_sum(sum);
-    for (int j = lane; j < k.K; j += kWave) {
-      sh.p[j] /= sum;
-      const int v = sh.at[j];
-      if (grad && v >= 0) sh.next[j] = static_cast<int16_t>(atomicExch(&sh.head[owner.of(v)], j));
+    return wave_sum(sum);
+  }
+  // entry j, and where its gradient is wanted on the list of the thread that stores it
+  template <typename S>
+  static __device__ __forceinline__ void enter(S& sh, const vocab::Owner& owner, int j, int v, float pj, bool list) {
+    sh.at[j] = v;
+    sh.p[j] = pj;
+    if (list && v >= 0) sh.next[j] = static_cast<int16_t>(atomicExch(&sh.head[owner.of(v)], j));
+  }
+
+  // for the gradient alone: the probabilities, and the entries among [lo, hi)
+  template <typename TX, typename S>
+  static __device__ __forceinline__ void entries(const Logits& p, const Args& k, int64_t row, const TX*,
+                                                 const vocab::Owner& owner, int lo, int hi, int lane, S& sh) {
+    Ahead a = entry(k, row, lane);
+    bool ok = is_entry(p, k, a, lane);
+    uint64_t any = __ballot(ok);
+    float top = ok ? a.t : -FLT_MAX, sum;
+    if (k.K <= kWave) {
+      top = wave_max(top);
+      const float e = ok ? exp2_of((a.t - top) * p.c) : 0.0f;
+      sum = wave_sum(e);
+      if (lane < k.K) enter(sh, owner, lane, a.id, e / sum, ok && a.id >= lo && a.id < hi);
+    } else {
+      for (int j = lane; j < k.K; j += kWave) {
+        if (j >= kWave) a = entry(k, row, j);
+        ok = is_entry(p, k, a, j);
+        sh.at[j] = ok ? a.id : -1;
+        sh.u[j] = a.t;
+        if (ok) top = fmaxf(top, a.t);
+        any |= __ballot(ok);
+      }
+      top = wave_max(top);
+      sum = weigh(p, k, top, lane, sh);
+      for (int j = lane; j < k.K; j += kWave) {
+        const int v = sh.at[j];
+        enter(sh, owner, j, v, sh.p[j] / sum, v >= lo && v < hi);
+      }
     }
-    if (lane == 0) {
-      sh.counted = any != 0;
-      sh.sum = sum;
-    }
+    if (lane == 0) sh.counted = any != 0;
   }
 
   template <typename S>
@@ -141,28 +190,70 @@ struct Distill {
     return sh.counted ? gw * static_cast<float>(p.tau) : 0.0f;
   }
 
-  // An index that comes several times is stored once, with the probabilities'
-  // sum in units of 2^-60, whose order does not matter.
-  template <typename TD, typename S>
-  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, const vocab::Owner&, int lo, int hi, int tid,
-                                               float m, float ks, float kr, S& sh) {
-    int j = sh.head[tid];
-    if (j < 0) return;
-    sh.head[tid] = -1;
-    for (; j >= 0; j = sh.next[j]) {
+  // A thread's list: its first entry in registers, the pieces that the others are in.
+  struct Mine {
+    int v, rest;
+    float w;
+    uint32_t mask;
+  };
+  template <typename S>
+  static __device__ __forceinline__ Mine mine(const vocab::Owner& owner, S& sh, int tid, bool any) {
+    Mine my{-1, -1, 0.0f, 0};
+    const int j0 = any ? sh.head[tid] : -1;
+    if (j0 < 0) return my;
+    my.v = sh.at[j0];
+    my.rest = sh.next[j0];
+    my.w = sh.p[j0];
+    if (my.rest < 0) return my;
+    // An index that comes several times is taken once, its probabilities summed in
+    // units of 2^-60: their order, which is not that of the entries, does not matter.
+    for (int j = j0; j >= 0; j = sh.next[j]) {
       const int v = sh.at[j];
-      if (v < lo || v >= hi || kr == 0.0f) continue;
-      float pj = sh.p[j];
+      if (v < 0) continue;
+      float w = sh.p[j];
       uint64_t units = 0;
       for (int i = sh.next[j]; i >= 0; i = sh.next[i]) {
         if (sh.at[i] != v) continue;
-        if (units == 0) units = in_units(pj);
+        if (units == 0) units = in_units(w);
         units += in_units(sh.p[i]);
         sh.at[i] = -1;
       }
-      if (units != 0 && pj == pj) pj = static_cast<float>(units) * 0x1p-60f;  // (NaN stays)
-      put_one(dx + v, ks * exp2_of((sh.x[j] - m) * p.c) - kr * pj);
+      if (units != 0 && w == w) w = static_cast<float>(units) * 0x1p-60f;  // (NaN stays)
+      sh.w[j] = w;
+      if (j == j0) {
+        my.w = w;
+        continue;
+      }
+      const int piece = v / owner.e;
+      my.mask |= 1u << (piece < owner.pieces ? min(owner.local(piece), vocab::kManyPieces) : vocab::kManyPieces);
     }
+    return my;
+  }
+  template <int E, typename S>
+  static __device__ __forceinline__ void correct(S& sh, const Mine& my, int local, int piece, float kr, int,
+                                                 float (&f)[E]) {
+    auto take = [&](int v, float w) __attribute__((always_inline)) {
+      const int i = v - piece * E;
+      if (static_cast<unsigned>(i) >= static_cast<unsigned>(E)) return;
+      const float less = kr * w;
+#pragma unroll
+      for (int l = 0; l < E; ++l) f[l] -= l == i ? less : 0.0f;
+    };
+    take(my.v, my.w);
+    if ((my.mask >> min(local, vocab::kManyPieces) & 1) == 0) return;
+    for (int j = my.rest; j >= 0; j = sh.next[j]) take(sh.at[j], sh.w[j]);
+  }
+  template <typename S>
+  static __device__ __forceinline__ float correct_one(S& sh, const Mine& my, int at, float kr, int, float f) {
+    if (my.v == at) f -= kr * my.w;
+    if (my.mask >> vocab::kManyPieces == 0) return f;
+    for (int j = my.rest; j >= 0; j = sh.next[j])
+      if (sh.at[j] == at) f -= kr * sh.w[j];
+    return f;
+  }
+  template <typename S>
+  static __device__ __forceinline__ void done(S& sh, int tid) {
+    sh.head[tid] = -1;
   }
   static __device__ __forceinline__ uint64_t in_units(float v) { return static_cast<uint64_t>(v * 0x1p60f); }
 

@@ -100,13 +100,29 @@ struct Policy {
     return sh.k;
   }
 
-  template <typename TD, typename S>
-  static __device__ __forceinline__ void patch(const Logits& p, TD* dx, const vocab::Owner& owner, int lo, int hi,
-                                               int tid, float m, float ks, float kr, S& sh) {
-    const int v = sh.tok;
-    if (tid != owner.of(v) || v < lo || v >= hi || kr == 0.0f) return;
-    put_one(dx + v, ks * exp2_of((sh.x - m) * p.c) - kr);
+  template <typename TX, typename S>
+  static __device__ __forceinline__ void entries(const Logits& p, const Args& k, int64_t row, const TX* x,
+                                                 const vocab::Owner& owner, int, int, int lane, S& sh) {
+    share<TX>(p, k, row, x, true, owner, lane, begin<TX>(p, k, row, x, lane, {}), sh);
   }
+  // the token
+  template <typename S>
+  static __device__ __forceinline__ int mine(const vocab::Owner&, const S& sh, int, bool any) {
+    return any ? sh.tok : -1;
+  }
+  template <int E, typename S>
+  static __device__ __forceinline__ void correct(S&, int tok, int, int piece, float kr, int, float (&f)[E]) {
+    const int i = tok - piece * E;
+    if (i < 0 || i >= E) return;
+#pragma unroll
+    for (int l = 0; l < E; ++l) f[l] = l == i ? f[l] - kr : f[l];
+  }
+  template <typename S>
+  static __device__ __forceinline__ float correct_one(S&, int tok, int at, float kr, int, float f) {
+    return tok == at ? f - kr : f;
+  }
+  template <typename S>
+  static __device__ __forceinline__ void done(S&, int) {}
 
   static __device__ __forceinline__ void none(const Logits& p, const Args& k, int64_t row) {
     p.stats[2 * row] = p.stats[2 * row + 1] = k.logp[row] = 0.0f;

@@ -15,7 +15,10 @@
 //   share        wave 0 of the row, after its sums: the row's entries into Shared
 //   finish       wave 0, with the row's maximum and sum: statistics, loss, k
 //   factor       k, every thread (after finish where kLateFactor, else after share)
-//   patch        every thread: the entries among the logits it stored, again
+//   mine         every thread: which of its pieces hold entries
+//   correct      the gradient of a piece that does: less k p_j at its entries
+//   correct_one  the same for one of the last V % E logits
+//   done         every thread: Shared as init left it
 //   none         one thread: the outputs of a row that does not count
 //
 // exp is 2^((x - max) log2(e)/tau): the difference first, so that its relative
@@ -125,6 +128,7 @@ __device__ __forceinline__ int64_t fresh(int64_t v) {
 // The thread that stores a logit's gradient.  Pieces below `held` lie in stretches
 // of `per` times 64, one a wave; the others, and with held = 0 all, go round the nt
 // threads; the logits behind the last piece are one a thread.
+// `local`: which of the thread's pieces it is.
 struct Owner {
   int pieces, e, nt, per, held;
   static __host__ __device__ __forceinline__ int blocks(int pieces, int waves) {
@@ -137,7 +141,11 @@ struct Owner {
     if (piece < held) return piece / kWave / per * kWave + piece % kWave;
     return (piece - held) & (nt - 1);
   }
+  __device__ __forceinline__ int local(int piece) const {
+    return piece < held ? piece / kWave % per : held / nt + (piece - held) / nt;
+  }
 };
+constexpr int kManyPieces = 31;  // a thread's pieces from the 31st on share the last bit of a mask
 
 // Barrier of a row's threads (NT = 64: the wave, whose LDS accesses keep their
 // order).
@@ -172,10 +180,10 @@ constexpr int kGroup = NT < kBlock ? kBlock : NT;
 // is busy while a row is reduced; nothing between that and the next row's first
 // use waits for a vector load.
 // waves a SIMD holds, by the registers a piece takes
-template <int NT, int NC>
-constexpr int kWaves = NC > 8 ? 4 : NC > 4 ? 5 : NC > 2 ? 6 : 8;
+template <int NC>
+constexpr int kWaves = NC > 8 ? 4 : NC > 4 ? 5 : 6;
 template <typename KIND, typename TX, typename TD, int NT, int NC, bool MORE, bool GRAD>
-__global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(const Logits p, const typename KIND::Args k) {
+__global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logits p, const typename KIND::Args k) {
   constexpr int E = kPiece<TX>, WAVES = NT / kWave;
   // two copies by turns where a wave may be a row ahead of another
   constexpr int COPIES = WAVES > 1 ? 2 : 1;
@@ -324,6 +332,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
     if constexpr (GRAD) {
       // k = 0: zeros, also where the logits hold anything
       if (kr == 0.0f) zero_row();
+      const auto mine = KIND::mine(owner, sh, ft, kr != 0.0f);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         pin(h[i]);
@@ -332,14 +341,16 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
           vec_f32(h[i], f);
 #pragma unroll
           for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          const int at = (wave * per + i) * kWave + (ft & 63);
+          KIND::correct(sh, mine, i, at, kr, ft, f);
           Vec<TD, E> o;
           f32_vec(o, f);
-          const int at = (wave * per + i) * kWave + (ft & 63);
           if (at < pieces) store_at(dx, o, at);
         }
         fetch(i, xn, live_next);
       }
-      if (kr != 0.0f) tail_out(ks * exp2_of((tv - m) * c));
+      if (kr != 0.0f && ft < tail)
+        tail_out(KIND::correct_one(sh, mine, pieces * E + ft, kr, ft, ks * exp2_of((tv - m) * c)));
       fetch_tail(xn);
       for (int i0 = MORE && kr != 0.0f ? NC * NT + ft : pieces; i0 < pieces; i0 += U * NT) {
         Vec<TX, E> v[U];
@@ -351,15 +362,15 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
           vec_f32(v[u], f);
 #pragma unroll
           for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          KIND::correct(sh, mine, owner.local(i0 + u * NT), i0 + u * NT, kr, ft, f);
           Vec<TD, E> o;
           f32_vec(o, f);
           if (i0 + u * NT < pieces) store_at(dx, o, i0 + u * NT);
         }
       }
-      // (a thread's stores to one place keep their order)
-      if (live) KIND::patch(p, dx, owner, 0, V, ft, m, ks, kr, sh);
     }
     if (live) {
+      if constexpr (GRAD) KIND::done(sh, ft);
       if constexpr (COPIES > 1) turn ^= 1;
       else team_sync<NT>();
     }
@@ -374,7 +385,7 @@ __global__ __launch_bounds__(kGroup<NT>, (kWaves<NT, NC>)) void loss_kernel(cons
 template <int NT>
 constexpr int kGradAhead = NT > kWave ? 2 : 4;
 template <typename KIND, typename TX, typename TD, int NT>
-__global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, const typename KIND::Args k, int splits,
+__global__ __launch_bounds__(kGroup<NT>, (NT > kWave ? 6 : 5)) void grad_kernel(const Logits p, const typename KIND::Args k, int splits,
                                                              int span, int64_t units) {
   constexpr int E = kPiece<TX>, U = kGradAhead<NT>;
   __shared__ typename KIND::template Shared<NT> s_kind[kTeams<NT>];
@@ -391,48 +402,53 @@ __global__ __launch_bounds__(kGroup<NT>, 8) void grad_kernel(const Logits p, con
     TD* const dx = static_cast<TD*>(p.dx) + row * V;
     const bool ends = part == splits - 1, one = ends && tid < tail;
     const float w = weight_of(p, row);
+    const bool live = w != 0.0f && KIND::live(k, row, V);
     float kr = 0.0f, m = 0.0f, ks = 0.0f;
-    if (w != 0.0f && KIND::live(k, row, V)) {
+    Vec<TX, E> v[U];
+    auto fetch = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_at<true>(v[u], x, max(0, min(i0 + u * NT, last - 1)));
+    };
+    if (live) {
+      if (pieces > 0) fetch(first + tid);  // in flight while the row's entries are looked up
       KIND::init(sh, tid);
       team_sync<NT>();
       m = scalar_of(p.stats + 2 * row);
       const float sum = scalar_of(p.stats + 2 * row + 1);
       if (wave == 0) {
-        KIND::template share<TX>(p, k, row, x, true, owner, lane,
-                                 KIND::template begin<TX>(p, k, row, x, lane, KIND::ahead(k, row, lane)), sh);
+        KIND::template entries<TX>(p, k, row, x, owner, first * E, ends ? V : last * E, lane, sh);
         if constexpr (KIND::kLateFactor) KIND::finish(p, k, row, g * w, m, sum, lane, sh, false);
       }
       team_sync<NT>();
       kr = uniform(KIND::factor(p, g * w, sh));
       ks = kr / sum;
     }
-    if (kr == 0.0f) {  // nothing to read
+    if (kr == 0.0f) {  // zeros, also where the logits hold anything
       Vec<TD, E> z;
 #pragma unroll
       for (int i = 0; i < Vec<TD, E>::kWords; ++i) z.w[i] = 0;
       for (int i = first + tid; i < last; i += NT) store_at(dx, z, i);
       if (one) put_one(dx + (int64_t)pieces * E + tid, 0.0f);
     } else {
+      const auto mine = KIND::mine(owner, sh, tid, true);
       for (int i0 = first + tid; i0 < last; i0 += U * NT) {
-        Vec<TX, E> v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) load_at<true>(v[u], x, min(i0 + u * NT, last - 1));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           float f[E];
           vec_f32(v[u], f);
 #pragma unroll
           for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          KIND::correct(sh, mine, owner.local(i0 + u * NT), i0 + u * NT, kr, tid, f);
           Vec<TD, E> o;
           f32_vec(o, f);
           if (i0 + u * NT < last) store_at(dx, o, i0 + u * NT);
         }
+        if (i0 + U * NT < last) fetch(i0 + U * NT);
       }
       if (one) {
         const int64_t at = (int64_t)pieces * E + tid;
-        put_one(dx + at, ks * exp2_of((one_f32(x[at]) - m) * c));
+        put_one(dx + at, KIND::correct_one(sh, mine, static_cast<int>(at), kr, tid, ks * exp2_of((one_f32(x[at]) - m) * c)));
       }
-      KIND::patch(p, dx, owner, first * E, ends ? V : last * E, tid, m, ks, kr, sh);
     }
     team_sync<NT>();  // Shared is free again
   }
@@ -445,7 +461,7 @@ template <typename KIND, typename TX, typename TD, int NT, int NC, bool MORE, bo
 hipError_t run_loss(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
   const int64_t need = (p.rows + kTeams<NT> - 1) / kTeams<NT>;
   // the work-groups the chip holds at once
-  const int64_t held = (int64_t)stream_cu_count(s) * 4 * kWaves<NT, NC> * kWave / kGroup<NT>;
+  const int64_t held = (int64_t)stream_cu_count(s) * 4 * kWaves<NC> * kWave / kGroup<NT>;
   const dim3 grid(static_cast<unsigned>(need < held ? need : held)), block(kGroup<NT>);
   hipLaunchKernelGGL((loss_kernel<KIND, TX, TD, NT, NC, MORE, GRAD>), grid, block, 0, s, p, k);
   return hipGetLastError();
@@ -453,13 +469,19 @@ hipError_t run_loss(const Logits& p, const typename KIND::Args& k, hipStream_t s
 
 template <typename KIND, typename TX, typename TD, bool GRAD>
 hipError_t loss_rows(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
+  // the fewest registers that hold a row, of the fewest waves
   const int pieces = p.V / kPiece<TX>;
   if (pieces == 0) return run_loss<KIND, TX, TD, 64, 0, false, GRAD>(p, k, s);
   if (pieces <= 2 * 64) return run_loss<KIND, TX, TD, 64, 2, false, GRAD>(p, k, s);
+  if (pieces <= 4 * 64) return run_loss<KIND, TX, TD, 64, 4, false, GRAD>(p, k, s);
   if (pieces <= 8 * 64) return run_loss<KIND, TX, TD, 64, 8, false, GRAD>(p, k, s);
   if (pieces <= 4 * 256) return run_loss<KIND, TX, TD, 256, 4, false, GRAD>(p, k, s);
+  if (pieces <= 8 * 256) return run_loss<KIND, TX, TD, 256, 8, false, GRAD>(p, k, s);
+  if (pieces <= 12 * 256) return run_loss<KIND, TX, TD, 256, 12, false, GRAD>(p, k, s);
   if (pieces <= 16 * 256) return run_loss<KIND, TX, TD, 256, 16, false, GRAD>(p, k, s);
+  if (pieces <= 12 * 512) return run_loss<KIND, TX, TD, 512, 12, false, GRAD>(p, k, s);
   if (pieces <= 16 * 512) return run_loss<KIND, TX, TD, 512, 16, false, GRAD>(p, k, s);
+  if (pieces <= 12 * 1024) return run_loss<KIND, TX, TD, 1024, 12, false, GRAD>(p, k, s);
   if (pieces <= 16 * 1024) return run_loss<KIND, TX, TD, 1024, 16, false, GRAD>(p, k, s);
   return run_loss<KIND, TX, TD, 1024, 12, true, GRAD>(p, k, s);
 }
