@@ -23,6 +23,7 @@ library is missing, or a tensor is not on the GPU, calls raise.
     distill_loss(logits, idx, teacher)       -> loss, row_loss, stats, dlogits; distill_loss_backward -> dlogits
     policy_loss(logits, tokens, old_logp, advantage) -> loss, row_loss, logp, stats, dlogits;
                                              policy_loss_backward -> dlogits; token_logp -> logp, stats
+    TokenModel                               embedding + MoEBlock + norm + tied head: a training step on token ids
 """
 from __future__ import annotations
 
@@ -45,7 +46,7 @@ __all__ = ["shape", "workspace_bytes", "workspace", "route", "route_hash", "disp
            "quantize_blocks_e4m3", "quantize_rows_e4m3", "bias_update", "MoELayer", "MoeError", "lib",
            "layer_norm", "layer_norm_backward", "balance_loss", "balance_loss_backward", "AdamW", "MoEBlock",
            "embedding", "embedding_backward", "distill_loss", "distill_loss_backward", "policy_loss",
-           "policy_loss_backward", "token_logp"]
+           "policy_loss_backward", "token_logp", "TokenModel"]
 
 
 def lib():
@@ -514,5 +515,5 @@ def bias_update(counts: torch.Tensor, bias: torch.Tensor, gamma: float,
 from .layer import MoELayer  # noqa: E402
 from .training import (AdamW, MoEBlock, balance_loss, balance_loss_backward, layer_norm,  # noqa: E402
                        layer_norm_backward)
-from .tokens import (distill_loss, distill_loss_backward, embedding, embedding_backward, policy_loss,  # noqa: E402
-                     policy_loss_backward, token_logp)
+from .tokens import (TokenModel, distill_loss, distill_loss_backward, embedding, embedding_backward,  # noqa: E402
+                     policy_loss, policy_loss_backward, token_logp)

@@ -1,7 +1,7 @@
 """The two ends of a training step on tokens: the embedding lookup with its
 gradient, and losses on a vocabulary's logits with theirs (distillation from a
 teacher's top logits, the clipped policy loss with a KL term), each one call into
-the library."""
+the library; and TokenModel, which runs them around a MoEBlock."""
 from __future__ import annotations
 
 import ctypes
@@ -10,7 +10,8 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import MOE_F32, _device_index, _dt, _lib, _stream, _ws_len, lib
+from . import MOE_F32, MOE_OP_LAYER_NORM_BACKWARD, _device_index, _dt, _lib, _stream, _ws_len, lib, workspace_bytes
+from .training import AdamW, MoEBlock, layer_norm, layer_norm_backward
 from .training import _arg as _sized
 
 _f32, _i32 = torch.float32, torch.int32
@@ -19,10 +20,14 @@ _f32, _i32 = torch.float32, torch.int32
 def _arg(t: Optional[torch.Tensor], numel: int, name: str, dtype: Optional[torch.dtype] = None) -> int:
     """The pointer of a tensor argument (0 for None): its size, type and layout are
     checked, and that it lives on the current device, whose stream the call uses."""
-    p = _sized(t, numel, name, dtype)
-    if t is not None and _device_index is not None and t.get_device() != _device_index():
+    if t is None:
+        return 0
+    on = t.get_device()
+    if (dtype is None or t.dtype is dtype) and on >= 0 and t.numel() >= numel and t.is_contiguous():
+        if _device_index is None or on == _device_index():
+            return t.data_ptr()
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device_index()}")
-    return p
+    return _sized(t, numel, name, dtype)  # raises
 
 
 # ---------------------------------------------------------------- embedding
@@ -85,19 +90,28 @@ def _grad_out(logits, with_grad, dlogits, grad_dtype):
     return dlogits, _arg(dlogits, n, "dlogits"), _dt(dlogits)
 
 
-def _row_outputs(logits, T, loss, row_loss, stats):
-    """(tensor, pointer) of a loss's outputs, made where not given"""
-    l_p, r_p, s_p = _arg(loss, 1, "loss", _f32), _arg(row_loss, T, "row_loss", _f32), _arg(stats, 2 * T, "stats", _f32)
-    if loss is None:  # what is made here needs no check
+def _row_outputs(logits, T, loss, row_loss, stats, logp=None, want_logp=False):
+    """[(tensor, pointer)] of a loss's outputs loss, row_loss, stats and logp, made
+    where not given (all of them: in one allocation)"""
+    if loss is row_loss is stats is logp is None:
+        made = logits.new_empty((4 if want_logp else 3) * T + 1, dtype=_f32)
+        at = made.data_ptr()
+        if want_logp:
+            stats, row_loss, logp, loss = made.split((2 * T, T, T, 1))
+        else:
+            stats, row_loss, loss = made.split((2 * T, T, 1))
+        return (loss, at + (16 if want_logp else 12) * T), (row_loss, at + 8 * T), (stats.view(T, 2), at), \
+            (logp, at + 12 * T if want_logp else 0)
+    if loss is None:
         loss = logits.new_empty(1, dtype=_f32)
-        l_p = loss.data_ptr()
     if row_loss is None:
         row_loss = logits.new_empty(T, dtype=_f32)
-        r_p = row_loss.data_ptr()
     if stats is None:
         stats = logits.new_empty((T, 2), dtype=_f32)
-        s_p = stats.data_ptr()
-    return (loss, l_p), (row_loss, r_p), (stats, s_p)
+    if logp is None and want_logp:
+        logp = logits.new_empty(T, dtype=_f32)
+    return (loss, _arg(loss, 1, "loss", _f32)), (row_loss, _arg(row_loss, T, "row_loss", _f32)), \
+        (stats, _arg(stats, 2 * T, "stats", _f32)), (logp, _arg(logp, T, "logp", _f32))
 
 
 def _size(logits) -> Tuple[int, int]:
@@ -125,7 +139,7 @@ def distill_loss(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor,
     x_p, i_p, t_p = _arg(logits, T * V, "logits"), _arg(idx, T * K, "idx", _i32), _arg(teacher, T * K, "teacher")
     w_p, g_p = _arg(weight, T, "weight", _f32), _arg(grad_loss, 1, "grad_loss", _f32)
     dlogits, d_p, d_t = _grad_out(logits, with_grad, dlogits, grad_dtype)
-    (loss, l_p), (row_loss, r_p), (stats, s_p) = _row_outputs(logits, T, loss, row_loss, stats)
+    (loss, l_p), (row_loss, r_p), (stats, s_p), _ = _row_outputs(logits, T, loss, row_loss, stats)
     st = lib().moe_distill_loss(T, V, K, x_p, _dt(logits), i_p, t_p, _dt(teacher), temperature, w_p, g_p, l_p, r_p, s_p,
                                 d_p, d_t, _stream())
     _lib.check("moe_distill_loss", st)
@@ -166,12 +180,9 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tens
     x_p, i_p = _arg(logits, T * V, "logits"), _arg(tokens, T, "tokens", _i32)
     o_p, a_p = _arg(old_logp, T, "old_logp", _f32), _arg(advantage, T, "advantage", _f32)
     f_p, w_p = _arg(ref_logp, T, "ref_logp", _f32), _arg(weight, T, "weight", _f32)
-    g_p, p_p = _arg(grad_loss, 1, "grad_loss", _f32), _arg(logp, T, "logp", _f32)
+    g_p = _arg(grad_loss, 1, "grad_loss", _f32)
     dlogits, d_p, d_t = _grad_out(logits, with_grad, dlogits, grad_dtype)
-    (loss, l_p), (row_loss, r_p), (stats, s_p) = _row_outputs(logits, T, loss, row_loss, stats)
-    if logp is None:
-        logp = logits.new_empty(T, dtype=_f32)
-        p_p = logp.data_ptr()
+    (loss, l_p), (row_loss, r_p), (stats, s_p), (logp, p_p) = _row_outputs(logits, T, loss, row_loss, stats, logp, True)
     h = _lib.MoePolicyParams(temperature, clip[0], clip[1], kl)
     st = lib().moe_policy_loss(T, V, x_p, _dt(logits), i_p, o_p, a_p, f_p, ctypes.byref(h), w_p, g_p, l_p, r_p, p_p,
                                s_p, d_p, d_t, _stream())
@@ -216,3 +227,82 @@ def token_logp(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 
     st = lib().moe_token_logp(T, V, x_p, _dt(logits), i_p, temperature, l_p, s_p, _stream())
     _lib.check("moe_token_logp", st)
     return logp, stats
+
+
+# ---------------------------------------------------------------- the model
+
+class TokenModel:
+    """Token ids to logits around a MoEBlock, for training:
+
+        stream = scale table[ids],  delta = positions[pos]
+        out, stream = block(delta, stream),  y = norm(out + stream)
+        logits = y table^T
+
+    The table is tied: its gradient is the head's, onto which the lookup's is
+    accumulated.  table [V, d] and positions [P, d] are bf16; scale None: sqrt(d).
+    forward(ids, pos) returns logits [T, V] (bf16); a loss leaves their gradient
+    (dlogits=logits writes it over them); backward(dlogits) leaves every weight's
+    gradient; step() is the AdamW step on all of them, the block's included.
+
+    What forward and backward leave or return are buffers of the model (and of the
+    block) that the next call writes again.  The products with the table are plain
+    library ones."""
+
+    def __init__(self, block: MoEBlock, table: torch.Tensor, positions: torch.Tensor, norm_w: torch.Tensor,
+                 norm_b: torch.Tensor, scale: Optional[float] = None, eps: float = 1e-5):
+        la = block.layer
+        T, d, V, P = la.T, la.d, table.shape[0], positions.shape[0]
+        if table.shape[1] != d or positions.shape[1] != d:
+            raise ValueError(f"table and positions need rows of {d}")
+        self.block, self.table, self.positions, self.norm_w, self.norm_b = block, table, positions, norm_w, norm_b
+        self.scale, self.eps = d ** 0.5 if scale is None else scale, eps
+        new = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device=table.device)  # noqa: E731
+        self.stream, self.delta, self.sum, self.y, self.dy, self.dx = (new(T, d) for _ in range(6))
+        self.logits = new(T, V)
+        self.mean, self.rstd = new(T, dt=_f32), new(T, dt=_f32)
+        self.d_table, self.d_positions = new(V, d), new(P, d, dt=_f32)
+        self.d_norm_w, self.d_norm_b = new(d, dt=_f32), new(d, dt=_f32)
+        self.norm_ws = new(max(256, workspace_bytes(MOE_OP_LAYER_NORM_BACKWARD, la.sh)), dt=torch.uint8)
+        self.table_ws = new(_embedding_ws_bytes(T, V, d), dt=torch.uint8)
+        self.positions_ws = new(_embedding_ws_bytes(T, P, d), dt=torch.uint8)
+        self.opt = None
+
+    def forward(self, ids: torch.Tensor, pos: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
+                token_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+        T = self.block.layer.T
+        for name, t in (("ids", ids), ("pos", pos)):
+            if t.numel() != T:
+                raise ValueError(f"{name}: needs {T} elements, has {t.numel()}")
+        self.ids, self.pos = ids, pos
+        embedding(ids, self.table, self.scale, out=self.stream)
+        embedding(pos, self.positions, out=self.delta)
+        out, stream = self.block.forward(self.delta, self.stream, seq_offsets, token_mask)
+        layer_norm(out, self.norm_w, self.norm_b, residual=stream, eps=self.eps, y=self.y, sum_out=self.sum,
+                   mean=self.mean, rstd=self.rstd)
+        return torch.mm(self.y, self.table.t(), out=self.logits)
+
+    def backward(self, dlogits: torch.Tensor, grad_loss: Optional[torch.Tensor] = None) -> None:
+        """dlogits [T, V] bf16; grad_loss: the balance loss's factor, as
+        MoEBlock.backward's."""
+        if dlogits.shape != self.logits.shape or dlogits.dtype != torch.bfloat16:
+            raise ValueError(f"dlogits: needs bf16 {tuple(self.logits.shape)}")
+        torch.mm(dlogits.t(), self.y, out=self.d_table)
+        torch.mm(dlogits, self.table, out=self.dy)
+        layer_norm_backward(self.dy, self.sum, self.norm_w, self.mean, self.rstd, dx=self.dx, dw=self.d_norm_w,
+                            db=self.d_norm_b, ws=self.norm_ws)
+        dx = self.block.backward(self.dx, self.dx, grad_loss)
+        embedding_backward(dx, self.ids, self.table.shape[0], self.scale, d_table=self.d_table, accumulate=True,
+                           ws=self.table_ws)
+        embedding_backward(dx, self.pos, self.positions.shape[0], d_table=self.d_positions, ws=self.positions_ws)
+
+    def step(self, grad_scale: Optional[torch.Tensor] = None) -> None:
+        """AdamW on the table, the positions, the norm and the block; the norm and the
+        positions do not decay."""
+        if self.opt is None:
+            args = dict(self.block.opt_args)
+            args["weight_decay"] = [args["weight_decay"], 0.0, 0.0, 0.0]
+            self.opt = AdamW([self.table, self.positions, self.norm_w, self.norm_b],
+                             [self.d_table, self.d_positions, self.d_norm_w, self.d_norm_b], master=self.block.master,
+                             **args)
+        self.opt.step(grad_scale)
+        self.block.step(grad_scale)
