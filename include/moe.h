@@ -642,13 +642,14 @@ int moe_adamw_step(int32_t n_tensors, const moe_adamw_tensor* tensors, const moe
  * 1 <= V <= MOE_MAX_VOCAB, T < 2^26; any element alignment.
  */
 #define MOE_MAX_VOCAB 16777216
+#define MOE_MAX_EMBEDDING 1048576
 #define MOE_MAX_TEACHER_TOP 256
 
 /*
  * moe_embedding - out[t] = scale * table[token_ids[t]], zeros for an id outside
  * [0, V) (padding).  The product is formed in fp32 and rounded once.
  *   token_ids [T] int32;  table [V, d] in table_dtype;  out [T, d] in out_dtype
- *   (each MOE_BF16 or MOE_F32).  d >= 1.  T = 0 is a no-op.
+ *   (each MOE_BF16 or MOE_F32).  1 <= d <= MOE_MAX_EMBEDDING.  T = 0 is a no-op.
  */
 int moe_embedding(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* table, int table_dtype,
                   float scale, void* out, int out_dtype, moe_stream_t stream);
@@ -663,8 +664,10 @@ int moe_embedding(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, con
  *            batch's ids are touched
  *   ws       moe_embedding_backward_workspace_size(T, V, d) bytes; nothing in it
  *            needs to start at zero
- * T ceil(d / 1024) < 2^25.  The sums are fp32 over runs of the batch sorted by id,
- * in token order (deterministic).
+ * The sums are fp32 over runs of the batch sorted by id, in token order
+ * (deterministic).  MOE_ERR_UNSUPPORTED where T, V and d together need more
+ * work-groups than a launch has (T ceil(d / 1024) / 7 and a table row or 32 KB each
+ * count one, of 2^24).
  */
 size_t moe_embedding_backward_workspace_size(int64_t T, int64_t V, int32_t d);
 int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* d_out,
@@ -691,10 +694,11 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
  *             sum_v exp((logits - m) / temperature)
  *   dlogits   [T, V] in dlogits_dtype out, or NULL: the loss alone.  May be
  *             logits where the types agree.  One reading of the logits serves
- *             both.
+ *             both.  No output may be an input otherwise.
  * A counted row with a NaN, a +inf or no finite logit gives NaN.  The sums run in
  * a fixed order (deterministic), the softmax's in fp32, a row's loss and the sum
- * over rows in fp64.  T = 0: loss = 0.
+ * over rows in fp64; a row's results do not depend on the other rows.  T = 0:
+ * loss = 0.
  */
 int moe_distill_loss(int64_t T, int64_t V, int32_t K, const void* logits, int logits_dtype, const int32_t* topk_idx,
                      const void* teacher, int teacher_dtype, double temperature, const float* weight,

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "common.h"
@@ -691,13 +692,15 @@ int moe_embedding(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, con
   const int st = vocab_check(T, V);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
-  if (token_ids == nullptr || table == nullptr || out == nullptr || out == table) return MOE_ERR_INVALID_ARG;
+  if (token_ids == nullptr || table == nullptr || out == nullptr || out == table || out == token_ids)
+    return MOE_ERR_INVALID_ARG;
+  if (d > MOE_MAX_EMBEDDING) return MOE_ERR_UNSUPPORTED;
   return hip_status(launch_embedding(T, static_cast<int>(V), d, token_ids, table, table_dtype, scale, out, out_dtype,
                                      as_stream(stream)));
 }
 
 size_t moe_embedding_backward_workspace_size(int64_t T, int64_t V, int32_t d) {
-  if (vocab_check(T, V) != MOE_OK || d < 1) return 0;
+  if (vocab_check(T, V) != MOE_OK || d < 1 || d > MOE_MAX_EMBEDDING) return 0;
   return embedding_bwd_workspace_bytes(T, V, d);
 }
 
@@ -709,9 +712,9 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
     return MOE_ERR_INVALID_ARG;
   const int st = vocab_check(T, V);
   if (st != MOE_OK) return st;
-  if (T * ((d + 1023) / 1024) >= (int64_t{1} << 25)) return MOE_ERR_UNSUPPORTED;  // the launch's work-groups
+  if (d > MOE_MAX_EMBEDDING || !embedding_bwd_supported(T, V, d, d_table_dtype, accumulate != 0)) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (token_ids == nullptr || d_out == nullptr)) return MOE_ERR_INVALID_ARG;
-  if (d_table == nullptr || d_table == d_out) return MOE_ERR_INVALID_ARG;
+  if (d_table == nullptr || d_table == d_out || d_table == token_ids) return MOE_ERR_INVALID_ARG;
   if (ws == nullptr || ws_bytes < embedding_bwd_workspace_bytes(T, V, d) || !aligned256(ws)) return MOE_ERR_WORKSPACE;
   return hip_status(launch_embedding_bwd(T, static_cast<int>(V), d, token_ids, d_out, d_out_dtype, scale, d_table,
                                          d_table_dtype, accumulate != 0, ws, as_stream(stream)));
@@ -733,6 +736,14 @@ static int loss_check(int64_t T, int64_t V, const void* x, int x_dtype, const vo
   return MOE_OK;
 }
 
+// what a row writes must not be what other rows still read
+static bool any_same(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o != nullptr && o == i) return true;
+  return false;
+}
+
 static int distill_check(int64_t T, int32_t K, const int32_t* idx, const void* teacher, int t_dtype, double tau) {
   if (K < 1 || !is_float(t_dtype) || !is_temperature(tau)) return MOE_ERR_INVALID_ARG;
   if (K > MOE_MAX_TEACHER_TOP) return MOE_ERR_UNSUPPORTED;
@@ -748,6 +759,9 @@ int moe_distill_loss(int64_t T, int64_t V, int32_t K, const void* logits, int lo
   if (st == MOE_OK) st = distill_check(T, K, topk_idx, teacher, teacher_dtype, temperature);
   if (st != MOE_OK) return st;
   if (loss == nullptr || (T > 0 && (row_loss == nullptr || stats == nullptr))) return MOE_ERR_INVALID_ARG;
+  if (any_same({loss, row_loss, stats, dlogits}, {weight, grad_loss, topk_idx, teacher}) ||
+      any_same({loss, row_loss, stats}, {logits, dlogits}))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_distill_loss(T, static_cast<int>(V), K, logits, logits_dtype, topk_idx, teacher,
                                         teacher_dtype, temperature, weight, grad_loss, loss, row_loss, stats, dlogits,
                                         dlogits_dtype, as_stream(stream)));
@@ -762,7 +776,9 @@ int moe_distill_loss_backward(int64_t T, int64_t V, int32_t K, const void* logit
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   // the row's entries are read while others' gradients are written
-  if (stats == nullptr || dlogits == nullptr || dlogits == logits) return MOE_ERR_INVALID_ARG;
+  if (stats == nullptr || dlogits == nullptr ||
+      any_same({dlogits}, {logits, stats, topk_idx, teacher, weight, grad_loss}))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_distill_loss_bwd(T, static_cast<int>(V), K, logits, logits_dtype, stats, topk_idx, teacher,
                                             teacher_dtype, temperature, weight, grad_loss, dlogits, dlogits_dtype,
                                             as_stream(stream)));
@@ -789,6 +805,9 @@ int moe_policy_loss(int64_t T, int64_t V, const void* logits, int logits_dtype, 
   if (st != MOE_OK) return st;
   if (loss == nullptr || (T > 0 && (row_loss == nullptr || logp == nullptr || stats == nullptr)))
     return MOE_ERR_INVALID_ARG;
+  if (any_same({loss, row_loss, logp, stats, dlogits}, {weight, grad_loss, tokens, old_logp, advantage, ref_logp}) ||
+      any_same({loss, row_loss, logp, stats}, {logits, dlogits}))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_policy_loss(T, static_cast<int>(V), logits, logits_dtype, tokens, old_logp, advantage,
                                        params->kl > 0.0 ? ref_logp : nullptr, params->clip_low, params->clip_high,
                                        params->kl, params->temperature, weight, grad_loss, loss, row_loss, logp, stats,
@@ -803,7 +822,9 @@ int moe_policy_loss_backward(int64_t T, int64_t V, const void* logits, int logit
   if (st == MOE_OK) st = policy_check(T, tokens, old_logp, advantage, ref_logp, params);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
-  if (stats == nullptr || dlogits == nullptr || dlogits == logits) return MOE_ERR_INVALID_ARG;
+  if (stats == nullptr || dlogits == nullptr ||
+      any_same({dlogits}, {logits, stats, tokens, old_logp, advantage, ref_logp, weight, grad_loss}))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_policy_loss_bwd(T, static_cast<int>(V), logits, logits_dtype, stats, tokens, old_logp,
                                            advantage, params->kl > 0.0 ? ref_logp : nullptr, params->clip_low,
                                            params->clip_high, params->kl, params->temperature, weight, grad_loss,
@@ -816,7 +837,8 @@ int moe_token_logp(int64_t T, int64_t V, const void* logits, int logits_dtype, c
   if (st != MOE_OK) return st;
   if (!is_temperature(temperature)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (tokens == nullptr || logp == nullptr || stats == nullptr) return MOE_ERR_INVALID_ARG;
+  if (tokens == nullptr || logp == nullptr || stats == nullptr || any_same({logp, stats}, {logits, tokens}))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_policy_loss(T, static_cast<int>(V), logits, logits_dtype, tokens, nullptr, nullptr, nullptr,
                                        0.0, 0.0, 0.0, temperature, nullptr, nullptr, nullptr, nullptr, logp, stats,
                                        nullptr, 0, as_stream(stream)));

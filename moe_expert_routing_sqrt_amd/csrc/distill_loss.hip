@@ -297,25 +297,11 @@ hipError_t launch_loss_sum(int64_t rows, const float* row_loss, const float* wei
   return hipGetLastError();
 }
 
-static Logits distill_logits(int64_t rows, int V, double tau, const float* weight, const float* grad) {
-  Logits p{};
-  p.rows = rows;
-  p.V = V;
-  p.weight = weight;
-  p.grad = grad;
-  p.even = static_cast<float>(1.0 / static_cast<double>(rows));
-  p.tau = tau;
-  p.inv_tau = 1.0 / tau;
-  p.inv_tau_f = static_cast<float>(1.0 / tau);
-  p.c = static_cast<float>(1.4426950408889634 / tau);
-  return p;
-}
-
 hipError_t launch_distill_loss(int64_t rows, int V, int K, const void* x, int x_dtype, const int32_t* idx,
                                const void* teacher, int t_dtype, double tau, const float* weight, const float* grad,
                                float* loss, float* row_loss, float* stats, void* dx, int dx_dtype, hipStream_t s) {
   if (rows > 0) {
-    Logits p = distill_logits(rows, V, tau, weight, grad);
+    Logits p = vocab::logits_of(rows, V, tau, weight, grad);
     p.x = x;
     p.dx = dx;
     p.stats = stats;
@@ -331,7 +317,7 @@ hipError_t launch_distill_loss(int64_t rows, int V, int K, const void* x, int x_
 hipError_t launch_distill_loss_bwd(int64_t rows, int V, int K, const void* x, int x_dtype, const float* stats,
                                    const int32_t* idx, const void* teacher, int t_dtype, double tau,
                                    const float* weight, const float* grad, void* dx, int dx_dtype, hipStream_t s) {
-  Logits p = distill_logits(rows, V, tau, weight, grad);
+  Logits p = vocab::logits_of(rows, V, tau, weight, grad);
   p.x = x;
   p.dx = dx;
   p.stats = const_cast<float*>(stats);  // read only

@@ -6,6 +6,10 @@
 // Both are bound by memory.  The gradient first sorts the batch by id, stably,
 // so that each table row's tokens are one run in token order: its sum is then
 // formed in registers in a fixed order, with no atomics and one store a row.
+// Measured: lookup of 16384 x 7168 bf16 out of 131072 rows 68 us (235 MB written,
+// the rows read again where they repeat); its gradient, written whole in fp32 (3.8
+// GB), 750 us, of which clearing takes 640 (5.5 TB/s, what a plain fill of that
+// size reaches); 16384 x 2048 accumulated into fp32 rows 53 us.
 #include <algorithm>
 
 #include "launch.h"
@@ -463,13 +467,25 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const GradArgs
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// column blocks of a run or a part (E elements a thread), and table rows that a
+// work-group clears: about 32 KB (128 KB: 2 % slower)
+int column_blocks(int d, int E) { return (d + E * kThreads - 1) / (E * kThreads); }
+int rows_to_clear(int d, int bytes) {
+  const int64_t rows = (int64_t{1} << 15) / ((int64_t)d * bytes);
+  return static_cast<int>(std::min<int64_t>(kWave - 1, std::max<int64_t>(1, rows)));
+}
+int64_t run_chunks(int64_t T) { return (T + kRunChunk - 1) / kRunChunk; }
+int64_t long_chunks(int64_t T) { return (T + kLong - 1) / kLong; }
+int64_t grad_groups(int64_t T, int64_t V, int d, int E, int bytes, bool add) {
+  const int64_t rows = rows_to_clear(d, bytes);
+  return (run_chunks(T) + long_chunks(T)) * column_blocks(d, E) + (add ? 0 : (V + rows - 1) / rows);
+}
+
 template <typename TX, typename TO, int E, bool ADD>
 hipError_t grad(GradArgs a, hipStream_t s) {
-  a.blocks = (a.d + E * kThreads - 1) / (E * kThreads);
-  // about 32 KB a work-group
-  a.zero_rows = static_cast<int>(std::min<int64_t>(kWave - 1, std::max<int64_t>(1, (int64_t{1} << 15) / ((int64_t)a.d * sizeof(TO)))));
-  const int64_t zeros = ADD ? 0 : ((int64_t)a.V + a.zero_rows - 1) / a.zero_rows;
-  const int64_t x = (int64_t)(a.runs + a.longs) * a.blocks + zeros;
+  a.blocks = column_blocks(a.d, E);
+  a.zero_rows = rows_to_clear(a.d, sizeof(TO));
+  const int64_t x = grad_groups(a.T, a.V, a.d, E, sizeof(TO), ADD);
   if (x == 0) return hipSuccess;
   if (x > kMaxGroups) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(x)), block(kThreads);
@@ -497,9 +513,14 @@ hipError_t launch_embedding(int64_t T, int V, int d, const int32_t* ids, const v
   return yb ? lookup<float, B, 4>(a, s) : lookup<float, float, 4>(a, s);
 }
 
+bool embedding_bwd_supported(int64_t T, int64_t V, int d, int d_table_dtype, bool add) {
+  static_assert(MOE_MAX_EMBEDDING / (kWave * 4) <= 65535, "a grid's second axis");
+  return grad_groups(T, V, d, 4, d_table_dtype == MOE_BF16 ? 2 : 4, add) <= kMaxGroups;
+}
+
 size_t embedding_bwd_workspace_bytes(int64_t T, int64_t V, int d) {
   if (T == 0) T = 1;
-  const int64_t chunks = (T + kLong - 1) / kLong;
+  const int64_t chunks = long_chunks(T);
   return up256(T * sizeof(int2)) + up256((V + 1) * sizeof(int)) + up256(chunks * sizeof(int)) +
          up256(chunks * 2 * d * sizeof(float));
 }
@@ -532,8 +553,8 @@ hipError_t launch_embedding_bwd(int64_t T, int V, int d, const int32_t* ids, con
   a.T = o.T;
   a.V = V;
   a.d = d;
-  a.runs = (o.T + kRunChunk - 1) / kRunChunk;
-  a.longs = (o.T + kLong - 1) / kLong;
+  a.runs = static_cast<int>(run_chunks(T));
+  a.longs = static_cast<int>(long_chunks(T));
   a.scale = scale;
   a.job = reinterpret_cast<int*>(w);
   w += up256(std::max(1, a.longs) * sizeof(int));

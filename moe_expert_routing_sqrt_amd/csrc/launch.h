@@ -158,6 +158,7 @@ hipError_t launch_adamw(int n_tensors, const moe_adamw_tensor* t, const moe_adam
 hipError_t launch_embedding(int64_t T, int V, int d, const int32_t* ids, const void* table, int table_dtype,
                             float scale, void* out, int out_dtype, hipStream_t s);
 size_t embedding_bwd_workspace_bytes(int64_t T, int64_t V, int d);
+bool embedding_bwd_supported(int64_t T, int64_t V, int d, int d_table_dtype, bool add);  // the launch's work-groups
 hipError_t launch_embedding_bwd(int64_t T, int V, int d, const int32_t* ids, const void* dy, int dy_dtype, float scale,
                                 void* d_table, int d_table_dtype, bool add, void* ws, hipStream_t s);
 

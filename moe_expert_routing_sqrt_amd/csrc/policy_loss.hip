@@ -89,7 +89,8 @@ struct Policy {
   static __device__ __forceinline__ float gap_of(float d) {
     if (!(fabsf(d) < 0.5f)) return exp_of(d) - d - 1.0f;
     float s = 1.0f / 3628800;
-    constexpr float kInv[] = {1.0f / 362880, 1.0f / 40320, 1.0f / 5040, 1.0f / 720, 1.0f / 120, 1.0f / 24, 1.0f / 6, 0.5f};
+    constexpr float kInv[] = {1.0f / 362880, 1.0f / 40320, 1.0f / 5040, 1.0f / 720,
+                              1.0f / 120,    1.0f / 24,    1.0f / 6,    0.5f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = __builtin_fmaf(s, d, kInv[i]);
     return s * d * d;
@@ -130,20 +131,6 @@ struct Policy {
   }
 };
 
-Logits policy_logits(int64_t rows, int V, double tau, const float* weight, const float* grad) {
-  Logits p{};
-  p.rows = rows;
-  p.V = V;
-  p.weight = weight;
-  p.grad = grad;
-  p.even = static_cast<float>(1.0 / static_cast<double>(rows));
-  p.tau = tau;
-  p.inv_tau = 1.0 / tau;
-  p.inv_tau_f = static_cast<float>(1.0 / tau);
-  p.c = static_cast<float>(1.4426950408889634 / tau);
-  return p;
-}
-
 }  // namespace
 
 hipError_t launch_policy_loss(int64_t rows, int V, const void* x, int x_dtype, const int32_t* tok,
@@ -151,7 +138,7 @@ hipError_t launch_policy_loss(int64_t rows, int V, const void* x, int x_dtype, c
                               double kl, double tau, const float* weight, const float* grad, float* loss,
                               float* row_loss, float* logp, float* stats, void* dx, int dx_dtype, hipStream_t s) {
   if (rows > 0) {
-    Logits p = policy_logits(rows, V, tau, weight, grad);
+    Logits p = vocab::logits_of(rows, V, tau, weight, grad);
     p.x = x;
     p.dx = dx;
     p.stats = stats;
@@ -170,7 +157,7 @@ hipError_t launch_policy_loss_bwd(int64_t rows, int V, const void* x, int x_dtyp
                                   const int32_t* tok, const float* old_logp, const float* adv, const float* ref,
                                   double lo, double hi, double kl, double tau, const float* weight, const float* grad,
                                   void* dx, int dx_dtype, hipStream_t s) {
-  Logits p = policy_logits(rows, V, tau, weight, grad);
+  Logits p = vocab::logits_of(rows, V, tau, weight, grad);
   p.x = x;
   p.dx = dx;
   p.stats = const_cast<float*>(stats);  // read only

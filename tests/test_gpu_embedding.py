@@ -154,6 +154,24 @@ def test_gradient_is_the_lookups_by_differences():
     assert (step.double() * dy.double()).sum() == (M.embedding_backward(dy, ids, V, scale=2.0).double() * e.double()).sum()
 
 
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
+def test_longest_rows(xt):
+    """Rows of the largest size, one of them with a long run."""
+    dev = need_gpu()
+    T, V, d = 90, 3, 1 << 20
+    ids = torch.full((T,), 2, dtype=torch.int32, device=dev)
+    ids[7], ids[9] = 0, -1
+    table = torch.randint(-8, 9, (V, d), device=dev).to(xt)
+    out = M.embedding(ids[:10], table, scale=2.0)
+    assert torch.equal(out[8], table[2] * 2) and torch.equal(out[7], table[0] * 2) and not out[9].any()
+    dy = torch.randint(-1, 2, (T, d), device=dev).to(xt)  # sums of at most 88: exact in bf16
+    got = M.embedding_backward(dy, ids, V, dtype=xt)
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[[7, 9]] = False
+    assert torch.equal(got[2].float(), dy[rest.to(dev)].float().sum(0))
+    assert torch.equal(got[0], dy[7]) and not got[1].any()
+
+
 def test_past_32_bit_offsets():
     """Tables and batches of more than 2^32 elements."""
     dev = need_gpu()

@@ -22,7 +22,8 @@ def _embed(T=4, V=8, d=8, ids=A, table=B, tt=1, scale=1.0, out=C, ot=1):
 
 @pytest.mark.parametrize("kw,want", SIZES + [
     (dict(d=0), INV), (dict(ids=None), INV), (dict(table=None), INV), (dict(out=None), INV), (dict(out=B), INV),
-    (dict(tt=2), INV), (dict(ot=-1), INV), (dict(scale=NAN), INV), (dict(scale=INF), INV),
+    (dict(tt=2), INV), (dict(ot=-1), INV), (dict(scale=NAN), INV), (dict(scale=INF), INV), (dict(out=A), INV),
+    (dict(d=(1 << 20) + 1), UNS),
     (dict(T=0, ids=None, table=None, out=None), 0)])
 def test_embedding_refusals(kw, want):
     assert _embed(**kw) == want
@@ -35,7 +36,8 @@ def _embed_bwd(T=4, V=8, d=8, ids=A, dy=B, yt=1, scale=1.0, table=C, tt=0, add=0
 @pytest.mark.parametrize("kw,want", SIZES + [
     (dict(d=0), INV), (dict(ids=None), INV), (dict(dy=None), INV), (dict(table=None), INV), (dict(table=B), INV),
     (dict(yt=2), INV), (dict(tt=9), INV), (dict(scale=NAN), INV), (dict(add=2), INV), (dict(ws=None), WS),
-    (dict(ws=D + 16), WS), (dict(T=1 << 24, d=1025), UNS)])
+    (dict(ws=D + 16), WS), (dict(T=(1 << 26) - 1, d=2049), UNS),
+    (dict(T=1, V=1 << 24, d=9000), UNS), (dict(d=(1 << 20) + 1), UNS), (dict(table=A), INV)])
 def test_embedding_backward_refusals(kw, want):
     assert _embed_bwd(**kw) == want
 
@@ -45,15 +47,15 @@ def test_embedding_backward_workspace():
         need = L.moe_embedding_backward_workspace_size(T, V, d)
         assert need >= 8 * T + 4 * V
         assert _embed_bwd(T=T, V=V, d=d, n=need - 1) == WS
-    for bad in ((-1, 8, 8), (4, 0, 8), (4, 8, 0), (1 << 26, 8, 8)):
+    for bad in ((-1, 8, 8), (4, 0, 8), (4, 8, 0), (1 << 26, 8, 8), (4, 8, (1 << 20) + 1)):
         assert L.moe_embedding_backward_workspace_size(*bad) == 0
 
 
-def _distill(T=4, V=8, K=2, x=A, xt=1, idx=B, t=C, tt=0, tau=1.0, loss=D, row=D, stats=D, dx=None, dt=1):
-    return L.moe_distill_loss(T, V, K, x, xt, idx, t, tt, tau, None, None, loss, row, stats, dx, dt, None)
+def _distill(T=4, V=8, K=2, x=A, xt=1, idx=B, t=C, tt=0, tau=1.0, w=None, loss=D, row=D, stats=D, dx=None, dt=1):
+    return L.moe_distill_loss(T, V, K, x, xt, idx, t, tt, tau, w, None, loss, row, stats, dx, dt, None)
 
 
-def _distill_bwd(T=4, V=8, K=2, x=A, xt=1, idx=B, t=C, tt=0, tau=1.0, stats=D, dx=D, dt=1):
+def _distill_bwd(T=4, V=8, K=2, x=A, xt=1, idx=B, t=C, tt=0, tau=1.0, stats=D, dx=0x5000, dt=1):
     return L.moe_distill_loss_backward(T, V, K, x, xt, stats, idx, t, tt, tau, None, None, dx, dt, None)
 
 
@@ -64,13 +66,15 @@ DISTILL = SIZES + [(dict(K=0), INV), (dict(K=257), UNS), (dict(x=None), INV), (d
 
 
 @pytest.mark.parametrize("kw,want", DISTILL + [
-    (dict(loss=None), INV), (dict(row=None), INV), (dict(dx=D, dt=2), INV), (dict(dx=A, dt=0), INV)])
+    (dict(loss=None), INV), (dict(row=None), INV), (dict(dx=0x5000, dt=2), INV), (dict(dx=A, dt=0), INV),
+    (dict(w=D), INV), (dict(row=C), INV), (dict(stats=A), INV), (dict(dx=D), INV), (dict(dx=C), INV)])
 def test_distill_refusals(kw, want):
     assert _distill(**kw) == want
 
 
 @pytest.mark.parametrize("kw,want", DISTILL + [
     (dict(dx=None), INV), (dict(dt=2), INV), (dict(dx=A), INV), (dict(dx=A, dt=0), INV),
+    (dict(dx=B), INV), (dict(dx=C), INV), (dict(dx=D), INV),
     (dict(T=0, x=None, idx=None, t=None, stats=None, dx=None), 0)])
 def test_distill_backward_refusals(kw, want):
     assert _distill_bwd(**kw) == want
@@ -85,7 +89,7 @@ def _policy(T=4, V=8, x=A, xt=1, tok=B, old=C, adv=C, ref=None, h=_h(), loss=D, 
                              row, logp, stats, dx, dt, None)
 
 
-def _policy_bwd(T=4, V=8, x=A, xt=1, tok=B, old=C, adv=C, ref=None, h=_h(), stats=D, dx=D, dt=1):
+def _policy_bwd(T=4, V=8, x=A, xt=1, tok=B, old=C, adv=C, ref=None, h=_h(), stats=D, dx=0x5000, dt=1):
     return L.moe_policy_loss_backward(T, V, x, xt, stats, tok, old, adv, ref, None if h is None else ctypes.byref(h),
                                       None, None, dx, dt, None)
 
@@ -97,14 +101,15 @@ POLICY = SIZES + [(dict(x=None), INV), (dict(xt=2), INV), (dict(tok=None), INV),
 
 
 @pytest.mark.parametrize("kw,want", POLICY + [
-    (dict(loss=None), INV), (dict(row=None), INV), (dict(logp=None), INV), (dict(dx=D, dt=7), INV),
-    (dict(dx=A, dt=0), INV)])
+    (dict(loss=None), INV), (dict(row=None), INV), (dict(logp=None), INV), (dict(dx=0x5000, dt=7), INV),
+    (dict(dx=A, dt=0), INV), (dict(logp=C), INV), (dict(row=C), INV), (dict(stats=A), INV), (dict(dx=D), INV)])
 def test_policy_refusals(kw, want):
     assert _policy(**kw) == want
 
 
 @pytest.mark.parametrize("kw,want", POLICY + [
     (dict(dx=None), INV), (dict(dt=2), INV), (dict(dx=A), INV),
+    (dict(dx=B), INV), (dict(dx=C), INV), (dict(dx=D), INV),
     (dict(T=0, x=None, tok=None, old=None, adv=None, stats=None, dx=None), 0)])
 def test_policy_backward_refusals(kw, want):
     assert _policy_bwd(**kw) == want
@@ -116,7 +121,7 @@ def _logp(T=4, V=8, x=A, xt=1, tok=B, tau=1.0, logp=C, stats=D):
 
 @pytest.mark.parametrize("kw,want", SIZES + [
     (dict(x=None), INV), (dict(xt=2), INV), (dict(tok=None), INV), (dict(tau=0.0), INV), (dict(logp=None), INV),
-    (dict(stats=None), INV), (dict(T=0, x=None, tok=None), 0)])
+    (dict(stats=None), INV), (dict(logp=A), INV), (dict(stats=B), INV), (dict(T=0, x=None, tok=None), 0)])
 def test_token_logp_refusals(kw, want):
     assert _logp(**kw) == want
 
