@@ -181,7 +181,7 @@ constexpr int kTogether = 4;  // pieces whose maximum is taken before their expo
 constexpr int kBlock = 256;   // threads of a work-group whose rows are narrower
 // waves a SIMD holds, by the registers that NC pieces take
 template <int NC>
-constexpr int kWaves = NC > 8 ? 4 : NC > 4 ? 5 : 6;
+constexpr int kWaves = NC > 8 ? 4 : NC > 6 ? 5 : 6;
 template <int NT>
 constexpr int kTeams = NT < kBlock ? kBlock / NT : 1;  // rows a work-group has at once
 template <int NT>
@@ -273,7 +273,8 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
     // would be copied where they meet, and the copies wait for all loads.)
     const float tv = ft < tail ? one_f32(t) : -INFINITY;
     float m = fmaxf(tv, -FLT_MAX), sum = exp2_of((tv - m) * c);
-    constexpr int G = NC < kTogether ? (NC > 0 ? NC : 1) : kTogether;
+    constexpr int G = NC == 0 ? 1 : NC % kTogether == 0 ? kTogether : NC % 3 == 0 ? 3 : 2;
+    static_assert(NC % G == 0, "whole groups");
 #pragma unroll
     for (int i0 = 0; i0 < NC; i0 += G) {
       if (live && i0 < per) {
@@ -287,11 +288,12 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
         }
 #pragma unroll
         for (int i = i0; i < i0 + G; ++i) {
+          if (i >= per) break;  // (32768 x 10000 bf16, 5 pieces in registers for 8: 150 us, 130 with this)
           float f[E], s1 = 0.0f;
           vec_f32(h[i], f);
 #pragma unroll
           for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m1) * c);
-          s2 += i < per && (wave * per + i) * kWave + (ft & 63) < pieces ? s1 : 0.0f;
+          s2 += (wave * per + i) * kWave + (ft & 63) < pieces ? s1 : 0.0f;
         }
         sum = sum * exp2_of((m - m1) * c) + s2;
         m = m1;
@@ -499,6 +501,8 @@ hipError_t loss_rows(const Logits& p, const typename KIND::Args& k, hipStream_t 
   if (pieces <= 4 * 64) return run_loss<KIND, TX, TD, 64, 4, false, GRAD>(p, k, s);
   if (pieces <= 8 * 64) return run_loss<KIND, TX, TD, 64, 8, false, GRAD>(p, k, s);
   if (pieces <= 4 * 256) return run_loss<KIND, TX, TD, 256, 4, false, GRAD>(p, k, s);
+  // (6 between 4 and 8: 32768 x 10000 bf16 130 -> 118 us)
+  if (pieces <= 6 * 256) return run_loss<KIND, TX, TD, 256, 6, false, GRAD>(p, k, s);
   if (pieces <= 8 * 256) return run_loss<KIND, TX, TD, 256, 8, false, GRAD>(p, k, s);
   if (pieces <= 12 * 256) return run_loss<KIND, TX, TD, 256, 12, false, GRAD>(p, k, s);
   if (pieces <= 16 * 256) return run_loss<KIND, TX, TD, 256, 16, false, GRAD>(p, k, s);

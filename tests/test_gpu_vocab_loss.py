@@ -44,6 +44,7 @@ TYPES = [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")]
 # what a row's threads hold (131072 bf16, 65536 fp32)
 SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (7, 100), (9, 512), (5, 1023), (6, 1025), (3, 4096), (4, 4099),
          (5, 8200), (3, 16385), (300, 33), (3, 32768), (3, 32769), (2, 65536), (2, 70001), (2, 131072), (2, 140003)]
+SIZES += [(4, 5001), (3, 6144), (3, 6149), (2, 12288), (2, 12297), (2, 24577), (2, 49159), (2, 98311)]  # more limits
 
 
 def _at(t, shift):
