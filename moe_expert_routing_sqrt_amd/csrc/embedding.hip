@@ -9,7 +9,7 @@
 // Measured: lookup of 16384 x 7168 bf16 out of 131072 rows 68 us (235 MB written,
 // the rows read again where they repeat); its gradient, written whole in fp32 (3.8
 // GB), 750 us, of which clearing takes 640 (5.5 TB/s, what a plain fill of that
-// size reaches); 16384 x 2048 accumulated into fp32 rows 53 us.
+// size reaches); 16384 x 2048 accumulated into fp32 rows 46 us.
 #include <algorithm>
 
 #include "launch.h"
@@ -273,7 +273,7 @@ struct GradArgs {
 
 __device__ __forceinline__ int lane_of(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
 
-constexpr int kRowsAhead = 8;  // rows in flight
+constexpr int kRowsAhead = 16;  // rows in flight (8: 16384 x 2048 accumulated 48 us instead of 46)
 
 // scale * acc (+ old) to the row
 template <typename TO, int E, bool ADD>
@@ -326,8 +326,17 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const GradArgs
 #pragma unroll
     for (int j = 0; j < E; ++j) acc[j] = 0.0f;
   };
-  auto load = [&](int k, int tok) __attribute__((always_inline)) {
-    if (q.c >= 0) load_piece(v[k], dy + (int64_t)tok * p.d, q.c, p.d);
+  // The pieces of TB tokens, tok(k) each.  No branch lies between the loads: behind
+  // one, each would be waited for (1000 x 1001 fp32: 19.7 us, 16.6 so).
+  const int c = max(q.c, 0);
+  auto load = [&](auto tok) __attribute__((always_inline)) {
+    if (p.d >= E) {
+#pragma unroll
+      for (int k = 0; k < TB; ++k) load_vec<false>(v[k], dy + (int64_t)tok(k) * p.d + c);
+    } else {
+#pragma unroll
+      for (int k = 0; k < TB; ++k) load_piece(v[k], dy + (int64_t)tok(k) * p.d, 0, p.d);
+    }
   };
   auto add = [&](int k) __attribute__((always_inline)) {
     float f[E];
@@ -356,26 +365,28 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const GradArgs
     const int end = e - last > kLong ? last : e;  // a long run is not this kind's
     auto starts = [&](int i) __attribute__((always_inline)) { return (i < kWave ? sa >> i : sb >> (i - kWave)) & 1; };
     TO* row = table;
-    Vec<TO, E> old, olds[ADD ? TB : 1];
+    Vec<TO, E> old, olds[ADD ? kRunChunk : 1];
     for (int i = __builtin_ctzll(here); i < end; i += TB) {
+      load([&](int k) __attribute__((always_inline)) {
+        const int at = min(i + k, end - 1);
+        return at < kWave ? lane_of(a.x, at) : lane_of(b.x, at - kWave);
+      });
+      if constexpr (ADD) {
 #pragma unroll
-      for (int k = 0; k < TB; ++k) {
-        const int at = i + k;
-        if (at >= end) break;
-        load(k, at < kWave ? lane_of(a.x, at) : lane_of(b.x, at - kWave));
-        if constexpr (ADD) {
-          if (at < kRunChunk && starts(at) && q.c >= 0)
+        for (int k = 0; k < kRunChunk; ++k) {
+          const int at = i + k;
+          if (at < min(kRunChunk, end) && starts(at) && q.c >= 0)
             load_piece(olds[k], table + (int64_t)lane_of(a.y, at) * p.d, q.c, p.d);
         }
       }
 #pragma unroll
       for (int k = 0; k < TB; ++k) {
         const int at = i + k;
-        if (at >= end) break;
-        if (at < kRunChunk && starts(at)) {
+        if (at >= end) continue;
+        if (k < kRunChunk && at < kRunChunk && starts(at)) {
           clear();
           row = table + (int64_t)lane_of(a.y, at) * p.d;
-          if constexpr (ADD) old = olds[k];
+          if constexpr (ADD) old = olds[k < kRunChunk ? k : 0];
         }
         add(k);
         if (starts(at + 1)) put_row<TO, E, ADD>(row, p.d, q, acc, old, p.scale);
@@ -398,15 +409,10 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(const GradArgs
     clear();
     const int to = min(e - p0, used);
     for (int i = max(s - p0, 0); i < to; i += TB) {
+      load([&](int k) __attribute__((always_inline)) { return lane_of(a.x, min(i + k, to - 1)); });
 #pragma unroll
       for (int k = 0; k < TB; ++k) {
-        if (i + k >= to) break;
-        load(k, lane_of(a.x, i + k));
-      }
-#pragma unroll
-      for (int k = 0; k < TB; ++k) {
-        if (i + k >= to) break;
-        add(k);
+        if (i + k < to) add(k);
       }
     }
     float* part = p.part + ((int64_t)g * 2 + side) * p.d;
