@@ -443,11 +443,11 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(const GradArgs
     for (int i = 0; i < B; ++i) {
       const int k = min(k0 + i, k1 - 1);
       const int64_t at = lead != 0 && k == 0 ? (int64_t)(c0 - 1) * 2 + 1 : (int64_t)(c0 + k - lead) * 2;
-      if (q.c >= 0) load_piece(t[i], p.part + at * p.d, q.c, p.d);
+      load_piece(t[i], p.part + at * p.d, max(q.c, 0), p.d);
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-      if (k0 + i >= k1 || q.c < 0) continue;
+      if (k0 + i >= k1) continue;
 #pragma unroll
       for (int j = 0; j < E; ++j) acc[j] += __uint_as_float(t[i].w[j]);
     }
