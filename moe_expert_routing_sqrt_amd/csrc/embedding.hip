@@ -9,7 +9,8 @@
 // Measured: lookup of 16384 x 7168 bf16 out of 131072 rows 68 us (235 MB written,
 // the rows read again where they repeat); its gradient, written whole in fp32 (3.8
 // GB), 750 us, of which clearing takes 640 (5.5 TB/s, what a plain fill of that
-// size reaches); 16384 x 2048 accumulated into fp32 rows 46 us.
+// size reaches); 16384 x 2048 accumulated into fp32 rows 47 us
+// (10 of them the sort).
 #include <algorithm>
 
 #include "launch.h"
@@ -273,7 +274,7 @@ struct GradArgs {
 
 __device__ __forceinline__ int lane_of(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
 
-constexpr int kRowsAhead = 16;  // rows in flight (8: 16384 x 2048 accumulated 48 us instead of 46)
+constexpr int kRowsAhead = 16;  // rows in flight (8: 16384 x 2048 accumulated 48 us, 46 so)
 
 // scale * acc (+ old) to the row
 template <typename TO, int E, bool ADD>
