@@ -97,9 +97,9 @@ def _row_outputs(logits, T, loss, row_loss, stats, logp=None, want_logp=False):
         made = logits.new_empty((4 if want_logp else 3) * T + 1, dtype=_f32)
         at = made.data_ptr()
         if want_logp:
-            stats, row_loss, logp, loss = made.split((2 * T, T, T, 1))
+            stats, row_loss, logp, loss = made.split_with_sizes((2 * T, T, T, 1))
         else:
-            stats, row_loss, loss = made.split((2 * T, T, 1))
+            stats, row_loss, loss = made.split_with_sizes((2 * T, T, 1))
         return (loss, at + (16 if want_logp else 12) * T), (row_loss, at + 8 * T), (stats.view(T, 2), at), \
             (logp, at + 12 * T if want_logp else 0)
     if loss is None:
