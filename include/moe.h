@@ -730,6 +730,9 @@ int moe_distill_loss_backward(int64_t T, int64_t V, int32_t K, const void* logit
  *             gradient are 0, and it may hold anything
  *   logp      [T] fp32 out
  *   the rest, and NaN, as moe_distill_loss
+ * Any difference of log-probabilities, infinite ones too: an advantage of 0
+ * counts 0 beside any ratio, a row_loss beyond fp32 is infinite, and a factor of
+ * the row's gradient beyond fp32 is fp32's largest number.
  */
 typedef struct moe_policy_params {
   double temperature, clip_low, clip_high, kl;
