@@ -17,17 +17,20 @@ from .training import _arg as _sized
 _f32, _i32 = torch.float32, torch.int32
 
 
-def _arg(t: Optional[torch.Tensor], numel: int, name: str, dtype: Optional[torch.dtype] = None) -> int:
-    """The pointer of a tensor argument (0 for None): its size, type and layout are
-    checked, and that it lives on the current device, whose stream the call uses."""
+def _arg(t: Optional[torch.Tensor], numel: Optional[int], name: str, dtype: Optional[torch.dtype] = None) -> int:
+    """The pointer of a tensor argument (0 for None): its size (exactly numel; None:
+    any), type and layout are checked, and that it lives on the current device, whose
+    stream the call uses."""
     if t is None:
         return 0
     on = t.get_device()
-    if (dtype is None or t.dtype is dtype) and on >= 0 and t.numel() >= numel and t.is_contiguous():
+    if (dtype is None or t.dtype is dtype) and on >= 0 and (numel is None or t.numel() == numel) and t.is_contiguous():
         if _device_index is None or on == _device_index():
             return t.data_ptr()
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device_index()}")
-    return _sized(t, numel, name, dtype)  # raises
+    if numel is not None and t.numel() != numel and (dtype is None or t.dtype is dtype):
+        raise ValueError(f"{name}: needs {numel} elements, has {t.numel()}")
+    return _sized(t, 0, name, dtype)  # raises
 
 
 # ---------------------------------------------------------------- embedding
@@ -38,7 +41,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: O
     (None: the table's).  Ids (int32) outside [0, V) give zeros."""
     V, d = table.shape
     T = ids.numel()
-    i_p, t_p, o_p = _arg(ids, T, "ids", _i32), _arg(table, 0, "table"), _arg(out, T * d, "out")
+    i_p, t_p, o_p = _arg(ids, T, "ids", _i32), _arg(table, None, "table"), _arg(out, T * d, "out")
     if out is None:
         out = table.new_empty((*ids.shape, d), dtype=out_dtype)
         o_p = out.data_ptr()
@@ -58,19 +61,19 @@ def embedding_backward(d_out: torch.Tensor, ids: torch.Tensor, n_rows: int, scal
     """The table's gradient [n_rows, d] for embedding's d_out [*ids.shape, d].
     accumulate: added to what d_table holds (a tied head's gradient, earlier
     micro-batches), else every row is written, in d_table or a new tensor of dtype."""
+    if accumulate and d_table is None:
+        raise ValueError("accumulate needs d_table")
     d = d_out.shape[-1]
     T = ids.numel()
     i_p, y_p = _arg(ids, T, "ids", _i32), _arg(d_out, T * d, "d_out")
     t_p = _arg(d_table, n_rows * d, "d_table")
     if d_table is None:
-        if accumulate:
-            raise ValueError("accumulate needs d_table")
         d_table = d_out.new_empty((n_rows, d), dtype=dtype)
         t_p = d_table.data_ptr()
     if ws is None:
         ws = torch.empty(_embedding_ws_bytes(T, n_rows, d), dtype=torch.uint8, device=d_out.device)
     st = lib().moe_embedding_backward(T, n_rows, d, i_p, y_p, _dt(d_out), scale, t_p, _dt(d_table),
-                                      1 if accumulate else 0, _arg(ws, 0, "ws"), _ws_len(ws), _stream())
+                                      1 if accumulate else 0, _arg(ws, None, "ws"), _ws_len(ws), _stream())
     _lib.check("moe_embedding_backward", st)
     return d_table
 
@@ -121,6 +124,14 @@ def _size(logits) -> Tuple[int, int]:
     return (logits.numel() // V if V else 0), V
 
 
+def _entries(idx, teacher) -> int:
+    """The entries of a row, of which idx and teacher have the same number"""
+    K = idx.shape[-1] if idx.dim() else 0
+    if teacher.dim() == 0 or teacher.shape[-1] != K:
+        raise ValueError(f"teacher: needs rows of {K}, as idx has, has shape {tuple(teacher.shape)}")
+    return K
+
+
 def distill_loss(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, temperature: float = 1.0,
                  weight: Optional[torch.Tensor] = None, with_grad: bool = False,
                  grad_loss: Optional[torch.Tensor] = None, grad_dtype: Optional[torch.dtype] = None,
@@ -135,7 +146,7 @@ def distill_loss(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor,
     grad_loss ([1] fp32 on the device; None: 1) from the same reading of the
     logits, in grad_dtype (None: the logits').  Else dlogits is None."""
     T, V = _size(logits)
-    K = idx.shape[-1]
+    K = _entries(idx, teacher)
     x_p, i_p, t_p = _arg(logits, T * V, "logits"), _arg(idx, T * K, "idx", _i32), _arg(teacher, T * K, "teacher")
     w_p, g_p = _arg(weight, T, "weight", _f32), _arg(grad_loss, 1, "grad_loss", _f32)
     dlogits, d_p, d_t = _grad_out(logits, with_grad, dlogits, grad_dtype)
@@ -153,7 +164,7 @@ def distill_loss_backward(logits: torch.Tensor, stats: torch.Tensor, idx: torch.
     """distill_loss's gradient from the logits and its stats (dlogits must not be
     logits)."""
     T, V = _size(logits)
-    K = idx.shape[-1]
+    K = _entries(idx, teacher)
     dlogits, d_p, d_t = _grad_out(logits, True, dlogits, grad_dtype)
     st = lib().moe_distill_loss_backward(T, V, K, _arg(logits, T * V, "logits"), _dt(logits),
                                          _arg(stats, 2 * T, "stats", _f32), _arg(idx, T * K, "idx", _i32),
