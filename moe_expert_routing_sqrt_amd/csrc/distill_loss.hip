@@ -16,7 +16,7 @@
 namespace moe {
 namespace {
 
-using vocab::exp2_of;
+using vocab::exp_tau;
 using vocab::Logits;
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -92,7 +92,7 @@ struct Distill {
     float top = ok ? few.a.t : -FLT_MAX, sum;
     if (k.K <= kWave) {  // all in this lane's registers
       top = wave_max(top);
-      const float u = few.a.t - top, e = ok ? exp2_of(u * p.c) : 0.0f;
+      const float u = few.a.t - top, e = ok ? exp_tau(p, u) : 0.0f;
       sum = wave_sum(e);
       if (lane < k.K) {
         sh.u[lane] = u;
@@ -123,7 +123,7 @@ struct Distill {
   static __device__ __forceinline__ float weigh(const Logits& p, const Args& k, float top, int lane, S& sh) {
     float sum = 0.0f;
     for (int j = lane; j < k.K; j += kWave) {
-      const float u = sh.u[j] - top, e = sh.at[j] >= 0 ? exp2_of(u * p.c) : 0.0f;
+      const float u = sh.u[j] - top, e = sh.at[j] >= 0 ? exp_tau(p, u) : 0.0f;
       sh.u[j] = u;
       sh.p[j] = e;
       sum += e;
@@ -148,7 +148,7 @@ struct Distill {
     float top = ok ? a.t : -FLT_MAX, sum;
     if (k.K <= kWave) {
       top = wave_max(top);
-      const float e = ok ? exp2_of((a.t - top) * p.c) : 0.0f;
+      const float e = ok ? exp_tau(p, a.t - top) : 0.0f;
       sum = wave_sum(e);
       if (lane < k.K) enter(sh, owner, lane, a.id, e / sum, ok && a.id >= lo && a.id < hi);
     } else {

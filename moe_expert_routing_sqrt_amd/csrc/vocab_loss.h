@@ -22,12 +22,14 @@
 //   none         one thread: the outputs of a row that does not count
 //
 // exp is 2^((x - max) log2(e)/tau): the difference first, so that its relative
-// error does not grow with the logits.  Sums are fp32, a thread's in order, then
+// error does not grow with the logits, the factor in two parts.  Sums are fp32, a thread's in order, then
 // a fixed tree.  A row without a finite logit gives NaN; a NaN spreads over its
 // row.  -inf is a logit of probability 0.
 #pragma once
 
 #include <hip/hip_runtime.h>
+
+#include <cmath>
 
 #include "launch.h"
 #include "rowvec.h"
@@ -45,7 +47,7 @@ struct Logits {
   const float* grad;    // [1] or nullptr: 1
   float* row_loss;
   float even;           // 1 / rows
-  float c;              // log2(e) / tau
+  float c, c_low;       // log2(e) / tau in two parts
   float inv_tau_f;
   double inv_tau, tau;
 };
@@ -60,11 +62,22 @@ inline Logits logits_of(int64_t rows, int V, double tau, const float* weight, co
   p.tau = tau;
   p.inv_tau = 1.0 / tau;
   p.inv_tau_f = static_cast<float>(1.0 / tau);
-  p.c = static_cast<float>(1.4426950408889634 / tau);
+  // The low part is positive, so that a difference of -inf stays -inf: c is the
+  // second number below.
+  const double c = 1.4426950408889634 / tau;
+  p.c = std::nextafter(std::nextafter(static_cast<float>(c), 0.0f), 0.0f);
+  p.c_low = static_cast<float>(c - static_cast<double>(p.c));
   return p;
 }
 
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// exp(v / tau).  log2(e)/tau as one fp32 number would put every term of a row off in
+// the same direction, by up to 2^-24 of its exponent; so it is the rounding of one
+// product.  4096 x 131072 bf16 with gradient: 2 % slower.
+__device__ __forceinline__ float exp_tau(const Logits& p, float v) {
+  return exp2_of(__builtin_fmaf(v, p.c, v * p.c_low));
+}
 
 // A value of an input that the kernel does not write, at an address that is the
 // same in all lanes, through the scalar cache: it does not wait for the vector
@@ -223,7 +236,6 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
   const float g = p.grad != nullptr ? scalar_of(p.grad) : 1.0f;
 
   const Owner owner{pieces, E, NT, per, NC * NT};
-  const float c = p.c;
   const TX* const x0 = static_cast<const TX*>(p.x);
   Vec<TX, E> h[NC > 0 ? NC : 1];
   TX t{};
@@ -272,7 +284,7 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
     // is one place that loads a piece, taken by every row: with two, the registers
     // would be copied where they meet, and the copies wait for all loads.)
     const float tv = ft < tail ? one_f32(t) : -INFINITY;
-    float m = fmaxf(tv, -FLT_MAX), sum = exp2_of((tv - m) * c);
+    float m = fmaxf(tv, -FLT_MAX), sum = exp_tau(p, tv - m);
     constexpr int G = NC == 0 ? 1 : NC % kTogether == 0 ? kTogether : NC % 3 == 0 ? 3 : 2;
     static_assert(NC % G == 0, "whole groups");
 #pragma unroll
@@ -292,10 +304,10 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
           float f[E], s1 = 0.0f;
           vec_f32(h[i], f);
 #pragma unroll
-          for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m1) * c);
+          for (int j = 0; j < E; ++j) s1 += exp_tau(p, f[j] - m1);
           s2 += (wave * per + i) * kWave + (ft & 63) < pieces ? s1 : 0.0f;
         }
-        sum = sum * exp2_of((m - m1) * c) + s2;
+        sum = sum * exp_tau(p, m - m1) + s2;
         m = m1;
       }
       if constexpr (!GRAD) {
@@ -318,14 +330,14 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
 #pragma unroll
           for (int j = 0; j < E; ++j) m1 = fmaxf(m1, f[j]);
 #pragma unroll
-          for (int j = 0; j < E; ++j) s1 += exp2_of((f[j] - m1) * c);
-          sum = sum * exp2_of((m - m1) * c) + (i0 + u * NT < pieces ? s1 : 0.0f);
+          for (int j = 0; j < E; ++j) s1 += exp_tau(p, f[j] - m1);
+          sum = sum * exp_tau(p, m - m1) + (i0 + u * NT < pieces ? s1 : 0.0f);
           m = m1;
         }
       }
       // the row's
       const float mw = wave_max(m);
-      sum = wave_sum(sum * exp2_of((m - mw) * c));
+      sum = wave_sum(sum * exp_tau(p, m - mw));
       m = mw;
       if constexpr (WAVES > 1) {
         if ((ft & 63) == 0) {
@@ -339,7 +351,7 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
         const float m1 = s_red[turn][0][ft & 15];
         sum = s_red[turn][1][ft & 15];
         m = row16_max(m1);
-        sum = row16_sum(sum * exp2_of((m1 - m) * c));
+        sum = row16_sum(sum * exp_tau(p, m1 - m));
       }
       if (wave == 0) KIND::finish(p, k, row, g * w, m, sum, ft, sh, true);
       if constexpr (GRAD) {
@@ -361,7 +373,7 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
           float f[E];
           vec_f32(h[i], f);
 #pragma unroll
-          for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          for (int j = 0; j < E; ++j) f[j] = ks * exp_tau(p, f[j] - m);
           const int at = (wave * per + i) * kWave + (ft & 63);
           KIND::correct(sh, mine, i, at, kr, ft, f);
           Vec<TD, E> o;
@@ -371,7 +383,7 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
         fetch(i, xn, live_next);
       }
       if (kr != 0.0f && ft < tail)
-        tail_out(KIND::correct_one(sh, mine, pieces * E + ft, kr, ft, ks * exp2_of((tv - m) * c)));
+        tail_out(KIND::correct_one(sh, mine, pieces * E + ft, kr, ft, ks * exp_tau(p, tv - m)));
       fetch_tail(xn);
       for (int i0 = MORE && kr != 0.0f ? NC * NT + ft : pieces; i0 < pieces; i0 += U * NT) {
         Vec<TX, E> v[U];
@@ -382,7 +394,7 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
           float f[E];
           vec_f32(v[u], f);
 #pragma unroll
-          for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          for (int j = 0; j < E; ++j) f[j] = ks * exp_tau(p, f[j] - m);
           KIND::correct(sh, mine, owner.local(i0 + u * NT), i0 + u * NT, kr, ft, f);
           Vec<TD, E> o;
           f32_vec(o, f);
@@ -416,7 +428,7 @@ __global__ __launch_bounds__(kGroup<NT>, (NT > kWave ? 6 : 5)) void grad_kernel(
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int V = p.V, pieces = V / E, tail = V % E;
-  const float g = p.grad != nullptr ? scalar_of(p.grad) : 1.0f, c = p.c;
+  const float g = p.grad != nullptr ? scalar_of(p.grad) : 1.0f;
   const Owner owner{pieces, E, NT, 1, 0};
   auto& sh = s_kind[team];
   for (int64_t unit = (int64_t)blockIdx.x * kTeams<NT> + team; unit < units; unit += (int64_t)gridDim.x * kTeams<NT>) {
@@ -461,7 +473,7 @@ __global__ __launch_bounds__(kGroup<NT>, (NT > kWave ? 6 : 5)) void grad_kernel(
           float f[E];
           vec_f32(v[u], f);
 #pragma unroll
-          for (int j = 0; j < E; ++j) f[j] = ks * exp2_of((f[j] - m) * c);
+          for (int j = 0; j < E; ++j) f[j] = ks * exp_tau(p, f[j] - m);
           KIND::correct(sh, mine, owner.local(i0 + u * NT), i0 + u * NT, kr, tid, f);
           Vec<TD, E> o;
           f32_vec(o, f);
@@ -471,7 +483,7 @@ __global__ __launch_bounds__(kGroup<NT>, (NT > kWave ? 6 : 5)) void grad_kernel(
       }
       if (one) {
         const int64_t at = (int64_t)pieces * E + tid;
-        const float f = ks * exp2_of((one_f32(x[at]) - m) * c);
+        const float f = ks * exp_tau(p, one_f32(x[at]) - m);
         put_one(dx + at, KIND::correct_one(sh, mine, static_cast<int>(at), kr, tid, f));
       }
     }
