@@ -639,7 +639,9 @@ int moe_adamw_step(int32_t n_tensors, const moe_adamw_tensor* tensors, const moe
  * ------------------------------------------------- tokens in, losses on logits
  * The two ends of a training step on tokens: rows of a table by token id, and
  * losses on the logits [T, V] of a vocabulary with their gradients.
- * 1 <= V <= MOE_MAX_VOCAB, T < 2^26; any element alignment.
+ * 1 <= V <= MOE_MAX_VOCAB, T < 2^26; any element alignment.  An output that
+ * shares memory with an input, a workspace or another output is refused, unless a
+ * call allows it (MOE_ERR_INVALID_ARG).
  */
 #define MOE_MAX_VOCAB 16777216
 #define MOE_MAX_EMBEDDING 1048576
@@ -694,7 +696,7 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
  *             sum_v exp((logits - m) / temperature)
  *   dlogits   [T, V] in dlogits_dtype out, or NULL: the loss alone.  May be
  *             logits where the types agree.  One reading of the logits serves
- *             both.  No output may be an input otherwise.
+ *             both.
  * A counted row with a NaN, a +inf or no finite logit gives NaN.  The sums run in
  * a fixed order (deterministic), the softmax's in fp32, a row's loss and the sum
  * over rows in fp64; a row's results do not depend on the other rows.  T = 0:

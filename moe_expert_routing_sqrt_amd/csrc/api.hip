@@ -686,15 +686,40 @@ static int vocab_check(int64_t T, int64_t V) {
   return MOE_OK;
 }
 
+// memory of n bytes
+struct Mem {
+  const void* p;
+  int64_t n;
+  bool meets(const Mem& o) const {
+    const char *a = static_cast<const char*>(p), *b = static_cast<const char*>(o.p);
+    return a != nullptr && b != nullptr && n > 0 && o.n > 0 && a < b + o.n && b < a + n;
+  }
+};
+static Mem floats(const void* p, int64_t n) { return {p, 4 * n}; }  // and int32
+static Mem of_type(const void* p, int64_t n, int dtype) { return {p, (dtype == MOE_BF16 ? 2 : 4) * n}; }
+
+// Whether an output shares memory with an input or another output: what a row
+// writes must not be what other rows still read, or write themselves.
+static bool any_shared(std::initializer_list<Mem> outs, std::initializer_list<Mem> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Mem& i : ins)
+      if (o->meets(i)) return true;
+    for (auto q = o + 1; q != outs.end(); ++q)
+      if (o->meets(*q)) return true;
+  }
+  return false;
+}
+
 int moe_embedding(int64_t T, int64_t V, int32_t d, const int32_t* token_ids, const void* table, int table_dtype,
                   float scale, void* out, int out_dtype, moe_stream_t stream) {
   if (!is_float(table_dtype) || !is_float(out_dtype) || !std::isfinite(scale) || d < 1) return MOE_ERR_INVALID_ARG;
   const int st = vocab_check(T, V);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
-  if (token_ids == nullptr || table == nullptr || out == nullptr || out == table || out == token_ids)
-    return MOE_ERR_INVALID_ARG;
+  if (token_ids == nullptr || table == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
   if (d > MOE_MAX_EMBEDDING) return MOE_ERR_UNSUPPORTED;
+  if (any_shared({of_type(out, T * d, out_dtype)}, {of_type(table, V * d, table_dtype), floats(token_ids, T)}))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_embedding(T, static_cast<int>(V), d, token_ids, table, table_dtype, scale, out, out_dtype,
                                      as_stream(stream)));
 }
@@ -714,8 +739,12 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
   if (st != MOE_OK) return st;
   if (d > MOE_MAX_EMBEDDING || !embedding_bwd_supported(T, V, d, d_table_dtype, accumulate != 0)) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (token_ids == nullptr || d_out == nullptr)) return MOE_ERR_INVALID_ARG;
-  if (d_table == nullptr || d_table == d_out || d_table == token_ids) return MOE_ERR_INVALID_ARG;
-  if (ws == nullptr || ws_bytes < embedding_bwd_workspace_bytes(T, V, d) || !aligned256(ws)) return MOE_ERR_WORKSPACE;
+  if (d_table == nullptr) return MOE_ERR_INVALID_ARG;
+  const size_t need = embedding_bwd_workspace_bytes(T, V, d);
+  if (ws == nullptr || ws_bytes < need || !aligned256(ws)) return MOE_ERR_WORKSPACE;
+  if (any_shared({of_type(d_table, V * d, d_table_dtype), {ws, static_cast<int64_t>(need)}},
+                 {of_type(d_out, T * d, d_out_dtype), floats(token_ids, T)}))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_embedding_bwd(T, static_cast<int>(V), d, token_ids, d_out, d_out_dtype, scale, d_table,
                                          d_table_dtype, accumulate != 0, ws, as_stream(stream)));
 }
@@ -736,14 +765,6 @@ static int loss_check(int64_t T, int64_t V, const void* x, int x_dtype, const vo
   return MOE_OK;
 }
 
-// what a row writes must not be what other rows still read
-static bool any_same(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
-  for (const void* o : outs)
-    for (const void* i : ins)
-      if (o != nullptr && o == i) return true;
-  return false;
-}
-
 static int distill_check(int64_t T, int32_t K, const int32_t* idx, const void* teacher, int t_dtype, double tau) {
   if (K < 1 || !is_float(t_dtype) || !is_temperature(tau)) return MOE_ERR_INVALID_ARG;
   if (K > MOE_MAX_TEACHER_TOP) return MOE_ERR_UNSUPPORTED;
@@ -759,8 +780,10 @@ int moe_distill_loss(int64_t T, int64_t V, int32_t K, const void* logits, int lo
   if (st == MOE_OK) st = distill_check(T, K, topk_idx, teacher, teacher_dtype, temperature);
   if (st != MOE_OK) return st;
   if (loss == nullptr || (T > 0 && (row_loss == nullptr || stats == nullptr))) return MOE_ERR_INVALID_ARG;
-  if (any_same({loss, row_loss, stats, dlogits}, {weight, grad_loss, topk_idx, teacher}) ||
-      any_same({loss, row_loss, stats}, {logits, dlogits}))
+  const Mem x = of_type(logits, T * V, logits_dtype), dx = of_type(dlogits, T * V, dlogits_dtype);
+  if (any_shared({floats(loss, 1), floats(row_loss, T), floats(stats, 2 * T), dx},
+                 {dlogits == logits ? Mem{} : x, floats(weight, T), floats(grad_loss, 1), floats(topk_idx, T * K),
+                  of_type(teacher, T * K, teacher_dtype)}))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_distill_loss(T, static_cast<int>(V), K, logits, logits_dtype, topk_idx, teacher,
                                         teacher_dtype, temperature, weight, grad_loss, loss, row_loss, stats, dlogits,
@@ -777,7 +800,9 @@ int moe_distill_loss_backward(int64_t T, int64_t V, int32_t K, const void* logit
   if (T == 0) return MOE_OK;
   // the row's entries are read while others' gradients are written
   if (stats == nullptr || dlogits == nullptr ||
-      any_same({dlogits}, {logits, stats, topk_idx, teacher, weight, grad_loss}))
+      any_shared({of_type(dlogits, T * V, dlogits_dtype)},
+                 {of_type(logits, T * V, logits_dtype), floats(stats, 2 * T), floats(topk_idx, T * K),
+                  of_type(teacher, T * K, teacher_dtype), floats(weight, T), floats(grad_loss, 1)}))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_distill_loss_bwd(T, static_cast<int>(V), K, logits, logits_dtype, stats, topk_idx, teacher,
                                             teacher_dtype, temperature, weight, grad_loss, dlogits, dlogits_dtype,
@@ -805,8 +830,10 @@ int moe_policy_loss(int64_t T, int64_t V, const void* logits, int logits_dtype, 
   if (st != MOE_OK) return st;
   if (loss == nullptr || (T > 0 && (row_loss == nullptr || logp == nullptr || stats == nullptr)))
     return MOE_ERR_INVALID_ARG;
-  if (any_same({loss, row_loss, logp, stats, dlogits}, {weight, grad_loss, tokens, old_logp, advantage, ref_logp}) ||
-      any_same({loss, row_loss, logp, stats}, {logits, dlogits}))
+  const Mem x = of_type(logits, T * V, logits_dtype), dx = of_type(dlogits, T * V, dlogits_dtype);
+  if (any_shared({floats(loss, 1), floats(row_loss, T), floats(logp, T), floats(stats, 2 * T), dx},
+                 {dlogits == logits ? Mem{} : x, floats(weight, T), floats(grad_loss, 1), floats(tokens, T),
+                  floats(old_logp, T), floats(advantage, T), floats(ref_logp, T)}))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_policy_loss(T, static_cast<int>(V), logits, logits_dtype, tokens, old_logp, advantage,
                                        params->kl > 0.0 ? ref_logp : nullptr, params->clip_low, params->clip_high,
@@ -823,7 +850,9 @@ int moe_policy_loss_backward(int64_t T, int64_t V, const void* logits, int logit
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if (stats == nullptr || dlogits == nullptr ||
-      any_same({dlogits}, {logits, stats, tokens, old_logp, advantage, ref_logp, weight, grad_loss}))
+      any_shared({of_type(dlogits, T * V, dlogits_dtype)},
+                 {of_type(logits, T * V, logits_dtype), floats(stats, 2 * T), floats(tokens, T), floats(old_logp, T),
+                  floats(advantage, T), floats(ref_logp, T), floats(weight, T), floats(grad_loss, 1)}))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_policy_loss_bwd(T, static_cast<int>(V), logits, logits_dtype, stats, tokens, old_logp,
                                            advantage, params->kl > 0.0 ? ref_logp : nullptr, params->clip_low,
@@ -837,7 +866,8 @@ int moe_token_logp(int64_t T, int64_t V, const void* logits, int logits_dtype, c
   if (st != MOE_OK) return st;
   if (!is_temperature(temperature)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (tokens == nullptr || logp == nullptr || stats == nullptr || any_same({logp, stats}, {logits, tokens}))
+  if (tokens == nullptr || logp == nullptr || stats == nullptr ||
+      any_shared({floats(logp, T), floats(stats, 2 * T)}, {of_type(logits, T * V, logits_dtype), floats(tokens, T)}))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_policy_loss(T, static_cast<int>(V), logits, logits_dtype, tokens, nullptr, nullptr, nullptr,
                                        0.0, 0.0, 0.0, temperature, nullptr, nullptr, nullptr, nullptr, logp, stats,
