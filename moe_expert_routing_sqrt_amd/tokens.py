@@ -39,6 +39,8 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: O
               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """Rows of table [V, d] by token id, times scale: [*ids.shape, d] in out_dtype
     (None: the table's).  Ids (int32) outside [0, V) give zeros."""
+    if out is not None and out_dtype is not None and out.dtype is not out_dtype:
+        raise TypeError("out must be of out_dtype")
     V, d = table.shape
     T = ids.numel()
     i_p, t_p, o_p = _arg(ids, T, "ids", _i32), _arg(table, None, "table"), _arg(out, T * d, "out")
@@ -56,11 +58,14 @@ def _embedding_ws_bytes(T: int, V: int, d: int) -> int:
 
 
 def embedding_backward(d_out: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float = 1.0,
-                       d_table: Optional[torch.Tensor] = None, dtype: torch.dtype = _f32, accumulate: bool = False,
-                       ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+                       d_table: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                       accumulate: bool = False, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The table's gradient [n_rows, d] for embedding's d_out [*ids.shape, d].
     accumulate: added to what d_table holds (a tied head's gradient, earlier
-    micro-batches), else every row is written, in d_table or a new tensor of dtype."""
+    micro-batches), else every row is written, in d_table or a new tensor of dtype
+    (None: fp32)."""
+    if d_table is not None and dtype is not None and d_table.dtype is not dtype:
+        raise TypeError("d_table must be of dtype")
     if accumulate and d_table is None:
         raise ValueError("accumulate needs d_table")
     d = d_out.shape[-1]
@@ -68,7 +73,7 @@ def embedding_backward(d_out: torch.Tensor, ids: torch.Tensor, n_rows: int, scal
     i_p, y_p = _arg(ids, T, "ids", _i32), _arg(d_out, T * d, "d_out")
     t_p = _arg(d_table, n_rows * d, "d_table")
     if d_table is None:
-        d_table = d_out.new_empty((n_rows, d), dtype=dtype)
+        d_table = d_out.new_empty((n_rows, d), dtype=_f32 if dtype is None else dtype)
         t_p = d_table.data_ptr()
     if ws is None:
         ws = torch.empty(_embedding_ws_bytes(T, n_rows, d), dtype=torch.uint8, device=d_out.device)
