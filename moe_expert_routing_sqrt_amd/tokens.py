@@ -260,8 +260,9 @@ class TokenModel:
     (dlogits=logits writes it over them); backward(dlogits) leaves every weight's
     gradient; step() is the AdamW step on all of them, the block's included.
 
-    What forward and backward leave or return are buffers of the model (and of the
-    block) that the next call writes again.  The products with the table are plain
+    forward keeps copies of ids and pos for backward; seq_offsets and token_mask must
+    stay as they are until then.  What forward and backward leave or return are buffers
+    of the model (and of the block) that the next call writes again.  The products with the table are plain
     library ones."""
 
     def __init__(self, block: MoEBlock, table: torch.Tensor, positions: torch.Tensor, norm_w: torch.Tensor,
@@ -275,6 +276,7 @@ class TokenModel:
         new = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device=table.device)  # noqa: E731
         self.stream, self.delta, self.sum, self.y, self.dy, self.dx = (new(T, d) for _ in range(6))
         self.logits = new(T, V)
+        self.ids, self.pos = new(T, dt=_i32), new(T, dt=_i32)
         self.mean, self.rstd = new(T, dt=_f32), new(T, dt=_f32)
         self.d_table, self.d_positions = new(V, d), new(P, d, dt=_f32)
         self.d_norm_w, self.d_norm_b = new(d, dt=_f32), new(d, dt=_f32)
@@ -286,12 +288,11 @@ class TokenModel:
     def forward(self, ids: torch.Tensor, pos: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
                 token_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
         T = self.block.layer.T
-        for name, t in (("ids", ids), ("pos", pos)):
-            if t.numel() != T:
-                raise ValueError(f"{name}: needs {T} elements, has {t.numel()}")
-        self.ids, self.pos = ids, pos
-        embedding(ids, self.table, self.scale, out=self.stream)
-        embedding(pos, self.positions, out=self.delta)
+        for name, t, kept in (("ids", ids, self.ids), ("pos", pos, self.pos)):
+            _arg(t, T, name, _i32)
+            kept.copy_(t.view(T))
+        embedding(self.ids, self.table, self.scale, out=self.stream)
+        embedding(self.pos, self.positions, out=self.delta)
         out, stream = self.block.forward(self.delta, self.stream, seq_offsets, token_mask)
         layer_norm(out, self.norm_w, self.norm_b, residual=stream, eps=self.eps, y=self.y, sum_out=self.sum,
                    mean=self.mean, rstd=self.rstd)
