@@ -266,7 +266,7 @@ class TokenModel:
     library ones."""
 
     def __init__(self, block: MoEBlock, table: torch.Tensor, positions: torch.Tensor, norm_w: torch.Tensor,
-                 norm_b: torch.Tensor, scale: Optional[float] = None, eps: float = 1e-5):
+                 norm_b: torch.Tensor, scale: Optional[float] = None, eps: float = 1e-5, master="block"):
         la = block.layer
         T, d, V, P = la.T, la.d, table.shape[0], positions.shape[0]
         if table.shape[1] != d or positions.shape[1] != d:
@@ -284,6 +284,9 @@ class TokenModel:
         self.table_ws = new(_embedding_ws_bytes(T, V, d), dt=torch.uint8)
         self.positions_ws = new(_embedding_ws_bytes(T, P, d), dt=torch.uint8)
         self.opt = None
+        if isinstance(master, str) and master == "block":  # its list holds the block's weights only
+            master = block.master if block.master is None or isinstance(block.master, str) else "new"
+        self.master = master
 
     def forward(self, ids: torch.Tensor, pos: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
                 token_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -319,7 +322,6 @@ class TokenModel:
             args = dict(self.block.opt_args)
             args["weight_decay"] = [args["weight_decay"], 0.0, 0.0, 0.0]
             self.opt = AdamW([self.table, self.positions, self.norm_w, self.norm_b],
-                             [self.d_table, self.d_positions, self.d_norm_w, self.d_norm_b], master=self.block.master,
-                             **args)
+                             [self.d_table, self.d_positions, self.d_norm_w, self.d_norm_b], master=self.master, **args)
         self.opt.step(grad_scale)
         self.block.step(grad_scale)

@@ -1,5 +1,5 @@
 """TokenModel keeps what it needs of a batch: a loader may refill its buffers between
-forward and backward."""
+forward and backward.  Its optimizer's masters are its own."""
 import pytest
 import torch
 
@@ -28,3 +28,21 @@ def test_refilled_ids():
     want = _run(m, ids, pos, batch)
     got = _run(m, ids.clone(), pos.clone(), batch, refill=True)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_a_block_with_masters_of_its_own():
+    dev = need_gpu()
+    m, ids, pos, g = _model(dev)
+    blk = m.block
+    blk.master = [None, None] + [w.float() if w.dtype is torch.bfloat16 else None
+                                 for w in (blk.layer.w_gate, blk.layer.w13, blk.layer.w2, blk.layer.sh_w13,
+                                           blk.layer.sh_w2)]
+    _run(m, ids, pos, _batch(g, dev, ids))
+    before = m.table.clone()
+    m.step()
+    assert not torch.equal(before, m.table) and torch.equal(m.table, m.opt.master[0].to(torch.bfloat16))
+    kept = [m.table.float() * 1.001, None, None, None]
+    m2 = M.TokenModel(blk, m.table, m.positions, m.norm_w, m.norm_b, scale=7.0, master=kept)
+    _run(m2, ids, pos, _batch(g, dev, ids))
+    m2.step()
+    assert m2.opt.master[0] is kept[0] and torch.equal(m2.table, kept[0].to(torch.bfloat16))
