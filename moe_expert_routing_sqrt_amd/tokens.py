@@ -254,7 +254,7 @@ class TokenModel:
         out, stream = block(delta, stream),  y = norm(out + stream)
         logits = y table^T
 
-    The table is tied: its gradient is the head's, onto which the lookup's is
+    The table is tied: its gradient (fp32) is the head's, onto which the lookup's is
     accumulated.  table [V, d] and positions [P, d] are bf16; scale None: sqrt(d).
     forward(ids, pos) returns logits [T, V] (bf16); a loss leaves their gradient
     (dlogits=logits writes it over them); backward(dlogits) leaves every weight's
@@ -278,7 +278,7 @@ class TokenModel:
         self.logits = new(T, V)
         self.ids, self.pos = new(T, dt=_i32), new(T, dt=_i32)
         self.mean, self.rstd = new(T, dt=_f32), new(T, dt=_f32)
-        self.d_table, self.d_positions = new(V, d), new(P, d, dt=_f32)
+        self.d_table, self.d_positions = new(V, d, dt=_f32), new(P, d, dt=_f32)
         self.d_norm_w, self.d_norm_b = new(d, dt=_f32), new(d, dt=_f32)
         self.norm_ws = new(max(256, workspace_bytes(MOE_OP_LAYER_NORM_BACKWARD, la.sh)), dt=torch.uint8)
         self.table_ws = new(_embedding_ws_bytes(T, V, d), dt=torch.uint8)
@@ -306,7 +306,7 @@ class TokenModel:
         MoEBlock.backward's."""
         if dlogits.shape != self.logits.shape or dlogits.dtype != torch.bfloat16:
             raise ValueError(f"dlogits: needs bf16 {tuple(self.logits.shape)}")
-        torch.mm(dlogits.t(), self.y, out=self.d_table)
+        torch.mm(dlogits.t(), self.y, out_dtype=_f32, out=self.d_table)
         torch.mm(dlogits, self.table, out=self.dy)
         layer_norm_backward(self.dy, self.sum, self.norm_w, self.mean, self.rstd, dx=self.dx, dw=self.d_norm_w,
                             db=self.d_norm_b, ws=self.norm_ws)
