@@ -699,8 +699,10 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
  *             both.
  * A counted row with a NaN, a +inf or no finite logit gives NaN.  The sums run in
  * a fixed order (deterministic), the softmax's in fp32, a row's loss and the sum
- * over rows in fp64; a row's results do not depend on the other rows.  T = 0:
- * loss = 0.
+ * over rows in fp64; a row's results do not depend on the other rows.  A row_loss
+ * carries the relative errors of its two sums as an absolute one, about 1e-7
+ * temperature^2: where student and teacher agree more closely than that, it is no
+ * more than its error and may be below 0.  T = 0: loss = 0.
  */
 int moe_distill_loss(int64_t T, int64_t V, int32_t K, const void* logits, int logits_dtype, const int32_t* topk_idx,
                      const void* teacher, int teacher_dtype, double temperature, const float* weight,
