@@ -9,8 +9,8 @@
 // student logits there, one lane each, read while the row's sums are formed, and
 // for the gradient a list for each thread that stores some of them, so that a
 // piece is corrected before it is stored instead of read and written again.
-// 4096 x 131072 bf16 with 64 entries and gradient 398 us (5.4 TB/s), the policy
-// loss, which has one entry, 383; forward alone 175 and 171.  64 x 32000: 12 us.
+// 4096 x 131072 bf16 with 64 entries and gradient 405 us (5.3 TB/s), the policy
+// loss, which has one entry, 391; forward alone 175 and 172.  64 x 32000: 13 us.
 #include "vocab_loss.h"
 
 namespace moe {

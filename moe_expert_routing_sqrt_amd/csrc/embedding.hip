@@ -9,8 +9,10 @@
 // Measured: lookup of 16384 x 7168 bf16 out of 131072 rows 68 us (235 MB written,
 // the rows read again where they repeat); its gradient, written whole in fp32 (3.8
 // GB), 750 us, of which clearing takes 640 (5.5 TB/s, what a plain fill of that
-// size reaches); 16384 x 2048 accumulated into fp32 rows 47 us
-// (10 of them the sort).
+// size reaches); 16384 x 2048 accumulated into fp32 rows 52 us in its three launches
+// (sort 10, sums 37, join 5), 55 a call, 46 where the batch before was the same one.
+// What is left of narrow rows is the sort and the sums' chains of loads: 16384 x 64
+// accumulated 28 us.
 #include <algorithm>
 
 #include "launch.h"
@@ -274,7 +276,7 @@ struct GradArgs {
 
 __device__ __forceinline__ int lane_of(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
 
-constexpr int kRowsAhead = 16;  // rows in flight (8: 16384 x 2048 accumulated 48 us, 46 so)
+constexpr int kRowsAhead = 16;  // rows in flight (8: 16384 x 2048 accumulated, the same batch again, 48 us, 46 so)
 
 // scale * acc (+ old) to the row
 template <typename TO, int E, bool ADD>

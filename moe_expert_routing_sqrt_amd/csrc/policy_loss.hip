@@ -6,9 +6,9 @@
 // A row with weight 0 or a token outside the vocabulary adds nothing.
 //
 // The token's logit and the row's few numbers are scalar loads, the loss is formed
-// by one lane.  8192 x 65536 bf16 with gradient, a tenth of the rows masked: 377 us
-// (5.4 TB/s); 32 x 65536 forward 8 us; the gradient alone, 2048 x 100003 fp32 to
-// bf16, 190 us (6.0 TB/s).  The log-probabilities alone take the same walk.
+// by one lane.  8192 x 65536 bf16 with gradient, a tenth of the rows masked: 379 us
+// (5.4 TB/s); 32 x 65536 forward 9 us; the gradient alone, 2048 x 100003 fp32 to
+// bf16, 192 us (6.0 TB/s).  The log-probabilities alone take the same walk.
 #include "vocab_loss.h"
 
 namespace moe {

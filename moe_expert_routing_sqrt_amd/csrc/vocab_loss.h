@@ -209,11 +209,13 @@ constexpr int kGroup = NT < kBlock ? kBlock : NT;
 // loaded into each register as this row's last use of it is over, so that memory
 // is busy while a row is reduced; nothing between that and the next row's first
 // use waits for a vector load (the loads of a row drained before its sums: 483 us
-// where this takes 415 at 4096 x 131072, bf16 with gradient).
+// where this took 415 when it came, at 4096 x 131072, bf16 with gradient; 406 of
+// that build without its exponentials).
 //
-// Bound by memory: that case moves 2.1 GB in 398 us (5.4 TB/s; 406 without the
-// exponentials), 8192 x 65536 2.0 GB in 378.  Work-groups that each stream a row of
-// their own stay below the 6.2 TB/s of an elementwise pass in address order.
+// Bound by memory: that case now moves 2.1 GB in 405 us (5.3 TB/s), 8192 x 65536 2.0
+// GB in 379.  Work-groups that each stream a row of their own stay below the 6.2 TB/s
+// of an elementwise pass in address order.  No vector registers spill; scalar ones do,
+// up to 82 of them into lanes.
 template <typename KIND, typename TX, typename TD, int NT, int NC, bool MORE, bool GRAD>
 __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logits p, const typename KIND::Args k) {
   constexpr int E = kPiece<TX>, WAVES = NT / kWave;
@@ -416,7 +418,7 @@ __global__ __launch_bounds__(kGroup<NT>, kWaves<NC>) void loss_kernel(const Logi
 // The gradient from the logits and the forward's statistics: a work-group has
 // `span` pieces of a row, a multiple of NT (NT = 64: a wave has them).  The row's few
 // entries are looked up while its pieces are on their way.  Runs at the rate of an
-// elementwise pass: 2048 x 100003 fp32 to bf16 (1.2 GB) 189 us, 6.1 TB/s.
+// elementwise pass: 2048 x 100003 fp32 to bf16 (1.2 GB) 192 us, 6.0 TB/s.
 template <int NT>
 constexpr int kGradAhead = NT > kWave ? 2 : 4;
 template <typename KIND, typename TX, typename TD, int NT>
@@ -506,8 +508,9 @@ template <typename KIND, typename TX, typename TD, bool GRAD>
 hipError_t loss_rows(const Logits& p, const typename KIND::Args& k, hipStream_t s) {
   const int pieces = p.V / kPiece<TX>;
   // The fewest registers that hold a row, of the fewest waves.  The width alone
-  // decides, so that a row's results do not depend on the rows beside it (few rows
-  // would be quicker with more waves: 64 x 32000 bf16 with gradient takes 12 us).
+  // decides, so that a row's results do not depend on the rows beside it.  (Few rows
+  // would be quicker cut over several work-groups, in an order of sums that V alone
+  // fixes too; that is not built: 64 x 32000 bf16 with gradient takes 13 us.)
   if (pieces == 0) return run_loss<KIND, TX, TD, 64, 0, false, GRAD>(p, k, s);
   if (pieces <= 2 * 64) return run_loss<KIND, TX, TD, 64, 2, false, GRAD>(p, k, s);
   if (pieces <= 4 * 64) return run_loss<KIND, TX, TD, 64, 4, false, GRAD>(p, k, s);
