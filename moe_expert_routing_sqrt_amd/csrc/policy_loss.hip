@@ -24,7 +24,8 @@ struct Policy {
     const float* adv;  // nullptr: log-probabilities only
     const float* ref;  // nullptr: no KL term
     float* logp;
-    float least, most, kl;  // the ratio's bounds, the KL term's weight
+    float least, most;  // the ratio's bounds
+    double kl;          // the KL term's weight
   };
   template <int NT>
   struct Shared {
@@ -61,8 +62,9 @@ struct Policy {
 
   // The differences of log-probabilities in fp64 (their absolute error is the
   // ratio's relative one).  Near 0 the exponentials are formed in fp32 with the
-  // exponent's rounding error carried; elsewhere the row's few numbers are fp64, which
-  // holds a ratio whose product with a small advantage or weight fp32 holds.  (fp64
+  // exponent's rounding error carried; elsewhere, and beside a huge advantage or KL
+  // weight, the row's few numbers are fp64, which holds products that fp32 holds only
+  // after the row's weight.  (fp64
   // in every row: 65536 x 256 forward 41 us, 39 so.)
   template <typename S>
   static __device__ __forceinline__ void finish(const Logits& p, const Args& k, int64_t row, float gw, float m,
@@ -79,15 +81,16 @@ struct Policy {
     const double move = logp - static_cast<double>(vocab::scalar_of(k.old_logp + row));
     const double d = k.ref != nullptr ? static_cast<double>(vocab::scalar_of(k.ref + row)) - logp : 0.0;
     float l, slope;
-    if (fabs(move) < kNear && fabs(d) < kNear) {
+    if (fabs(move) < kNear && fabs(d) < kNear && fabsf(a) < kSmall && k.kl < kSmall) {
       const float r = exp_of(static_cast<float>(move));
       const float free = r * a, cut = fminf(fmaxf(r, k.least), k.most) * a;
       l = free > cut ? -cut : -free;
       slope = free > cut ? 0.0f : -free;
       if (k.ref != nullptr) {
         const float df = static_cast<float>(d), g = gap_of(df);
-        l += k.kl * g;
-        slope -= k.kl * (fabsf(df) < 0.5f ? df + g : exp_of(df) - 1.0f);
+        const float kl = static_cast<float>(k.kl);
+        l += kl * g;
+        slope -= kl * (fabsf(df) < 0.5f ? df + g : exp_of(df) - 1.0f);
       }
       sh.k = within(-slope * p.inv_tau_f * gw);
     } else {
@@ -108,7 +111,8 @@ struct Policy {
     }
     if (outputs) p.row_loss[row] = l;
   }
-  static constexpr double kNear = 40.0;
+  static constexpr double kNear = 40.0;  // e^40 1e20 is an fp32 number
+  static constexpr float kSmall = 1e20f;
   // held to fp32's range, so that entries of probability 0 keep a gradient of 0 (NaN stays)
   template <typename F>
   static __device__ __forceinline__ float within(F v) {
@@ -186,7 +190,7 @@ hipError_t launch_policy_loss(int64_t rows, int V, const void* x, int x_dtype, c
     p.stats = stats;
     p.row_loss = row_loss;
     const Policy::Args k{tok, old_logp, adv, ref, logp, static_cast<float>(1.0 - lo),
-                         static_cast<float>(1.0 + hi), static_cast<float>(kl)};
+                         static_cast<float>(1.0 + hi), kl};
     const hipError_t e = vocab::loss_dtypes<Policy>(p, k, x_dtype, dx_dtype, s);
     if (e != hipSuccess || loss == nullptr) return e;
   }
@@ -204,7 +208,7 @@ hipError_t launch_policy_loss_bwd(int64_t rows, int V, const void* x, int x_dtyp
   p.dx = dx;
   p.stats = const_cast<float*>(stats);  // read only
   const Policy::Args k{tok, old_logp, adv, ref, nullptr, static_cast<float>(1.0 - lo),
-                       static_cast<float>(1.0 + hi), static_cast<float>(kl)};
+                       static_cast<float>(1.0 + hi), kl};
   return vocab::grad_dtypes<Policy>(p, k, x_dtype, dx_dtype, s);
 }
 

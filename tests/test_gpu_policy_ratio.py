@@ -155,3 +155,38 @@ def test_a_gradient_factor_of_zero_and_a_nan():
     assert torch.isposinf(got[1][0]) and not got[4][0].any()
     got = M.policy_loss(x, tok, old, adv, with_grad=True)
     assert torch.isnan(got[1][1:]).all() and torch.isnan(got[4][1:]).all() and torch.isfinite(got[4][0]).all()
+
+
+def test_large_advantages_and_kl_weights():
+    """Products that fp32 does not hold before the row's weight: 1e38 times a ratio of
+    e^39 at a weight of 1e-30, and a KL weight beyond fp32."""
+    dev = need_gpu()
+    x, tok, logp, q, zz, S = _rows(300, 4, "f32", dev)
+    at = torch.from_numpy(logp.astype(np.float32)).to(dev)
+    adv = torch.tensor([-1e38, 1e38, -1e25, 0.0], device=dev)
+    old = at - 39
+    w = torch.full((4,), 1e-30, device=dev)
+    hot = np.arange(300) == host(tok)[:, None]
+
+    def rel_of(rel):
+        r = rel[:, None] + S[:, None] + U * (3 * zz + 14)
+        return np.where(hot, rel[:, None] + r * q / np.maximum(1 - q, 1e-12), r)
+
+    wide = float(np.float32(1e-30))
+    got = M.policy_loss(x, tok, old, adv, clip=CLIP, weight=w, with_grad=True)
+    a, r = host(adv).astype(np.float64), np.exp(logp - host(old).astype(np.float64))
+    slope = np.where(a < 0, -r * a, 0.0)
+    dx = _grad(slope, wide, q, host(tok))
+    row = np.where(a < 0, -r * a, -(1 + CLIP[1]) * a)
+    _check(got, row, np.abs(row) * (S + 12 * U), dx, rel_of(S + 12 * U), "f32")
+    none = M.policy_loss(x, tok, old, adv, clip=CLIP, weight=w, with_grad=True, grad_loss=torch.zeros(1, device=dev))
+    assert not none[4].any()
+    ref, kl = at + 1, 1e39
+    d = host(ref).astype(np.float64) - logp
+    got = M.policy_loss(x, tok, at, adv * 0, ref_logp=ref, kl=kl, weight=w, with_grad=True)
+    dx = _grad(-kl * np.expm1(d), wide, q, host(tok))
+    rel = (np.exp(d) * (S + 4 * U) + 8 * U * (np.exp(d) + 1)) / np.expm1(d)
+    _check(got, kl * (np.expm1(d) - d), np.zeros(4), dx, rel_of(rel), "f32")
+    none = M.policy_loss(x, tok, at, adv * 0, ref_logp=ref, kl=kl, weight=w, with_grad=True,
+                         grad_loss=torch.zeros(1, device=dev))
+    assert not none[4].any()
