@@ -683,7 +683,7 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
  *     row_loss[t] = temperature^2 sum_j p_j (log p_j - log q[topk_idx_j])
  *     loss = sum_t weight[t] row_loss[t]
  *     dlogits[t,v] = grad_loss weight[t] temperature (q[v] - sum_{j: topk_idx_j = v} p_j)
- *   logits    [T, V] in logits_dtype (MOE_BF16 or MOE_F32)
+ *   logits    [T, V] in logits_dtype (MOE_BF16 or MOE_F32);  0 < temperature <= 1e36
  *   topk_idx  [T, K] int32, teacher [T, K] in teacher_dtype: an index outside
  *             [0, V) or a teacher logit of -inf is no entry; an index may repeat.
  *             1 <= K <= MOE_MAX_TEACHER_TOP
@@ -728,7 +728,7 @@ int moe_distill_loss_backward(int64_t T, int64_t V, int32_t K, const void* logit
  *     dl/dlogp = -r A (0 where the clamped term is the smaller) + kl (1 - exp(d))
  *   logits    [T, V] in logits_dtype;  tokens [T] int32
  *   old_logp, advantage [T] fp32;  ref_logp [T] fp32, or NULL with kl = 0
- *   params    host: temperature > 0, clip_low, clip_high, kl >= 0, all finite
+ *   params    host: 0 < temperature <= 1e36; clip_low, clip_high, kl >= 0 and finite
  *   weight    [T] fp32, or NULL: 1/T each.  A row of weight 0, or with a token
  *             outside [0, V), does not count: its loss, logp, statistics and
  *             gradient are 0, and it may hold anything

@@ -749,9 +749,10 @@ int moe_embedding_backward(int64_t T, int64_t V, int32_t d, const int32_t* token
                                          d_table_dtype, accumulate != 0, ws, as_stream(stream)));
 }
 
-// a softmax temperature whose log2(e)/temperature fp32 holds
+// A softmax temperature whose log2(e)/temperature fp32 holds, and at which a
+// difference of logits that fp32 does not hold is a probability of 0.
 static bool is_temperature(double t) {
-  return std::isfinite(t) && t > 0.0 && std::isnormal(static_cast<float>(1.4426950408889634 / t)) &&
+  return t > 0.0 && t <= 1e36 && std::isnormal(static_cast<float>(1.4426950408889634 / t)) &&
          std::isnormal(static_cast<float>(t));
 }
 
