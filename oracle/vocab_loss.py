@@ -83,6 +83,8 @@ def policy(x, tok, old, adv, ref=None, clip=(0.2, 0.2), kl=0.0, tau=1.0, weight=
         logp = logq[tok[r]]
         ratio, a = np.exp(logp - float(old[r])), float(adv[r])
         free, cut = ratio * a, min(max(ratio, 1 - clip[0]), 1 + clip[1]) * a
+        if a == 0 and ratio == np.inf:  # an advantage of 0 counts 0 beside any ratio
+            free = 0.0
         row[r] = -min(free, cut)
         slope = -free if free <= cut else 0.0
         if kl:
