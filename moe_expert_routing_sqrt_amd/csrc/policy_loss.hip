@@ -64,8 +64,7 @@ struct Policy {
   // ratio's relative one).  Near 0 the exponentials are formed in fp32 with the
   // exponent's rounding error carried; elsewhere, and beside a huge advantage or KL
   // weight, the row's few numbers are fp64, which holds products that fp32 holds only
-  // after the row's weight.  (fp64
-  // in every row: 65536 x 256 forward 41 us, 39 so.)
+  // after the row's weight.  (fp64 in every row: 65536 x 256 forward 41 us, 39 so.)
   template <typename S>
   static __device__ __forceinline__ void finish(const Logits& p, const Args& k, int64_t row, float gw, float m,
                                                 float sum, int lane, S& sh, bool outputs) {
@@ -118,7 +117,7 @@ struct Policy {
   static __device__ __forceinline__ float within(F v) {
     return v > FLT_MAX ? FLT_MAX : v < -FLT_MAX ? -FLT_MAX : static_cast<float>(v);
   }
-  // |v| up to kNear and somewhat above
+  // |v| up to kNear
   static __device__ __forceinline__ float exp_of(float v) {
     const float t = v * 1.44269504f, lo = __builtin_fmaf(v, 1.44269504f, -t) + v * 1.92596299e-8f;
     const float e = exp2_of(t);
